@@ -12,6 +12,9 @@ from ._binding import (EP_DEVERR_RECV_OVERFLOW, EP_DEVERR_SLOT_RANGE, EP_DEVERR_
                        EP_LAYOUT_SCRATCH_BYTES,
                        EP_MAX_EXPERTS,
                        EP_MAX_RANKS, EP_OK, LIB_PATH, EPError, ep_combine, ep_combine_recv,
+                       ep_combine_unpermute, ep_combine_unpermute_grad,
+                       ep_dispatch_permute_fp8, ep_dispatch_permute_grad, ep_rmsnorm,
+                       ep_rmsnorm_grad, ep_rmsnorm_grad_workspace_bytes,
                        ep_combine_send, ep_dispatch, ep_dispatch_fp8, ep_dispatch_permute,
                        ep_dispatch_layout, ep_dispatch_permute_layout, ep_dispatch_preprocess, ep_dispatch_recv,
                        ep_layout_dispatch,
@@ -23,6 +26,9 @@ from ._binding import (EP_DEVERR_RECV_OVERFLOW, EP_DEVERR_SLOT_RANGE, EP_DEVERR_
 from .buffers import DispatchBuffers, LayoutBuffers, StageBuffers
 
 __all__ = [
+    "ep_rmsnorm", "ep_rmsnorm_grad", "ep_rmsnorm_grad_workspace_bytes",
+    "ep_dispatch_permute_fp8", "ep_dispatch_permute_grad", "ep_combine_unpermute",
+    "ep_combine_unpermute_grad",
     "ep_get_layout", "ep_get_layout_no_alloc", "ep_dispatch_preprocess", "ep_layout_counts",
     "ep_layout_counts_workspace_bytes", "ep_dispatch_layout", "ep_dispatch_permute_layout",
     "ep_layout_dispatch",

@@ -73,6 +73,15 @@ def load() -> ctypes.CDLL:
                                    P, i64, P, P]
     L.ep_combine_send.argtypes = [P, i64, P, i64, i32, i32, i32, P, i64, P, P, i32, P]
     L.ep_combine_recv.argtypes = [P, i32, i64, P, i64, i32, P, P, P]
+    f32 = ctypes.c_float
+    L.ep_rmsnorm.argtypes = [P, P, P, i32, f32, i64, i32, P, P, P, P, P]
+    L.ep_rmsnorm_grad_workspace_bytes.argtypes = [i64, i32]
+    L.ep_rmsnorm_grad_workspace_bytes.restype = sz
+    L.ep_rmsnorm_grad.argtypes = [P, P, P, P, i32, f32, i64, i32, P, P, P, sz, P]
+    L.ep_dispatch_permute_fp8.argtypes = [P, P, P, i64, i32, i32, P, P, P, P, P, i64, P, P]
+    L.ep_combine_unpermute.argtypes = [P, i64, P, i64, i32, i32, P, P, P, P, P]
+    L.ep_combine_unpermute_grad.argtypes = [P, P, i64, P, i64, i32, i32, P, P, P, P, P]
+    L.ep_dispatch_permute_grad.argtypes = [P, P, i64, i64, i32, i32, P, P, P, P, P]
     L.ep_hbm_copy.argtypes = [P, P, sz, P]
     L.ep_hbm_fan.argtypes = [P, P, sz, i32, i32, P]
     L.ep_hbm_spread.argtypes = [P, P, sz, i32, i32, P]
@@ -80,7 +89,9 @@ def load() -> ctypes.CDLL:
               "ep_layout_counts", "ep_dispatch_layout", "ep_dispatch_permute_layout", "ep_dispatch", "ep_dispatch_fp8", "ep_dispatch_permute",
               "ep_restripe_prob", "ep_restripe_prob_sparse", "ep_combine", "ep_dispatch_send",
               "ep_dispatch_recv", "ep_combine_send", "ep_combine_recv", "ep_hbm_copy",
-              "ep_hbm_fan", "ep_hbm_spread"):
+              "ep_hbm_fan", "ep_hbm_spread", "ep_rmsnorm", "ep_rmsnorm_grad",
+              "ep_dispatch_permute_fp8", "ep_combine_unpermute", "ep_combine_unpermute_grad",
+              "ep_dispatch_permute_grad"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -622,6 +633,168 @@ def ep_combine_recv(stage, node_slot, *, out, error_flag=None, stream=None) -> N
         _ptr(stage, torch.bfloat16, "stage"), N, Tmax, _ptr(node_slot, torch.int32, "node_slot"),
         T, H, _ptr(out, torch.bfloat16, "out"), _ptr(error_flag, torch.int32, "error_flag", True),
         _stream(stream)), "ep_combine_recv")
+
+
+def _rows_2d(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _e4m3_bytes(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """e4m3 codes as the bytes the C ABI takes: uint8, or float8_e4m3fn viewed as uint8."""
+    return t.view(torch.uint8) if t is not None and t.dtype == torch.float8_e4m3fn else t
+
+
+def _norm_weight(weight: torch.Tensor, H: int):
+    if weight.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"weight: expected torch.bfloat16 or torch.float32, got {weight.dtype}")
+    _shape(weight, (H,), "weight")
+    return _ptr(weight, weight.dtype, "weight"), int(weight.dtype == torch.float32)
+
+
+def ep_rmsnorm(x, weight, *, residual=None, residual_out=None, y=None, y_fp8=None, y_scales=None,
+               eps: float = 1e-6, stream=None) -> None:
+    """The RMS norm of s = x + residual (fp32): residual_out = bf16(s), y = bf16(norm(s) *
+    weight), and the e4m3 codes (uint8 or float8_e4m3fn [T][H]) with their scales (fp32
+    [T][H/128]). x, residual, residual_out, y: bf16 [T][H]; weight: bf16 or fp32 [H].
+    residual_out may be x or residual, y the other of the two."""
+    T, H = _rows_2d(x, "x")
+    y_fp8 = _e4m3_bytes(y_fp8)
+    _shape(residual, (T, H), "residual")
+    _shape(residual_out, (T, H), "residual_out")
+    _shape(y, (T, H), "y")
+    _shape(y_fp8, (T, H), "y_fp8")
+    _shape(y_scales, (T, H // 128), "y_scales")
+    w, w_fp32 = _norm_weight(weight, H)
+    _check(load().ep_rmsnorm(
+        _ptr(x, torch.bfloat16, "x"), _ptr(residual, torch.bfloat16, "residual", True), w, w_fp32,
+        eps, T, H, _ptr(residual_out, torch.bfloat16, "residual_out", True),
+        _ptr(y, torch.bfloat16, "y", True), _ptr(y_fp8, torch.uint8, "y_fp8", True),
+        _ptr(y_scales, torch.float32, "y_scales", True), _stream(stream)), "ep_rmsnorm")
+
+
+def ep_rmsnorm_grad_workspace_bytes(num_tokens: int, hidden: int) -> int:
+    return int(load().ep_rmsnorm_grad_workspace_bytes(num_tokens, hidden))
+
+
+def ep_rmsnorm_grad(grad_y, h, weight, *, grad_x, grad_residual_out=None, grad_weight=None,
+                    workspace=None, eps: float = 1e-6, stream=None) -> None:
+    """The gradient of ep_rmsnorm's y (and, through grad_residual_out, of its residual_out):
+    grad_x, which is x's and the residual's alike, and grad_weight (fp32 [H], overwritten;
+    needs `workspace`, uint8 of ep_rmsnorm_grad_workspace_bytes). h: the forward's
+    residual_out (its x without a residual). grad_y, grad_residual_out, h, grad_x: bf16
+    [T][H]. grad_x may be grad_y, grad_residual_out or h."""
+    T, H = _rows_2d(h, "h")
+    _shape(grad_y, (T, H), "grad_y")
+    _shape(grad_residual_out, (T, H), "grad_residual_out")
+    _shape(grad_x, (T, H), "grad_x")
+    _shape(grad_weight, (H,), "grad_weight")
+    w, w_fp32 = _norm_weight(weight, H)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(load().ep_rmsnorm_grad(
+        _ptr(grad_y, torch.bfloat16, "grad_y"),
+        _ptr(grad_residual_out, torch.bfloat16, "grad_residual_out", True),
+        _ptr(h, torch.bfloat16, "h"), w, w_fp32, eps, T, H,
+        _ptr(grad_x, torch.bfloat16, "grad_x"),
+        _ptr(grad_weight, torch.float32, "grad_weight", True),
+        _ptr(workspace, torch.uint8, "workspace", True), ws_bytes, _stream(stream)),
+        "ep_rmsnorm_grad")
+
+
+def ep_dispatch_permute_fp8(x_fp8, x_scales, topk_weights, expert_slot, *, perm_x_fp8,
+                            perm_scales, perm_weights=None, perm_src_idx=None, error_flag=None,
+                            stream=None) -> None:
+    """ep_dispatch_permute for e4m3 rows: x_fp8 uint8 or float8_e4m3fn [T][H] with x_scales
+    fp32 [T][H/128] into perm_x_fp8 [cap][H] and perm_scales [cap][H/128]."""
+    T, H = _rows_2d(x_fp8, "x_fp8")
+    _, k = _rows_2d(expert_slot, "expert_slot")
+    cap, _ = _rows_2d(perm_x_fp8, "perm_x_fp8")
+    x_fp8, perm_x_fp8 = _e4m3_bytes(x_fp8), _e4m3_bytes(perm_x_fp8)
+    _shape(x_scales, (T, H // 128), "x_scales")
+    _shape(topk_weights, (T, k), "topk_weights")
+    _shape(expert_slot, (T, k), "expert_slot")
+    _shape(perm_x_fp8, (cap, H), "perm_x_fp8")
+    _shape(perm_scales, (cap, H // 128), "perm_scales")
+    _shape(perm_weights, (cap,), "perm_weights")
+    _shape(perm_src_idx, (cap,), "perm_src_idx")
+    _at_least(error_flag, 1, "error_flag")
+    _check(load().ep_dispatch_permute_fp8(
+        _ptr(x_fp8, torch.uint8, "x_fp8"), _ptr(x_scales, torch.float32, "x_scales"),
+        _ptr(topk_weights, torch.float32, "topk_weights", True), T, H, k,
+        _ptr(expert_slot, torch.int32, "expert_slot"),
+        _ptr(perm_x_fp8, torch.uint8, "perm_x_fp8"),
+        _ptr(perm_scales, torch.float32, "perm_scales"),
+        _ptr(perm_weights, torch.float32, "perm_weights", True),
+        _ptr(perm_src_idx, torch.int32, "perm_src_idx", True), cap,
+        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
+        "ep_dispatch_permute_fp8")
+
+
+def ep_combine_unpermute(expert_out, topk_weights, expert_slot, *, out, addend=None,
+                         error_flag=None, stream=None) -> None:
+    """out[t] = bf16(sum over t's routed pairs of topk_weights * expert_out[row], + addend[t]).
+    expert_out: bf16 [rows][H]; topk_weights: fp32 [T][k] or None (every weight 1);
+    expert_slot: int32 [T][k]; addend, out: bf16 [T][H] (out may be addend)."""
+    rows, H = _rows_2d(expert_out, "expert_out")
+    T, k = _rows_2d(expert_slot, "expert_slot")
+    _shape(topk_weights, (T, k), "topk_weights")
+    _shape(addend, (T, H), "addend")
+    _shape(out, (T, H), "out")
+    _at_least(error_flag, 1, "error_flag")
+    _check(load().ep_combine_unpermute(
+        _ptr(expert_out, torch.bfloat16, "expert_out"), rows,
+        _ptr(topk_weights, torch.float32, "topk_weights", True), T, H, k,
+        _ptr(expert_slot, torch.int32, "expert_slot"),
+        _ptr(addend, torch.bfloat16, "addend", True), _ptr(out, torch.bfloat16, "out"),
+        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
+        "ep_combine_unpermute")
+
+
+def ep_combine_unpermute_grad(grad_out, expert_out, topk_weights, expert_slot, *,
+                              grad_expert_out, grad_topk_weights=None, error_flag=None,
+                              stream=None) -> None:
+    """The gradient of ep_combine_unpermute: grad_expert_out (bf16 [rows][H], rows of no pair
+    left as they were; may be expert_out) and grad_topk_weights (fp32 [T][k]). expert_out may
+    be None when grad_topk_weights is."""
+    T, H = _rows_2d(grad_out, "grad_out")
+    _, k = _rows_2d(expert_slot, "expert_slot")
+    rows, _ = _rows_2d(grad_expert_out, "grad_expert_out")
+    _shape(expert_out, (rows, H), "expert_out")
+    _shape(topk_weights, (T, k), "topk_weights")
+    _shape(expert_slot, (T, k), "expert_slot")
+    _shape(grad_expert_out, (rows, H), "grad_expert_out")
+    _shape(grad_topk_weights, (T, k), "grad_topk_weights")
+    _at_least(error_flag, 1, "error_flag")
+    _check(load().ep_combine_unpermute_grad(
+        _ptr(grad_out, torch.bfloat16, "grad_out"),
+        _ptr(expert_out, torch.bfloat16, "expert_out", grad_topk_weights is None), rows,
+        _ptr(topk_weights, torch.float32, "topk_weights", True), T, H, k,
+        _ptr(expert_slot, torch.int32, "expert_slot"),
+        _ptr(grad_expert_out, torch.bfloat16, "grad_expert_out"),
+        _ptr(grad_topk_weights, torch.float32, "grad_topk_weights", True),
+        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
+        "ep_combine_unpermute_grad")
+
+
+def ep_dispatch_permute_grad(grad_perm_x, expert_slot, *, grad_x, grad_perm_weights=None,
+                             grad_topk_weights=None, error_flag=None, stream=None) -> None:
+    """The gradient of ep_dispatch_permute: grad_x[t] = bf16(sum of t's routed rows of
+    grad_perm_x), grad_topk_weights (fp32 [T][k]) from grad_perm_weights (fp32 [rows])."""
+    rows, H = _rows_2d(grad_perm_x, "grad_perm_x")
+    T, k = _rows_2d(expert_slot, "expert_slot")
+    _shape(grad_perm_weights, (rows,), "grad_perm_weights")
+    _shape(grad_x, (T, H), "grad_x")
+    _shape(grad_topk_weights, (T, k), "grad_topk_weights")
+    _at_least(error_flag, 1, "error_flag")
+    _check(load().ep_dispatch_permute_grad(
+        _ptr(grad_perm_x, torch.bfloat16, "grad_perm_x"),
+        _ptr(grad_perm_weights, torch.float32, "grad_perm_weights", grad_topk_weights is None),
+        rows, T, H, k, _ptr(expert_slot, torch.int32, "expert_slot"),
+        _ptr(grad_x, torch.bfloat16, "grad_x"),
+        _ptr(grad_topk_weights, torch.float32, "grad_topk_weights", True),
+        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
+        "ep_dispatch_permute_grad")
 
 
 def ep_hbm_copy(src, dst, nbytes: Optional[int] = None, stream=None) -> None:

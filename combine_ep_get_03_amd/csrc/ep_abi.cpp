@@ -4,8 +4,10 @@
 #include "ep.h"
 
 #include <limits.h>
+#include <math.h>
 
 #include "ep_internal.hpp"
+#include "expert_ops.hpp"
 
 namespace {
 
@@ -49,6 +51,24 @@ int check_layout_args(const int64_t* topk_idx, int64_t T, int k, int E, int R, i
         !aligned(rank_offset, 4) || !aligned(expert_offset, 4) || !aligned(token_slot, 4) ||
         !aligned(error_flag, 4))
         return EP_ERR_ALIGN;
+    return EP_OK;
+}
+
+// Sizes shared by the calls over expert_slot.
+int check_expert_rows(int64_t T, int H, int k, int64_t rows, int row_multiple) {
+    if (T < 0 || H < 1 || k < 1 || rows < 0) return EP_ERR_ARG;
+    if (T > static_cast<int64_t>(INT32_MAX) / k) return EP_ERR_ARG;
+    if (H % row_multiple != 0) return EP_ERR_ALIGN;
+    if (static_cast<int64_t>(H) / 8 * 64 > INT32_MAX) return EP_ERR_ARG;
+    return EP_OK;
+}
+
+// Sizes shared by the norm and its gradient.
+int check_norm_sizes(int64_t T, int H, float eps) {
+    if (T < 0 || H < 1 || !(eps >= 0.0f) || isinf(eps)) return EP_ERR_ARG;
+    if (H % 8 != 0) return EP_ERR_ALIGN;
+    if (static_cast<int64_t>(H) / 8 * 64 > INT32_MAX) return EP_ERR_ARG;
+    if (T > static_cast<int64_t>(INT32_MAX)) return EP_ERR_ARG;
     return EP_OK;
 }
 
@@ -548,6 +568,131 @@ int ep_combine_recv(const void* stage, int num_nodes, int64_t max_tokens_per_ran
         return EP_ERR_ALIGN;
     return hip_status(ep::launch_combine_recv(stage, N, Tmax, node_slot, T, H, out, error_flag,
                                               static_cast<hipStream_t>(stream)));
+}
+
+int ep_rmsnorm(const void* x, const void* residual, const void* weight, int weight_is_fp32,
+               float eps, int64_t num_tokens, int hidden, void* residual_out, void* y,
+               uint8_t* y_fp8, float* y_scales, void* stream) {
+    const int64_t T = num_tokens;
+    const int H = hidden;
+    const int st = check_norm_sizes(T, H, eps);
+    if (st != EP_OK) return st;
+    if (y_fp8 && H % ep::kNormGroup != 0) return EP_ERR_ALIGN;
+    if (T > 0) {
+        if (!x || !weight || (residual_out && !residual)) return EP_ERR_ARG;
+        if (!residual_out && !y && !y_fp8) return EP_ERR_ARG;
+        if ((y_fp8 == nullptr) != (y_scales == nullptr)) return EP_ERR_ARG;
+        if (residual_out && residual_out == y) return EP_ERR_ARG;
+    }
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+        !aligned(residual_out, 16) || !aligned(y, 16) || !aligned(y_fp8, 8) ||
+        !aligned(y_scales, 4))
+        return EP_ERR_ALIGN;
+    return hip_status(ep::launch_rmsnorm(x, residual, weight, weight_is_fp32 != 0, eps, T, H,
+                                         residual_out, y, y_fp8, y_scales,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_rmsnorm_grad_workspace_bytes(int64_t num_tokens, int hidden) {
+    if (check_norm_sizes(num_tokens, hidden, 0.0f) != EP_OK) return 0;
+    return ep::rmsnorm_grad_workspace_bytes(num_tokens, hidden);
+}
+
+int ep_rmsnorm_grad(const void* grad_y, const void* grad_residual_out, const void* h,
+                    const void* weight, int weight_is_fp32, float eps, int64_t num_tokens,
+                    int hidden, void* grad_x, float* grad_weight, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    const int64_t T = num_tokens;
+    const int H = hidden;
+    const int st = check_norm_sizes(T, H, eps);
+    if (st != EP_OK) return st;
+    if (T > 0 && (!grad_y || !h || !weight || !grad_x)) return EP_ERR_ARG;
+    if (!aligned(grad_y, 16) || !aligned(grad_residual_out, 16) || !aligned(h, 16) ||
+        !aligned(weight, 16) || !aligned(grad_x, 16) || !aligned(grad_weight, 4) ||
+        !aligned(workspace, 16))
+        return EP_ERR_ALIGN;
+    const size_t need = grad_weight ? ep::rmsnorm_grad_workspace_bytes(T, H) : 0;
+    if (workspace_bytes < need || (need > 0 && !workspace)) return EP_ERR_CAPACITY;
+    return hip_status(ep::launch_rmsnorm_grad(grad_y, grad_residual_out, h, weight,
+                                              weight_is_fp32 != 0, eps, T, H, grad_x, grad_weight,
+                                              workspace, static_cast<hipStream_t>(stream)));
+}
+
+int ep_dispatch_permute_fp8(const uint8_t* x_fp8, const float* x_scales,
+                            const float* topk_weights, int64_t num_tokens, int hidden,
+                            int num_topk, const int32_t* expert_slot, uint8_t* perm_x_fp8,
+                            float* perm_scales, float* perm_weights, int32_t* perm_src_idx,
+                            int64_t capacity, int32_t* error_flag, void* stream) {
+    const int64_t T = num_tokens;
+    const int H = hidden, k = num_topk;
+    const int st = check_expert_rows(T, H, k, capacity, ep::kNormGroup);
+    if (st != EP_OK) return st;
+    if (T > 0 && (!x_fp8 || !x_scales || !expert_slot || !perm_x_fp8 || !perm_scales))
+        return EP_ERR_ARG;
+    if (T > 0 && perm_weights && !topk_weights) return EP_ERR_ARG;
+    if (!aligned(x_fp8, 16) || !aligned(x_scales, 4) || !aligned(topk_weights, 4) ||
+        !aligned(expert_slot, 4) || !aligned(perm_x_fp8, 16) || !aligned(perm_scales, 4) ||
+        !aligned(perm_weights, 4) || !aligned(perm_src_idx, 4) || !aligned(error_flag, 4))
+        return EP_ERR_ALIGN;
+    return hip_status(ep::launch_dispatch_permute_fp8(
+        x_fp8, x_scales, topk_weights, T, H, k, expert_slot, perm_x_fp8, perm_scales, perm_weights,
+        perm_src_idx, capacity, error_flag, static_cast<hipStream_t>(stream)));
+}
+
+int ep_combine_unpermute(const void* expert_out, int64_t num_rows, const float* topk_weights,
+                         int64_t num_tokens, int hidden, int num_topk,
+                         const int32_t* expert_slot, const void* addend, void* out,
+                         int32_t* error_flag, void* stream) {
+    const int64_t T = num_tokens;
+    const int H = hidden, k = num_topk;
+    const int st = check_expert_rows(T, H, k, num_rows, 8);
+    if (st != EP_OK) return st;
+    if (T > 0 && (!expert_slot || !out || (num_rows > 0 && !expert_out))) return EP_ERR_ARG;
+    if (!aligned(expert_out, 16) || !aligned(topk_weights, 4) || !aligned(expert_slot, 4) ||
+        !aligned(addend, 16) || !aligned(out, 16) || !aligned(error_flag, 4))
+        return EP_ERR_ALIGN;
+    return hip_status(ep::launch_combine_unpermute(expert_out, num_rows, topk_weights, expert_slot,
+                                                   T, H, k, addend, out, error_flag,
+                                                   static_cast<hipStream_t>(stream)));
+}
+
+int ep_combine_unpermute_grad(const void* grad_out, const void* expert_out, int64_t num_rows,
+                              const float* topk_weights, int64_t num_tokens, int hidden,
+                              int num_topk, const int32_t* expert_slot, void* grad_expert_out,
+                              float* grad_topk_weights, int32_t* error_flag, void* stream) {
+    const int64_t T = num_tokens;
+    const int H = hidden, k = num_topk;
+    const int st = check_expert_rows(T, H, k, num_rows, 8);
+    if (st != EP_OK) return st;
+    if (T > 0 && (!grad_out || !expert_slot)) return EP_ERR_ARG;
+    if (T > 0 && num_rows > 0 && (!grad_expert_out || (grad_topk_weights && !expert_out)))
+        return EP_ERR_ARG;
+    if (!aligned(grad_out, 16) || !aligned(expert_out, 16) || !aligned(topk_weights, 4) ||
+        !aligned(expert_slot, 4) || !aligned(grad_expert_out, 16) ||
+        !aligned(grad_topk_weights, 4) || !aligned(error_flag, 4))
+        return EP_ERR_ALIGN;
+    return hip_status(ep::launch_combine_unpermute_grad(
+        grad_out, expert_out, num_rows, topk_weights, expert_slot, T, H, k, grad_expert_out,
+        grad_topk_weights, error_flag, static_cast<hipStream_t>(stream)));
+}
+
+int ep_dispatch_permute_grad(const void* grad_perm_x, const float* grad_perm_weights,
+                             int64_t num_rows, int64_t num_tokens, int hidden, int num_topk,
+                             const int32_t* expert_slot, void* grad_x, float* grad_topk_weights,
+                             int32_t* error_flag, void* stream) {
+    const int64_t T = num_tokens;
+    const int H = hidden, k = num_topk;
+    const int st = check_expert_rows(T, H, k, num_rows, 8);
+    if (st != EP_OK) return st;
+    if (T > 0 && (!expert_slot || !grad_x)) return EP_ERR_ARG;
+    if (T > 0 && num_rows > 0 && (!grad_perm_x || (grad_topk_weights && !grad_perm_weights)))
+        return EP_ERR_ARG;
+    if (!aligned(grad_perm_x, 16) || !aligned(grad_perm_weights, 4) || !aligned(expert_slot, 4) ||
+        !aligned(grad_x, 16) || !aligned(grad_topk_weights, 4) || !aligned(error_flag, 4))
+        return EP_ERR_ALIGN;
+    return hip_status(ep::launch_dispatch_permute_grad(
+        grad_perm_x, grad_perm_weights, num_rows, expert_slot, T, H, k, grad_x, grad_topk_weights,
+        error_flag, static_cast<hipStream_t>(stream)));
 }
 
 int ep_hbm_copy(const void* src, void* dst, size_t bytes, void* stream) {

@@ -9,7 +9,7 @@ outputs:
 - one call per step: ep_get_layout, ep_dispatch, ep_restripe_prob, ep_combine.
 `step()` takes the one-call layout + dispatch or the counts path where they apply. Also the two-phase ("hook") form of
 dispatch and combine, whose send phase returns a callable that enqueues the receive phase
-later.
+later, and ExpertPath, the expert-major block with the norm in front of it and its gradients.
 
 Device buffers are allocated once per shape (torch, memory plumbing only); the step
 functions enqueue their calls and return without synchronising.
@@ -236,3 +236,116 @@ class Path:
             B.ep_combine_recv(st.stage_x, lb.node_slot, out=self.out, error_flag=self.error_flag,
                               stream=stream)
         return recv_hook
+
+
+class ExpertPath:
+    """The expert-major block on one GPU: buffers and calls for T tokens of H channels over E
+    experts, top-k.
+
+        norm(x, weight, residual)        ep_rmsnorm: residual_out, y (and e4m3 with fp8=True)
+        dispatch(topk_idx, topk_weights) ep_get_layout with expert slots, then
+                                         ep_dispatch_permute, or with fp8=True
+                                         ep_dispatch_permute_fp8, of the norm's output
+        ... the caller's experts on rows expert_offset[e] .. expert_offset[e + 1] - 1 of
+            perm_x (perm_x_fp8 and perm_scales with fp8=True) ...
+        combine(expert_out, topk_weights, addend)   ep_combine_unpermute: out
+
+    and with training=True, in reverse,
+
+        combine_grad(grad_out, expert_out, topk_weights)  grad_expert_out, grad_topk_weights
+        dispatch_grad(grad_perm_x)                        grad_y
+        norm_grad(weight, grad_residual_out)              grad_x, grad_weight
+
+    The gate weights are applied once, by combine(), so their gradient is combine_grad()'s.
+    h is what the norm was taken of as the backward reads it: residual_out, or x without a
+    residual. Rows of perm_x behind the last routed pair are left as they were."""
+
+    def __init__(self, T: int, H: int, E: int, k: int, *, R: int = 1, N: int = 1,
+                 eps: float = 1e-6, fp8: bool = False, training: bool = False, device="cuda"):
+        self.T, self.H, self.E, self.k, self.R, self.N, self.eps = T, H, E, k, R, N, eps
+        self.fp8, self.training = fp8, training
+        bf16 = dict(dtype=torch.bfloat16, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        u8 = dict(dtype=torch.uint8, device=device)
+        cap = T * k
+        self.layout_buf = LayoutBuffers.alloc(T, E, R, N, device, k_expert_slots=k)
+        self.residual_out = torch.empty((T, H), **bf16)
+        self.y = torch.empty((T, H), **bf16)
+        self.out = torch.empty((T, H), **bf16)
+        self.perm_src_idx = torch.empty(cap, dtype=torch.int32, device=device)
+        self.h: Optional[torch.Tensor] = None  # set by norm()
+        if fp8:
+            self.y_fp8 = torch.empty((T, H), **u8)
+            self.y_scales = torch.empty((T, H // 128), **f32)
+            self.perm_x_fp8 = torch.empty((cap, H), **u8)
+            self.perm_scales = torch.empty((cap, H // 128), **f32)
+        else:
+            self.perm_x = torch.empty((cap, H), **bf16)
+        if training:
+            self.grad_expert_out = torch.empty((cap, H), **bf16)
+            self.grad_topk_weights = torch.empty((T, k), **f32)
+            self.grad_y = torch.empty((T, H), **bf16)
+            self.grad_x = torch.empty((T, H), **bf16)
+            self.grad_weight = torch.empty(H, **f32)
+            ws = max(16, B.ep_rmsnorm_grad_workspace_bytes(T, H))
+            self.norm_workspace = torch.empty(ws, **u8)
+
+    @property
+    def error_flag(self) -> torch.Tensor:
+        return self.layout_buf.error_flag
+
+    @property
+    def expert_offset(self) -> torch.Tensor:
+        return self.layout_buf.expert_offset
+
+    def norm(self, x, weight, residual=None, stream=None) -> None:
+        with_sum = residual is not None
+        B.ep_rmsnorm(x, weight, residual=residual,
+                     residual_out=self.residual_out if with_sum else None, y=self.y,
+                     y_fp8=self.y_fp8 if self.fp8 else None,
+                     y_scales=self.y_scales if self.fp8 else None, eps=self.eps, stream=stream)
+        self.h = self.residual_out if with_sum else x
+
+    def dispatch(self, topk_idx, topk_weights=None, stream=None) -> None:
+        """The layout of the batch and the norm's rows in expert-major order."""
+        lb = self.layout_buf
+        lb.compute(topk_idx, self.E, self.R, self.N, stream=stream)
+        if self.fp8:
+            B.ep_dispatch_permute_fp8(self.y_fp8, self.y_scales, topk_weights, lb.expert_slot,
+                                      perm_x_fp8=self.perm_x_fp8, perm_scales=self.perm_scales,
+                                      perm_src_idx=self.perm_src_idx,
+                                      error_flag=self.error_flag, stream=stream)
+        else:
+            B.ep_dispatch_permute(self.y, topk_weights, lb.expert_slot, perm_x=self.perm_x,
+                                  perm_src_idx=self.perm_src_idx, error_flag=self.error_flag,
+                                  stream=stream)
+
+    def combine(self, expert_out, topk_weights, addend=None, stream=None) -> None:
+        B.ep_combine_unpermute(expert_out, topk_weights, self.layout_buf.expert_slot,
+                               out=self.out, addend=addend, error_flag=self.error_flag,
+                               stream=stream)
+
+    def _needs_training(self) -> None:
+        if not self.training:
+            raise ValueError("the gradients need an ExpertPath built with training=True")
+
+    def combine_grad(self, grad_out, expert_out, topk_weights, stream=None) -> None:
+        self._needs_training()
+        B.ep_combine_unpermute_grad(grad_out, expert_out, topk_weights,
+                                    self.layout_buf.expert_slot,
+                                    grad_expert_out=self.grad_expert_out,
+                                    grad_topk_weights=self.grad_topk_weights,
+                                    error_flag=self.error_flag, stream=stream)
+
+    def dispatch_grad(self, grad_perm_x, stream=None) -> None:
+        self._needs_training()
+        B.ep_dispatch_permute_grad(grad_perm_x, self.layout_buf.expert_slot, grad_x=self.grad_y,
+                                   error_flag=self.error_flag, stream=stream)
+
+    def norm_grad(self, weight, grad_residual_out=None, stream=None) -> None:
+        self._needs_training()
+        if self.h is None:
+            raise ValueError("norm_grad needs norm() first")
+        B.ep_rmsnorm_grad(self.grad_y, self.h, weight, grad_x=self.grad_x,
+                          grad_residual_out=grad_residual_out, grad_weight=self.grad_weight,
+                          workspace=self.norm_workspace, eps=self.eps, stream=stream)

@@ -27,6 +27,10 @@
  *   ep_dispatch_send/_recv, ep_combine_send/_recv
  *                            the two-phase ("hook") form of dispatch and combine
  *                            ("[PR #347]", sections 2.1, 2.2.2 and 3.3.2).
+ * and the operators around the expert-major rows, with their gradients: ep_rmsnorm (the
+ * residual's addition, the norm and an e4m3 output), ep_dispatch_permute_fp8 and
+ * ep_combine_unpermute; ep_rmsnorm_grad, ep_dispatch_permute_grad and
+ * ep_combine_unpermute_grad.
  *
  * Conventions for every entry point:
  *  - Every array argument is a DEVICE pointer owned by the caller; the library allocates
@@ -489,6 +493,144 @@ int ep_combine_send(const void *partial, int64_t num_partial_rows, const int32_t
 int ep_combine_recv(const void *stage, int num_nodes, int64_t max_tokens_per_rank,
                     const int32_t *node_slot, int64_t num_tokens, int hidden, void *out,
                     int32_t *error_flag, void *stream);
+
+/* The operators around the expert-major rows: what a mixture-of-experts block runs before
+ * its dispatch (the norm), e4m3 rows sorted by expert, the experts' rows back to their
+ * tokens with the gate weights applied, and the gradients of all of these. The pages
+ * measure the dispatch + permute ("[PR #634] Hybrid ep nixl restripe") and take an e4m3
+ * payload ("[PR #347] Feature/sm free normal kernel", section 3.2.1); the way back from
+ * expert-major rows, the norm and the gradients are this library's own.
+ *
+ * Common to the four calls over expert_slot (int32 [T][k], from ep_get_layout or
+ * ep_dispatch_permute_layout): a negative entry is a pair that is not routed; entries >= 0
+ * of one call must be distinct rows (as ep_get_layout makes them). Any k >= 1 with
+ * T * k <= INT32_MAX.
+ *
+ * ep_rmsnorm -- with s = float(x) + float(residual) (fp32, not rounded; s = x without a
+ * residual) and n = s / sqrt(mean over the row of s^2 + eps):
+ * In:  x         bf16 [T][H]
+ *      residual  bf16 [T][H]                                                   (nullable)
+ *      weight    bf16 [H], or fp32 [H] with weight_is_fp32 != 0
+ *      eps       finite, >= 0 (an all-zero row with eps == 0 is 0 / 0 = NaN)
+ * Out: residual_out bf16 [T][H]  bf16_rne(s); needs residual                   (nullable)
+ *      y            bf16 [T][H]  bf16_rne(n * weight)                          (nullable)
+ *      y_scales     fp32 [T][H/128], y_fp8 uint8 [T][H]  for each group of 128 channels,
+ *                   a = max |n * weight| over the group's numbers: scale = max(a, 2^-100) /
+ *                   448, code = e4m3 (E4M3FN) of n * weight * (448 / max(a, 2^-100)), rounded
+ *                   to nearest even from fp32 (not from y); an all-zero group has scale 1.0
+ *                   and codes 0. A NaN gets the NaN code.           (nullable, both or none)
+ *      At least one output must be asked for.
+ * Sums and the norm are fp32: |s| up to about 1e18 (squares that pass fp32 give n = 0).
+ * residual_out may be x's or residual's memory and y may be the other's (the same start
+ * address); any other overlap of outputs and inputs is undefined.
+ * Sizes: T >= 0; H % 8 == 0, H % 128 == 0 with y_fp8 (else EP_ERR_ALIGN); rows 16-byte
+ *   aligned, y_fp8 8-byte aligned, weight 16-byte aligned, y_scales 4-byte aligned.
+ * Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_HIP. */
+int ep_rmsnorm(const void *x, const void *residual, const void *weight, int weight_is_fp32,
+               float eps, int64_t num_tokens, int hidden, void *residual_out, void *y,
+               uint8_t *y_fp8, float *y_scales, void *stream);
+
+/* Bytes of device workspace ep_rmsnorm_grad needs when grad_weight is asked for. Returns 0
+ * when num_tokens == 0 and for sizes ep_rmsnorm_grad rejects. */
+size_t ep_rmsnorm_grad_workspace_bytes(int64_t num_tokens, int hidden);
+
+/* ep_rmsnorm_grad -- the gradient of y = norm(h) * weight and of the residual's addition,
+ * with r = 1 / sqrt(mean(h^2) + eps), n = h r, g = grad_y * weight (all fp32):
+ * In:  grad_y            bf16 [T][H]  gradient of y
+ *      grad_residual_out bf16 [T][H]  gradient of residual_out, from the rest of the
+ *                                     network                                  (nullable)
+ *      h                 bf16 [T][H]  the forward's residual_out (its x without a residual)
+ *      weight, weight_is_fp32, eps    as in the forward
+ * Out: grad_x      bf16 [T][H]  bf16_rne(r (g - n mean(g n)) + grad_residual_out): the
+ *                               gradient of x and of residual alike
+ *      grad_weight fp32 [H]     overwritten: sum over t of grad_y n, in an order fixed by
+ *                               the sizes (the same inputs give the same bits) (nullable)
+ * The e4m3 output's gradient is taken as y's (the rounding passes it through).
+ * grad_x may be grad_y's, grad_residual_out's or h's memory (the same start address).
+ * Workspace: at least ep_rmsnorm_grad_workspace_bytes(T, H) bytes, 16-byte aligned, contents
+ *   on entry irrelevant, clobbered; NULL is accepted when grad_weight is NULL or T == 0.
+ * T == 0 writes grad_weight as zeros. Sizes and alignment as ep_rmsnorm.
+ * Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_CAPACITY (workspace), EP_ERR_HIP. */
+int ep_rmsnorm_grad(const void *grad_y, const void *grad_residual_out, const void *h,
+                    const void *weight, int weight_is_fp32, float eps, int64_t num_tokens,
+                    int hidden, void *grad_x, float *grad_weight, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* ep_dispatch_permute_fp8 -- ep_dispatch_permute for rows already in e4m3 with one scale
+ * per 128 channels, as ep_rmsnorm writes them.
+ *
+ * In:  x_fp8        uint8 [T][H], x_scales fp32 [T][H/128] (both copied as bits)
+ *      topk_weights fp32 [T][k] (may be NULL when perm_weights is NULL)
+ *      expert_slot  int32 [T][k]
+ * Out: for each t, j with q = expert_slot[t][j] >= 0:
+ *      perm_x_fp8   uint8 [cap][H]      row q = row t of x_fp8
+ *      perm_scales  fp32 [cap][H/128]   row q = row t of x_scales
+ *      perm_weights fp32 [cap]          topk_weights[t][j]                     (nullable)
+ *      perm_src_idx int32 [cap]         t                                      (nullable)
+ *      Other rows are not written. A row >= capacity is skipped and sets
+ *      EP_DEVERR_RECV_OVERFLOW.
+ * Sizes: H % 128 == 0 (else EP_ERR_ALIGN); x_fp8 and perm_x_fp8 16-byte aligned.
+ * Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_HIP. */
+int ep_dispatch_permute_fp8(const uint8_t *x_fp8, const float *x_scales,
+                            const float *topk_weights, int64_t num_tokens, int hidden,
+                            int num_topk, const int32_t *expert_slot, uint8_t *perm_x_fp8,
+                            float *perm_scales, float *perm_weights, int32_t *perm_src_idx,
+                            int64_t capacity, int32_t *error_flag, void *stream);
+
+/* ep_combine_unpermute -- the experts' rows back to their tokens: the weighted counterpart
+ * of ep_combine for expert-major rows.
+ *
+ * In:  expert_out   bf16 [num_rows][H], laid out like ep_dispatch_permute's perm_x
+ *      topk_weights fp32 [T][k]; NULL = every weight 1 (applied in the experts already)
+ *      expert_slot  int32 [T][k]
+ *      addend       bf16 [T][H], say a shared expert's output                  (nullable)
+ * Out: out          bf16 [T][H]; out[t] = bf16_rne( sum over j with q = expert_slot[t][j] >= 0
+ *                   of topk_weights[t][j] * float(expert_out[q]), in fp32, plus
+ *                   float(addend[t]) ); a token with no pair gets addend[t], or +0.0.
+ *      Rows and weights of pairs that are not routed are not read into the sum. A row
+ *      >= num_rows is skipped and sets EP_DEVERR_SLOT_RANGE. out may be addend's memory.
+ * Sizes: H % 8 == 0; expert_out, addend and out 16-byte aligned.
+ * Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_HIP. */
+int ep_combine_unpermute(const void *expert_out, int64_t num_rows, const float *topk_weights,
+                         int64_t num_tokens, int hidden, int num_topk,
+                         const int32_t *expert_slot, const void *addend, void *out,
+                         int32_t *error_flag, void *stream);
+
+/* ep_combine_unpermute_grad -- the gradient of ep_combine_unpermute (the addend's is
+ * grad_out itself).
+ *
+ * In:  grad_out     bf16 [T][H]
+ *      expert_out   bf16 [num_rows][H]; may be NULL when grad_topk_weights is NULL
+ *      topk_weights fp32 [T][k]; NULL = every weight 1
+ *      expert_slot  int32 [T][k]
+ * Out: grad_expert_out   bf16 [num_rows][H]  row q = bf16_rne(topk_weights[t][j] * grad_out[t])
+ *                        for each t, j with q = expert_slot[t][j] >= 0; other rows are not
+ *                        written. May be expert_out's memory.
+ *      grad_topk_weights fp32 [T][k]  <grad_out[t], expert_out[q]> in fp32; +0.0 for a pair
+ *                        that is not routed                                    (nullable)
+ *      A row >= num_rows is skipped (its weight's gradient is +0.0) and sets
+ *      EP_DEVERR_SLOT_RANGE.
+ * Sizes: H % 8 == 0; rows 16-byte aligned. Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_HIP. */
+int ep_combine_unpermute_grad(const void *grad_out, const void *expert_out, int64_t num_rows,
+                              const float *topk_weights, int64_t num_tokens, int hidden,
+                              int num_topk, const int32_t *expert_slot, void *grad_expert_out,
+                              float *grad_topk_weights, int32_t *error_flag, void *stream);
+
+/* ep_dispatch_permute_grad -- the gradient of ep_dispatch_permute.
+ *
+ * In:  grad_perm_x       bf16 [num_rows][H]
+ *      grad_perm_weights fp32 [num_rows]; needed with grad_topk_weights, else may be NULL
+ *      expert_slot       int32 [T][k]
+ * Out: grad_x            bf16 [T][H]  bf16_rne( sum over j with q = expert_slot[t][j] >= 0 of
+ *                        float(grad_perm_x[q]) ), in fp32; +0.0 for a token with no pair
+ *      grad_topk_weights fp32 [T][k]  grad_perm_weights[q]; +0.0 for a pair that is not
+ *                        routed                                                (nullable)
+ *      A row >= num_rows is skipped and sets EP_DEVERR_SLOT_RANGE.
+ * Sizes: H % 8 == 0; rows 16-byte aligned. Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_HIP. */
+int ep_dispatch_permute_grad(const void *grad_perm_x, const float *grad_perm_weights,
+                             int64_t num_rows, int64_t num_tokens, int hidden, int num_topk,
+                             const int32_t *expert_slot, void *grad_x, float *grad_topk_weights,
+                             int32_t *error_flag, void *stream);
 
 /* ep_hbm_copy -- measurement helper, not a step of the path: a plain 128-bit copy of
  * `bytes` bytes (a multiple of 16; both pointers 16-byte aligned) used as the HBM

@@ -1,0 +1,224 @@
+"""The operators together, as a mixture-of-experts block uses them: norm, layout, expert-major
+dispatch, experts, weighted way back, and the gradients from the block's output to its
+inputs, through ExpertPath and against the whole block in 64 bits on the CPU (the routing
+taken as given). Also a decode loop of single tokens and a training step in a graph."""
+import pytest
+import torch
+
+import combine_ep_get_03_amd as ep
+import plain_ops as P
+from combine_ep_get_03_amd.pipeline import ExpertPath
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def inputs(seed, T, H, E, k, dropped=0.1):
+    g = gen(seed)
+    d = dict(x=torch.randn((T, H), generator=g, device="cuda").to(BF16),
+             residual=(2 * torch.randn((T, H), generator=g, device="cuda")).to(BF16),
+             weight=(1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(BF16),
+             shared=torch.randn((T, H), generator=g, device="cuda").to(BF16),
+             grad_out=torch.randn((T, H), generator=g, device="cuda").to(BF16),
+             grad_res=torch.randn((T, H), generator=g, device="cuda").to(BF16),
+             gate=torch.rand((T, k), generator=g, device="cuda") + 0.1,
+             scale=0.5 + torch.rand((E, H), generator=g, device="cuda"))
+    idx = torch.rand((T, E), generator=g, device="cuda").topk(k, dim=1).indices
+    drop = torch.rand((T, k), generator=g, device="cuda") < dropped
+    d["idx"] = torch.where(drop, -1, idx).contiguous()
+    return d
+
+
+def expert_rows(offset, T, k, E):
+    """Expert of every routed row, from the layout's offsets."""
+    o = offset.long()
+    row = torch.arange(int(o[-1]), device=o.device)
+    return torch.bucketize(row, o[1:], right=True)
+
+
+def experts(rows, e, scale):
+    """Each expert scales its channels: bf16(row * scale[e])."""
+    return (rows.float() * scale[e]).to(BF16)
+
+
+def block_64(d, eps):
+    """The block in 64 bits, with autograd: (residual_out, y, out, leaves)."""
+    leaf = {n: P.f64(d[n]).requires_grad_() for n in ("x", "residual", "weight", "gate", "shared")}
+    s, y = P.rmsnorm(leaf["x"], leaf["residual"], leaf["weight"], eps)
+    idx = d["idx"].cpu()
+    hit = (idx >= 0).unsqueeze(2)
+    zero = torch.zeros((), dtype=torch.float64)
+    per = y.unsqueeze(1) * P.f64(d["scale"])[idx.clamp(min=0)]
+    out = (torch.where(hit, per, zero) * leaf["gate"].unsqueeze(2)).sum(dim=1) + leaf["shared"]
+    return s, y, out, leaf
+
+
+@pytest.mark.parametrize("T,H,E,k,R,N", [(1, 7168, 256, 8, 32, 4), (257, 1024, 16, 4, 4, 2),
+                                         (130, 512, 64, 6, 1, 1), (1000, 128, 16, 2, 2, 1)])
+def test_block_forward_and_backward(T, H, E, k, R, N):
+    print(f"\ncase: block T={T} H={H} E={E} k={k}", flush=True)
+    d = inputs(T + H, T, H, E, k)
+    p = ExpertPath(T, H, E, k, R=R, N=N, training=True)
+    p.norm(d["x"], d["weight"], d["residual"])
+    p.dispatch(d["idx"], d["gate"])
+    M = int(p.expert_offset[-1])
+    assert M == int((d["idx"] >= 0).sum())
+    e = expert_rows(p.expert_offset, T, k, E)
+    expert_out = torch.full((T * k, H), float("nan"), dtype=BF16, device="cuda")
+    expert_out[:M] = experts(p.perm_x[:M], e, d["scale"])
+    p.combine(expert_out, d["gate"], addend=d["shared"])
+    # backwards
+    p.combine_grad(d["grad_out"], expert_out, d["gate"])
+    grad_perm = torch.full((T * k, H), float("nan"), dtype=BF16, device="cuda")
+    grad_perm[:M] = experts(p.grad_expert_out[:M], e, d["scale"])
+    p.dispatch_grad(grad_perm)
+    p.norm_grad(d["weight"], d["grad_res"])
+    assert int(p.error_flag) == 0
+
+    s, y, out, leaf = block_64(d, p.eps)
+    (out * P.f64(d["grad_out"])).sum().add((s * P.f64(d["grad_res"])).sum()).backward()
+    with torch.no_grad():
+        gate, scale, idx = P.f64(d["gate"]), P.f64(d["scale"]), d["idx"].cpu()
+        P.assert_within(p.residual_out, s, P.sum_bound(s), "residual_out")
+        P.assert_within(p.y, y, P.y_bound(y), "y")
+        hit = (idx >= 0).unsqueeze(2)
+        zero = torch.zeros((), dtype=torch.float64)
+        # out: each pair's row was rounded to bf16 twice (the norm's output, the expert's), the
+        # sum once more
+        mag = (torch.where(hit, (y.unsqueeze(1) * scale[idx.clamp(min=0)]).abs(), zero)
+               * gate.unsqueeze(2)).sum(dim=1)
+        P.assert_within(p.out, out, 2.2 * P.BF16 * mag + P.BF16 * 1.01 * out.abs() + 1e-6 * leaf["shared"].abs(),
+                        "out")
+        # the gate's gradient: rows twice rounded, under a dot product with grad_out
+        go = P.f64(d["grad_out"])
+        dot = torch.where(hit, (y.unsqueeze(1) * scale[idx.clamp(min=0)] * go.unsqueeze(1)).abs(), zero).sum(dim=2)
+        P.assert_within(p.grad_topk_weights, leaf["gate"].grad, 2.2 * P.BF16 * dot, "gate's gradient")
+        # the norm's incoming gradient: three roundings on the way (the row's gradient, the
+        # expert's, the sum over a token's rows)
+        dy = (torch.where(hit, scale[idx.clamp(min=0)] * go.unsqueeze(1), zero) * gate.unsqueeze(2))
+        gy, gy_mag = dy.sum(dim=1), dy.abs().sum(dim=1)
+        gy_off = 2.2 * P.BF16 * gy_mag + 1.01 * P.BF16 * gy.abs()
+        P.assert_within(p.grad_y, gy, gy_off, "grad_y")
+        # the norm's own gradient, with grad_y off by gy_off and h rounded to bf16: n is off by
+        # BF16 |n| and r by BF16 relative at most, so each term of dx = r (g - n mean(g n))
+        # by at most 3 BF16 (four factors that hold h: r, n, r and n) plus its share of gy_off
+        w = P.f64(d["weight"]).abs()
+        r = 1 / torch.sqrt(s.square().mean(dim=1, keepdim=True) + p.eps)
+        n, g, g_off = (s * r).abs(), gy.abs() * w, gy_off * w
+        first, second = r * g, r * n * (g * n).mean(dim=1, keepdim=True)
+        off = r * (g_off + n * (g_off * n).mean(dim=1, keepdim=True)) + P.BF16 * 1.1 * first + 5 * P.BF16 * second
+        P.assert_within(p.grad_x, leaf["x"].grad, 1.05 * off + P.BF16 * 1.01 * leaf["x"].grad.abs(), "grad_x")
+        assert torch.equal(leaf["x"].grad, leaf["residual"].grad)
+        woff = ((gy_off + 2.2 * P.BF16 * gy.abs()) * n).sum(dim=0)
+        P.assert_within(p.grad_weight, leaf["weight"].grad, 1.05 * woff, "grad_weight")
+
+
+@pytest.mark.parametrize("T,H,E,k", [(1, 7168, 256, 8), (100, 1024, 16, 4)])
+def test_block_with_e4m3_rows(T, H, E, k):
+    print(f"\ncase: fp8 block T={T} H={H}", flush=True)
+    d = inputs(T + H + 1, T, H, E, k)
+    p = ExpertPath(T, H, E, k, fp8=True)
+    p.norm(d["x"], d["weight"], d["residual"])
+    p.dispatch(d["idx"])
+    M = int(p.expert_offset[-1])
+    e = expert_rows(p.expert_offset, T, k, E)
+    rows = p.perm_x_fp8[:M].view(torch.float8_e4m3fn).float() * p.perm_scales[:M].repeat_interleave(128, dim=1)
+    expert_out = torch.full((T * k, H), float("nan"), dtype=BF16, device="cuda")
+    expert_out[:M] = experts(rows, e, d["scale"])
+    p.combine(expert_out, d["gate"], addend=d["shared"])
+    assert int(p.error_flag) == 0
+    src = p.perm_src_idx[:M].cpu().long()
+    assert torch.equal(p.perm_x_fp8[:M].cpu(), p.y_fp8.cpu()[src])
+    s, y, out, _ = block_64(d, p.eps)
+    with torch.no_grad():
+        idx, hit = d["idx"].cpu(), (d["idx"].cpu() >= 0).unsqueeze(2)
+        zero = torch.zeros((), dtype=torch.float64)
+        scale = P.f64(d["scale"])[idx.clamp(min=0)]
+        per_off = P.fp8_bound(y, P.fp8_scales(y)).unsqueeze(1) * scale * (1 + P.BF16) \
+            + P.BF16 * (y.unsqueeze(1) * scale).abs()
+        off = (torch.where(hit, per_off, zero) * P.f64(d["gate"]).unsqueeze(2)).sum(dim=1)
+        P.assert_within(p.out, out, 1.02 * off + P.BF16 * 1.02 * out.abs() + 1e-5, "out")
+
+
+def test_decode_loop_of_single_tokens():
+    """Ten steps of one token through one ExpertPath, the residual stream kept in place."""
+    H, E, k, T = 2048, 64, 8, 1
+    print("\ncase: decode loop", flush=True)
+    p = ExpertPath(T, H, E, k)
+    d = inputs(77, T, H, E, k, dropped=0.0)
+    res, x = d["residual"], d["x"]
+    for step in range(10):
+        p.norm(x, d["weight"], res)
+        s, y = P.rmsnorm(P.f64(x), P.f64(res), P.f64(d["weight"]), p.eps)
+        P.assert_within(p.y, y, P.y_bound(y), f"y of step {step}")
+        idx = torch.rand((T, E), generator=gen(step), device="cuda").topk(k, dim=1).indices
+        p.dispatch(idx, d["gate"])
+        e = expert_rows(p.expert_offset, T, k, E)
+        expert_out = experts(p.perm_x, e, d["scale"])
+        p.combine(expert_out, d["gate"])
+        slot = p.layout_buf.expert_slot.cpu()
+        want = P.unpermute(P.f64(expert_out), P.f64(d["gate"]), slot, None)
+        P.assert_within(p.out, want, P.unpermute_bound(want, P.f64(expert_out), P.f64(d["gate"]), slot, None),
+                        f"out of step {step}")
+        x, res = p.out.clone(), p.residual_out.clone()
+
+
+def test_training_step_replays_in_a_graph_beside_an_eager_one():
+    """The whole step captured, replayed on new inputs, with the same step run eagerly on a
+    second ExpertPath between the replays; both give the same bits."""
+    T, H, E, k = 200, 1024, 16, 4
+    print("\ncase: training step in a graph", flush=True)
+    d = inputs(5, T, H, E, k)
+    a, b = (ExpertPath(T, H, E, k, training=True) for _ in range(2))
+
+    def step(p):
+        p.norm(d["x"], d["weight"], d["residual"])
+        p.dispatch(d["idx"], d["gate"])
+        p.combine(p.perm_x, d["gate"], addend=d["shared"])
+        p.combine_grad(d["grad_out"], p.perm_x, d["gate"])
+        p.dispatch_grad(p.grad_expert_out)
+        p.norm_grad(d["weight"], d["grad_res"])
+
+    names = ["residual_out", "y", "out", "grad_expert_out", "grad_topk_weights", "grad_y", "grad_x",
+             "grad_weight"]
+    for p in (a, b):
+        p.grad_expert_out.zero_()
+    step(a)
+    step(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a)
+    for rep in range(3):
+        new = inputs(200 + rep, T, H, E, k)
+        for n in d:
+            d[n].copy_(new[n])
+        for p in (a, b):
+            for n in names:
+                getattr(p, n).zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        step(b)
+        torch.cuda.synchronize()
+        for n in names:
+            u, v = getattr(a, n), getattr(b, n)
+            assert torch.equal(u.view(torch.uint8), v.view(torch.uint8)), (rep, n)
+        assert int(a.error_flag) == 0 and int(b.error_flag) == 0
+
+
+def test_gradients_need_a_training_path():
+    p = ExpertPath(4, 128, 16, 2)
+    x = torch.zeros((4, 128), dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="training"):
+        p.dispatch_grad(x)
+    q = ExpertPath(4, 128, 16, 2, training=True)
+    with pytest.raises(ValueError, match="norm"):
+        q.norm_grad(torch.ones(128, device="cuda"))
+    assert ep.EP_OK == 0
