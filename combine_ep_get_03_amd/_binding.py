@@ -641,16 +641,54 @@ def _rows_2d(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _e4m3_bytes(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    """e4m3 codes as the bytes the C ABI takes: uint8, or float8_e4m3fn viewed as uint8."""
-    return t.view(torch.uint8) if t is not None and t.dtype == torch.float8_e4m3fn else t
+# The calls below take a few microseconds on the GPU at decode-sized batches, so the host's
+# share is kept small: one look at the current device per call, one combined check per
+# tensor (a failed one is explained by _shape and _ptr), device addresses as plain ints.
+# One call of ep_rmsnorm with four outputs, kernel launch included: 16.4 us with _shape and
+# _ptr per tensor, HOST_AFTER us so (AMD EPYC host).
+def _row_ptr(t: Optional[torch.Tensor], dtype, shape, name: str, cur: int):
+    """Device address of a required tensor of exactly this type and shape."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == cur and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _shape(t, shape, name)
+    _ptr(t, dtype, name)  # raises
 
 
-def _norm_weight(weight: torch.Tensor, H: int):
-    if weight.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"weight: expected torch.bfloat16 or torch.float32, got {weight.dtype}")
-    _shape(weight, (H,), "weight")
-    return _ptr(weight, weight.dtype, "weight"), int(weight.dtype == torch.float32)
+def _row_ptr_or_null(t: Optional[torch.Tensor], dtype, shape, name: str, cur: int):
+    return None if t is None else _row_ptr(t, dtype, shape, name, cur)
+
+
+def _flag_ptr(t: Optional[torch.Tensor], cur: int):
+    """Device address of the error flag (one int32 or more), or NULL."""
+    if t is None:
+        return None
+    _at_least(t, 1, "error_flag")
+    return _row_ptr(t, torch.int32, t.shape, "error_flag", cur)
+
+
+def _current(stream):
+    """(current device, raw stream handle) of a call; a device that no tensor is on before
+    the first use of the GPU."""
+    if not torch.cuda.is_initialized():
+        return -2, None
+    cur = torch.cuda.current_device()
+    return cur, torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
+
+
+def _codes_ptr(t: Optional[torch.Tensor], shape, name: str, cur: int, nullable: bool = False):
+    """Device address of e4m3 codes: uint8, or float8_e4m3fn."""
+    if t is None and nullable:
+        return None
+    dtype = torch.float8_e4m3fn if t is not None and t.dtype is torch.float8_e4m3fn else torch.uint8
+    return _row_ptr(t, dtype, shape, name, cur)
+
+
+def _norm_weight(weight: torch.Tensor, H: int, cur: int):
+    dtype = weight.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"weight: expected torch.bfloat16 or torch.float32, got {dtype}")
+    return _row_ptr(weight, dtype, (H,), "weight", cur), int(dtype is torch.float32)
 
 
 def ep_rmsnorm(x, weight, *, residual=None, residual_out=None, y=None, y_fp8=None, y_scales=None,
@@ -659,19 +697,17 @@ def ep_rmsnorm(x, weight, *, residual=None, residual_out=None, y=None, y_fp8=Non
     weight), and the e4m3 codes (uint8 or float8_e4m3fn [T][H]) with their scales (fp32
     [T][H/128]). x, residual, residual_out, y: bf16 [T][H]; weight: bf16 or fp32 [H].
     residual_out may be x or residual, y the other of the two."""
-    T, H = _rows_2d(x, "x")
-    y_fp8 = _e4m3_bytes(y_fp8)
-    _shape(residual, (T, H), "residual")
-    _shape(residual_out, (T, H), "residual_out")
-    _shape(y, (T, H), "y")
-    _shape(y_fp8, (T, H), "y_fp8")
-    _shape(y_scales, (T, H // 128), "y_scales")
-    w, w_fp32 = _norm_weight(weight, H)
+    rows = T, H = _rows_2d(x, "x")
+    cur, st = _current(stream)
+    w, w_fp32 = _norm_weight(weight, H, cur)
+    bf16 = torch.bfloat16
     _check(load().ep_rmsnorm(
-        _ptr(x, torch.bfloat16, "x"), _ptr(residual, torch.bfloat16, "residual", True), w, w_fp32,
-        eps, T, H, _ptr(residual_out, torch.bfloat16, "residual_out", True),
-        _ptr(y, torch.bfloat16, "y", True), _ptr(y_fp8, torch.uint8, "y_fp8", True),
-        _ptr(y_scales, torch.float32, "y_scales", True), _stream(stream)), "ep_rmsnorm")
+        _row_ptr(x, bf16, rows, "x", cur), _row_ptr_or_null(residual, bf16, rows, "residual", cur),
+        w, w_fp32, eps, T, H, _row_ptr_or_null(residual_out, bf16, rows, "residual_out", cur),
+        _row_ptr_or_null(y, bf16, rows, "y", cur),
+        _codes_ptr(y_fp8, rows, "y_fp8", cur, True),
+        _row_ptr_or_null(y_scales, torch.float32, (T, H // 128), "y_scales", cur), st),
+        "ep_rmsnorm")
 
 
 def ep_rmsnorm_grad_workspace_bytes(num_tokens: int, hidden: int) -> int:
@@ -685,21 +721,19 @@ def ep_rmsnorm_grad(grad_y, h, weight, *, grad_x, grad_residual_out=None, grad_w
     needs `workspace`, uint8 of ep_rmsnorm_grad_workspace_bytes). h: the forward's
     residual_out (its x without a residual). grad_y, grad_residual_out, h, grad_x: bf16
     [T][H]. grad_x may be grad_y, grad_residual_out or h."""
-    T, H = _rows_2d(h, "h")
-    _shape(grad_y, (T, H), "grad_y")
-    _shape(grad_residual_out, (T, H), "grad_residual_out")
-    _shape(grad_x, (T, H), "grad_x")
-    _shape(grad_weight, (H,), "grad_weight")
-    w, w_fp32 = _norm_weight(weight, H)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rows = T, H = _rows_2d(h, "h")
+    cur, st = _current(stream)
+    w, w_fp32 = _norm_weight(weight, H, cur)
+    bf16 = torch.bfloat16
+    ws = None if workspace is None else _row_ptr(workspace, torch.uint8, workspace.shape,
+                                                 "workspace", cur)
     _check(load().ep_rmsnorm_grad(
-        _ptr(grad_y, torch.bfloat16, "grad_y"),
-        _ptr(grad_residual_out, torch.bfloat16, "grad_residual_out", True),
-        _ptr(h, torch.bfloat16, "h"), w, w_fp32, eps, T, H,
-        _ptr(grad_x, torch.bfloat16, "grad_x"),
-        _ptr(grad_weight, torch.float32, "grad_weight", True),
-        _ptr(workspace, torch.uint8, "workspace", True), ws_bytes, _stream(stream)),
-        "ep_rmsnorm_grad")
+        _row_ptr(grad_y, bf16, rows, "grad_y", cur),
+        _row_ptr_or_null(grad_residual_out, bf16, rows, "grad_residual_out", cur),
+        _row_ptr(h, bf16, rows, "h", cur), w, w_fp32, eps, T, H,
+        _row_ptr(grad_x, bf16, rows, "grad_x", cur),
+        _row_ptr_or_null(grad_weight, torch.float32, (H,), "grad_weight", cur),
+        ws, 0 if workspace is None else workspace.numel(), st), "ep_rmsnorm_grad")
 
 
 def ep_dispatch_permute_fp8(x_fp8, x_scales, topk_weights, expert_slot, *, perm_x_fp8,
@@ -710,25 +744,19 @@ def ep_dispatch_permute_fp8(x_fp8, x_scales, topk_weights, expert_slot, *, perm_
     T, H = _rows_2d(x_fp8, "x_fp8")
     _, k = _rows_2d(expert_slot, "expert_slot")
     cap, _ = _rows_2d(perm_x_fp8, "perm_x_fp8")
-    x_fp8, perm_x_fp8 = _e4m3_bytes(x_fp8), _e4m3_bytes(perm_x_fp8)
-    _shape(x_scales, (T, H // 128), "x_scales")
-    _shape(topk_weights, (T, k), "topk_weights")
-    _shape(expert_slot, (T, k), "expert_slot")
-    _shape(perm_x_fp8, (cap, H), "perm_x_fp8")
-    _shape(perm_scales, (cap, H // 128), "perm_scales")
-    _shape(perm_weights, (cap,), "perm_weights")
-    _shape(perm_src_idx, (cap,), "perm_src_idx")
-    _at_least(error_flag, 1, "error_flag")
+    cur, st = _current(stream)
+    G = H // 128
+    f32, i32 = torch.float32, torch.int32
     _check(load().ep_dispatch_permute_fp8(
-        _ptr(x_fp8, torch.uint8, "x_fp8"), _ptr(x_scales, torch.float32, "x_scales"),
-        _ptr(topk_weights, torch.float32, "topk_weights", True), T, H, k,
-        _ptr(expert_slot, torch.int32, "expert_slot"),
-        _ptr(perm_x_fp8, torch.uint8, "perm_x_fp8"),
-        _ptr(perm_scales, torch.float32, "perm_scales"),
-        _ptr(perm_weights, torch.float32, "perm_weights", True),
-        _ptr(perm_src_idx, torch.int32, "perm_src_idx", True), cap,
-        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
-        "ep_dispatch_permute_fp8")
+        _codes_ptr(x_fp8, (T, H), "x_fp8", cur),
+        _row_ptr(x_scales, f32, (T, G), "x_scales", cur),
+        _row_ptr_or_null(topk_weights, f32, (T, k), "topk_weights", cur), T, H, k,
+        _row_ptr(expert_slot, i32, (T, k), "expert_slot", cur),
+        _codes_ptr(perm_x_fp8, (cap, H), "perm_x_fp8", cur),
+        _row_ptr(perm_scales, f32, (cap, G), "perm_scales", cur),
+        _row_ptr_or_null(perm_weights, f32, (cap,), "perm_weights", cur),
+        _row_ptr_or_null(perm_src_idx, i32, (cap,), "perm_src_idx", cur), cap,
+        _flag_ptr(error_flag, cur), st), "ep_dispatch_permute_fp8")
 
 
 def ep_combine_unpermute(expert_out, topk_weights, expert_slot, *, out, addend=None,
@@ -738,16 +766,14 @@ def ep_combine_unpermute(expert_out, topk_weights, expert_slot, *, out, addend=N
     expert_slot: int32 [T][k]; addend, out: bf16 [T][H] (out may be addend)."""
     rows, H = _rows_2d(expert_out, "expert_out")
     T, k = _rows_2d(expert_slot, "expert_slot")
-    _shape(topk_weights, (T, k), "topk_weights")
-    _shape(addend, (T, H), "addend")
-    _shape(out, (T, H), "out")
-    _at_least(error_flag, 1, "error_flag")
+    cur, st = _current(stream)
+    bf16 = torch.bfloat16
     _check(load().ep_combine_unpermute(
-        _ptr(expert_out, torch.bfloat16, "expert_out"), rows,
-        _ptr(topk_weights, torch.float32, "topk_weights", True), T, H, k,
-        _ptr(expert_slot, torch.int32, "expert_slot"),
-        _ptr(addend, torch.bfloat16, "addend", True), _ptr(out, torch.bfloat16, "out"),
-        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
+        _row_ptr(expert_out, bf16, (rows, H), "expert_out", cur), rows,
+        _row_ptr_or_null(topk_weights, torch.float32, (T, k), "topk_weights", cur), T, H, k,
+        _row_ptr(expert_slot, torch.int32, (T, k), "expert_slot", cur),
+        _row_ptr_or_null(addend, bf16, (T, H), "addend", cur),
+        _row_ptr(out, bf16, (T, H), "out", cur), _flag_ptr(error_flag, cur), st),
         "ep_combine_unpermute")
 
 
@@ -760,21 +786,18 @@ def ep_combine_unpermute_grad(grad_out, expert_out, topk_weights, expert_slot, *
     T, H = _rows_2d(grad_out, "grad_out")
     _, k = _rows_2d(expert_slot, "expert_slot")
     rows, _ = _rows_2d(grad_expert_out, "grad_expert_out")
-    _shape(expert_out, (rows, H), "expert_out")
-    _shape(topk_weights, (T, k), "topk_weights")
-    _shape(expert_slot, (T, k), "expert_slot")
-    _shape(grad_expert_out, (rows, H), "grad_expert_out")
-    _shape(grad_topk_weights, (T, k), "grad_topk_weights")
-    _at_least(error_flag, 1, "error_flag")
+    cur, st = _current(stream)
+    bf16 = torch.bfloat16
+    if expert_out is None and grad_topk_weights is not None:
+        raise ValueError("expert_out is required with grad_topk_weights")
     _check(load().ep_combine_unpermute_grad(
-        _ptr(grad_out, torch.bfloat16, "grad_out"),
-        _ptr(expert_out, torch.bfloat16, "expert_out", grad_topk_weights is None), rows,
-        _ptr(topk_weights, torch.float32, "topk_weights", True), T, H, k,
-        _ptr(expert_slot, torch.int32, "expert_slot"),
-        _ptr(grad_expert_out, torch.bfloat16, "grad_expert_out"),
-        _ptr(grad_topk_weights, torch.float32, "grad_topk_weights", True),
-        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
-        "ep_combine_unpermute_grad")
+        _row_ptr(grad_out, bf16, (T, H), "grad_out", cur),
+        _row_ptr_or_null(expert_out, bf16, (rows, H), "expert_out", cur), rows,
+        _row_ptr_or_null(topk_weights, torch.float32, (T, k), "topk_weights", cur), T, H, k,
+        _row_ptr(expert_slot, torch.int32, (T, k), "expert_slot", cur),
+        _row_ptr(grad_expert_out, bf16, (rows, H), "grad_expert_out", cur),
+        _row_ptr_or_null(grad_topk_weights, torch.float32, (T, k), "grad_topk_weights", cur),
+        _flag_ptr(error_flag, cur), st), "ep_combine_unpermute_grad")
 
 
 def ep_dispatch_permute_grad(grad_perm_x, expert_slot, *, grad_x, grad_perm_weights=None,
@@ -783,18 +806,16 @@ def ep_dispatch_permute_grad(grad_perm_x, expert_slot, *, grad_x, grad_perm_weig
     grad_perm_x), grad_topk_weights (fp32 [T][k]) from grad_perm_weights (fp32 [rows])."""
     rows, H = _rows_2d(grad_perm_x, "grad_perm_x")
     T, k = _rows_2d(expert_slot, "expert_slot")
-    _shape(grad_perm_weights, (rows,), "grad_perm_weights")
-    _shape(grad_x, (T, H), "grad_x")
-    _shape(grad_topk_weights, (T, k), "grad_topk_weights")
-    _at_least(error_flag, 1, "error_flag")
+    cur, st = _current(stream)
+    if grad_perm_weights is None and grad_topk_weights is not None:
+        raise ValueError("grad_perm_weights is required with grad_topk_weights")
     _check(load().ep_dispatch_permute_grad(
-        _ptr(grad_perm_x, torch.bfloat16, "grad_perm_x"),
-        _ptr(grad_perm_weights, torch.float32, "grad_perm_weights", grad_topk_weights is None),
-        rows, T, H, k, _ptr(expert_slot, torch.int32, "expert_slot"),
-        _ptr(grad_x, torch.bfloat16, "grad_x"),
-        _ptr(grad_topk_weights, torch.float32, "grad_topk_weights", True),
-        _ptr(error_flag, torch.int32, "error_flag", True), _stream(stream)),
-        "ep_dispatch_permute_grad")
+        _row_ptr(grad_perm_x, torch.bfloat16, (rows, H), "grad_perm_x", cur),
+        _row_ptr_or_null(grad_perm_weights, torch.float32, (rows,), "grad_perm_weights", cur),
+        rows, T, H, k, _row_ptr(expert_slot, torch.int32, (T, k), "expert_slot", cur),
+        _row_ptr(grad_x, torch.bfloat16, (T, H), "grad_x", cur),
+        _row_ptr_or_null(grad_topk_weights, torch.float32, (T, k), "grad_topk_weights", cur),
+        _flag_ptr(error_flag, cur), st), "ep_dispatch_permute_grad")
 
 
 def ep_hbm_copy(src, dst, nbytes: Optional[int] = None, stream=None) -> None:

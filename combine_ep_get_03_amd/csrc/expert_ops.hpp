@@ -33,11 +33,59 @@ __device__ __forceinline__ u32x4 narrow8(const float (&f)[8]) {
     return w;
 }
 
-// Sum over the wave's 64 lanes, in every lane.
+// Cross-lane moves in the vector pipe (DPP): lanes whose source is outside the row of 16, or
+// that the masks leave out, take 0.
+template <int kCtrl, int kRowMask = 0xf>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, kRowMask, 0xf,
+                                                      kRowMask == 0xf));
+}
+
+// Sum over the wave's 64 lanes (all of them active), the same value in every lane: prefix
+// sums within rows of 16 (row_shr 1, 2, 4, 8), then each row's last lane into the rows
+// above it (row_bcast 15 and 31); lane 63 ends with the total.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
-    return v;
+    v += dpp_or_zero<0x111>(v);
+    v += dpp_or_zero<0x112>(v);
+    v += dpp_or_zero<0x114>(v);
+    v += dpp_or_zero<0x118>(v);
+    v += dpp_or_zero<0x142, 0xa>(v);
+    v += dpp_or_zero<0x143, 0xc>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
+}
+
+// Largest of 16 aligned lanes (a row), in each of them: rotations by 8, 4, 2, 1. v >= 0.
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, dpp_or_zero<0x128>(v));
+    v = fmaxf(v, dpp_or_zero<0x124>(v));
+    v = fmaxf(v, dpp_or_zero<0x122>(v));
+    return fmaxf(v, dpp_or_zero<0x121>(v));
+}
+
+// Largest of 8 aligned lanes, in each of them: neighbours, pairs, then the halves mirrored.
+// v >= 0.
+__device__ __forceinline__ float half_row_max(float v) {
+    v = fmaxf(v, dpp_or_zero<0xb1>(v));   // quad_perm 1 0 3 2
+    v = fmaxf(v, dpp_or_zero<0x4e>(v));   // quad_perm 2 3 0 1
+    return fmaxf(v, dpp_or_zero<0x141>(v));  // row_half_mirror
+}
+
+// Word v (16 bytes) of a buffer; zeros past its end.
+template <int kPolicy>
+__device__ __forceinline__ u32x4 load_word(__amdgpu_buffer_rsrc_t b, int v) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, v * 16, 0, kPolicy));
+}
+
+// Stores word v; dropped past the buffer's end.
+template <int kPolicy>
+__device__ __forceinline__ void store_word(__amdgpu_buffer_rsrc_t b, int v, u32x4 w) {
+    __builtin_amdgcn_raw_buffer_store_b128(w, b, v * 16, 0, kPolicy);
+}
+
+// Row t of an array of rows of V words as a buffer; of no bytes when the array is null, so
+// that its loads are zeros and its stores dropped without a branch.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const u32x4* rows, int64_t t, int V) {
+    return raw_buffer(rows ? rows + t * V : nullptr, rows ? static_cast<uint32_t>(V) * 16u : 0u);
 }
 
 // ---------------------------------------------------------------- launchers

@@ -6,114 +6,247 @@
 //   its gradient   grad_y[q] = bf16(w[t][j] grad_out[t]), grad_w[t][j] = <grad_out[t], y[q]>
 //   permute's      grad_x[t] = bf16(sum over j of grad_perm_x[q]), grad_w[t][j] = grad_perm_w[q]
 // All are bound by the bytes of the expert-major rows, which move once.
+#include "dispatch_rows.hpp"
 #include "expert_ops.hpp"
 
 namespace ep {
 namespace {
 
-constexpr int kT = 256;  // threads per block
+constexpr int kT = 256;  // threads per block: a few waves, each with its own piece of work
 constexpr int kWaves = kT / kWave;
+constexpr int64_t kMaxWaves = int64_t{1} << 24;  // per launch: a wave's index stays 32 bits
 
-// Wave (t, j) copies token t's codes and scales to row q.
+// Launches f(t0, t_end, grid) over token ranges of at most kMaxWaves waves.
+template <typename F>
+hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
+    const int64_t step = std::max<int64_t>(1, kMaxWaves / waves_per_token);
+    for (int64_t t0 = 0; t0 < T; t0 += step) {
+        const int64_t t_end = std::min(T, t0 + step);
+        const int64_t grid = ((t_end - t0) * waves_per_token + kWaves - 1) / kWaves;
+        if (!grid_fits(grid, kT)) return hipErrorInvalidConfiguration;
+        f(t0, t_end, static_cast<unsigned>(grid));
+        EP_RETURN_IF_LAUNCH_FAILED();
+    }
+    return hipSuccess;
+}
+
+// Wave (t, j) copies token t's codes and scales to row q, in the form of the bf16 permute:
+// the row's loads are issued before the slot arrives, the codes leave as one burst of
+// 128-bit stores (store_row_pass) and the token's other waves find the row in the L2.
+// HBM-write bound: 8 rows written per row read at top-8. 4096 tokens of 7168 channels over
+// 256 experts: 46.4 us, 5.9 TB/s; one wave per pair looping over guarded stores 47.2 us.
+//
+// A row's scales (224 bytes at 7168 channels) fill no whole cache line, so neighbouring rows,
+// written by waves of different XCDs, share lines. Cached scale stores let each L2 gather
+// its share of a line; past about half of the L2s' 32 MB they are evicted half-filled, and
+// non-temporal stores take over. Measured, cached against non-temporal: 46.0 against
+// 51.5 us at 4096 tokens (7 MB of scales), 93.3 against 103.4 us at 8192 (15 MB), 172.8
+// against 152.1 us at 12000 (22 MB), 236.6 against 229.3 us at 16384 (29 MB).
+constexpr int64_t kCachedScaleBytes = int64_t{16} << 20;
+
+template <int WPL, bool kMulti, int kScalePolicy>
 __global__ __launch_bounds__(kT) void permute_fp8_kernel(
     const u32x4* __restrict__ codes, const float* __restrict__ scales,
-    const float* __restrict__ topk_w, int64_t pairs, int V, int G, int k,
-    const int32_t* __restrict__ expert_slot, u32x4* __restrict__ perm_codes,
+    const float* __restrict__ topk_w, int64_t t0, int64_t t_end, int V, int G, int k,
+    const int32_t* __restrict__ expert_slot, FastDiv D, u32x4* __restrict__ perm_codes,
     float* __restrict__ perm_scales, float* __restrict__ perm_w, int32_t* __restrict__ perm_src,
     int64_t cap, int32_t* __restrict__ error_flag) {
-    const int64_t p = static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / kWave;
-    if (p >= pairs) return;
+    int64_t t;
+    int j;
+    if (!dest_wave<kT>(t0, t_end, D, t, j)) return;
     const int lane = lane_id();
-    const int64_t q = expert_slot[p];
+    const int64_t q = expert_slot[t * k + j];
+    const float w = perm_w ? topk_w[t * k + j] : 0.0f;
+    const u32x4* xr = codes + t * V;
+    const float* sr = scales + t * G;
+    u32x4 v[WPL];
+    load_row_cached(v, xr, 0, V);  // first pass, issued before the slot is known
+    float s = sr[min(lane, G - 1)];
     if (q < 0) return;
     if (q >= cap) {
         if (lane == 0) raise_error(error_flag, kErrRecvOverflow);
         return;
     }
-    const int64_t t = p / k;
-    for (int v = lane; v < V; v += kWave) store_stream(perm_codes + q * V + v, codes[t * V + v]);
-    for (int g = lane; g < G; g += kWave) perm_scales[q * G + g] = scales[t * G + g];
+    u32x4* row = perm_codes + q * V;
+    for (int v0 = 0; v0 < V; v0 += kWave * WPL) {
+        if (v0 != 0) load_row_cached(v, xr, v0, V);
+        store_row_pass(row, V, v0, v);
+        if constexpr (!kMulti) break;
+    }
+    const __amdgpu_buffer_rsrc_t sb = raw_buffer(perm_scales + q * G, static_cast<uint32_t>(G) * 4u);
+    for (int g = lane; g - lane < G; g += kWave) {  // stores past G are dropped
+        if (g != lane) s = sr[min(g, G - 1)];
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), sb, g * 4, 0, kScalePolicy);
+    }
     if (lane == 0) {
-        if (perm_w) perm_w[q] = topk_w[p];
+        if (perm_w) perm_w[q] = w;
         if (perm_src) perm_src[q] = static_cast<int32_t>(t);
     }
 }
 
-// One block per token.
+// kB of token t's pairs, j0 .. j0 + kB - 1, for every lane of a wave alike: their weights, and
+// their rows' places as buffers of V words. A pair that is not routed, out of range or past
+// k gets a buffer of no bytes and the weight 0, so that its load returns zeros and its
+// store is dropped without a branch: behind a branch of its own, each load would first
+// wait for every load before it. t has to be the same in all lanes.
+template <int kB>
+struct Pairs {
+    int32_t q[kB];
+    float w[kB];
+
+    __device__ __forceinline__ Pairs(const int32_t* __restrict__ slot,
+                                     const float* __restrict__ topk_w, int64_t t, int j0, int k,
+                                     int64_t num_rows, int32_t& errbits) {
+        const int64_t at = t * k;
+#pragma unroll
+        for (int i = 0; i < kB; ++i) q[i] = slot[at + min(j0 + i, k - 1)];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) w[i] = 1.0f;
+        if (topk_w) {
+#pragma unroll
+            for (int i = 0; i < kB; ++i) w[i] = topk_w[at + min(j0 + i, k - 1)];
+        }
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+            if (q[i] >= num_rows) errbits |= kErrSlotRange;
+            if (q[i] >= num_rows || j0 + i >= k) q[i] = -1;
+            if (q[i] < 0) w[i] = 0.0f;
+        }
+    }
+
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t place(const u32x4* rows, int i, int V) const {
+        return raw_buffer(rows + static_cast<int64_t>(max(q[i], 0)) * V,
+                          q[i] >= 0 ? static_cast<uint32_t>(V) * 16u : 0u);
+    }
+};
+
+// Wave (t, c) sums words [64 c, 64 c + 64) of token t's rows, one word per lane, kB rows'
+// loads in flight together. Bound by the rows' reads (8 per row written at top-8). Measured
+// on MI355X at 7168 channels, top-8 of 256 experts: 91.1 us at 4096 tokens and 410.7 us at
+// 16384 with an addend (5.8 and 5.7 TB/s); 64 tokens 4.2 us. Two words per lane ran 90.9,
+// 419.7 and 5.3 us; cached row loads 97.2 and 434.9 us; a block per token walking its pairs
+// one after the other 99.2, 456.2 and 12.7 us.
+template <int kB>
 __global__ __launch_bounds__(kT) void unpermute_kernel(
     const u32x4* __restrict__ rows, int64_t num_rows, const float* __restrict__ topk_w,
-    const int32_t* __restrict__ expert_slot, int V, int k, const u32x4* addend, u32x4* out,
-    const float* __restrict__ grad_perm_w, float* __restrict__ grad_w,
-    int32_t* __restrict__ error_flag) {
-    const int64_t t = blockIdx.x;
-    const int32_t* slot = expert_slot + t * k;
-    for (int v = threadIdx.x; v < V; v += kT) {
-        float acc[8] = {};
-        for (int j = 0; j < k; ++j) {
-            const int64_t q = slot[j];
-            if (q < 0 || q >= num_rows) continue;
-            const float w = topk_w ? topk_w[t * k + j] : 1.0f;
-            float f[8];
-            widen8(load_stream(rows + q * V + v), f);
+    const int32_t* __restrict__ expert_slot, int64_t t0, int64_t t_end, int V, int k, FastDiv C,
+    const u32x4* addend, u32x4* out, const float* __restrict__ grad_perm_w,
+    float* __restrict__ grad_w, int32_t* __restrict__ error_flag) {
+    int64_t t;
+    int c;
+    if (!dest_wave<kT>(t0, t_end, C, t, c)) return;
+    const int lane = lane_id();
+    const int v = c * kWave + lane;
+    const u32x4 ad = load_word<kPolicyNt>(row_buffer(addend, t, V), v);
+    float acc[8] = {};
+    int32_t errbits = 0;
+    for (int j0 = 0; j0 < k; j0 += kB) {
+        const Pairs<kB> pr(expert_slot, topk_w, t, j0, k, num_rows, errbits);
+        u32x4 p[kB];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += w * f[i];
-        }
-        if (addend) {
-            float f[8];
-            widen8(addend[t * V + v], f);
+        for (int i = 0; i < kB; ++i) p[i] = load_word<kPolicyNt>(pr.place(rows, i, V), v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += f[i];
+        for (int i = 0; i < kB; ++i) {
+            float f[8];
+            widen8(p[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += pr.w[i] * f[e];
         }
-        out[t * V + v] = narrow8(acc);
     }
-    for (int j = threadIdx.x; j < k; j += kT) {
-        const int64_t q = slot[j];
-        if (q >= num_rows) raise_error(error_flag, kErrSlotRange);
-        if (grad_w) grad_w[t * k + j] = q >= 0 && q < num_rows ? grad_perm_w[q] : 0.0f;
+    float f[8];
+    widen8(ad, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] += acc[e];
+    store_word<kPolicyNt>(row_buffer(out, t, V), v, narrow8(f));
+    if (c == 0) {
+        if (errbits && lane == 0) raise_error(error_flag, errbits);
+        if (grad_w) {
+            for (int j = lane; j < k; j += kWave) {
+                const int64_t s = expert_slot[t * k + j];
+                grad_w[t * k + j] = s >= 0 && s < num_rows ? grad_perm_w[s] : 0.0f;
+            }
+        }
     }
 }
 
-// One block per token: its pairs in turn.
+// Wave (t, j) has the pair's row to itself: kDot adds up <grad_out[t], row q> in registers and
+// one wave reduction, kRows writes row q = w grad_out[t]; with both, the row is read before
+// it is written, word by word, so grad_rows may be rows. grad_out's row is read with
+// cached loads, which a token's other waves hit, and its first pass is issued before the
+// slot arrives. A short-lived wave per pair keeps the rows in flight close together in
+// memory: a block per token, all its pairs at once (one read of grad_out, dots joined
+// through LDS), took 191.5 against 187.5 us at 4096 tokens and 9.3 against 8.2 us at 64.
+//
+// kPolicy: the cache policy of the rows' loads.
+template <int WPL, bool kDot, bool kRows, int kPolicy>
 __global__ __launch_bounds__(kT) void unpermute_grad_kernel(
     const u32x4* __restrict__ grad_out, const u32x4* rows, int64_t num_rows,
-    const float* __restrict__ topk_w, const int32_t* __restrict__ expert_slot, int V, int k,
-    u32x4* grad_rows, float* __restrict__ grad_w, int32_t* __restrict__ error_flag) {
-    __shared__ float red[kWaves];
-    const int64_t t = blockIdx.x;
-    for (int j = 0; j < k; ++j) {
-        const int64_t q = expert_slot[t * k + j];
-        const bool routed = q >= 0 && q < num_rows;
-        if (q >= num_rows && threadIdx.x == 0) raise_error(error_flag, kErrSlotRange);
-        float dot = 0.0f;
-        if (routed) {
-            const float w = topk_w ? topk_w[t * k + j] : 1.0f;
-            for (int v = threadIdx.x; v < V; v += kT) {
-                float g[8];
-                widen8(grad_out[t * V + v], g);
-                if (grad_w) {
-                    float f[8];
-                    widen8(load_stream(rows + q * V + v), f);
+    const float* __restrict__ topk_w, const int32_t* __restrict__ expert_slot, int64_t t0,
+    int64_t t_end, int V, int k, FastDiv D, u32x4* grad_rows, float* __restrict__ grad_w,
+    int32_t* __restrict__ error_flag) {
+    int64_t t;
+    int j;
+    if (!dest_wave<kT>(t0, t_end, D, t, j)) return;
+    const int lane = lane_id();
+    const int64_t at = t * k + j;
+    const int64_t q = expert_slot[at];
+    const float w = topk_w ? topk_w[at] : 1.0f;
+    const __amdgpu_buffer_rsrc_t gb = row_buffer(grad_out, t, V);
+    u32x4 g[WPL];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot += g[i] * f[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] *= w;
-                store_stream(grad_rows + q * V + v, narrow8(g));
-            }
+    for (int i = 0; i < WPL; ++i) g[i] = load_word<0>(gb, i * kWave + lane);
+    if (q < 0 || q >= num_rows) {
+        if (lane == 0) {
+            if (kDot) grad_w[at] = 0.0f;
+            if (q >= num_rows) raise_error(error_flag, kErrSlotRange);
         }
-        if (grad_w) {
-            dot = wave_sum(dot);
-            if (lane_id() == 0) red[threadIdx.x / kWave] = dot;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                float s = 0.0f;
-                for (int i = 0; i < kWaves; ++i) s += red[i];
-                grad_w[t * k + j] = s;
+        return;
+    }
+    const __amdgpu_buffer_rsrc_t yb = row_buffer(rows, q, V);
+    const __amdgpu_buffer_rsrc_t ob = row_buffer(grad_rows, q, V);
+    float dot = 0.0f;
+    for (int v0 = 0; v0 < V; v0 += kWave * WPL) {
+        u32x4 y[WPL];
+        if constexpr (kDot) {
+#pragma unroll
+            for (int i = 0; i < WPL; ++i) y[i] = load_word<kPolicy>(yb, v0 + i * kWave + lane);
+        }
+        if (v0 != 0) {
+#pragma unroll
+            for (int i = 0; i < WPL; ++i) g[i] = load_word<0>(gb, v0 + i * kWave + lane);
+        }
+#pragma unroll
+        for (int i = 0; i < WPL; ++i) {
+            float gf[8];
+            widen8(g[i], gf);
+            if constexpr (kDot) {  // words past the row are zeros on both sides
+                float f[8];
+                widen8(y[i], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dot += gf[e] * f[e];
             }
-            __syncthreads();
+            if constexpr (kRows) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) gf[e] *= w;
+                store_word<kPolicyNt>(ob, v0 + i * kWave + lane, narrow8(gf));
+            }
         }
     }
+    if constexpr (kDot) {
+        dot = wave_sum(dot);
+        if (lane == 0) grad_w[at] = dot;
+    }
 }
+
+// Above this many bytes of routed rows the dots and the rows are two launches, one that
+// mostly reads and one that mostly writes: HBM moves a stream of reads and then a stream of
+// writes faster than the two mixed over scattered rows. Measured on MI355X, one launch
+// against two: 188.1 against 172.3 us at 4096 tokens (470 MB of rows), 394 against 343 us at
+// 8192, 48.5 against 46.1 us at 1024 (117 MB). Below it one launch with cached row loads,
+// since a set this small may still lie in the 256 MB Infinity Cache, where the experts
+// left it: 22.7 us against 28.1 us with non-temporal loads at 512 tokens (59 MB), and the
+// second launch would be a larger share.
+constexpr int64_t kOneLaunchBytes = int64_t{64} << 20;
 
 }  // namespace
 
@@ -122,29 +255,55 @@ hipError_t launch_dispatch_permute_fp8(const void* x_fp8, const float* x_scales,
                                        const int32_t* expert_slot, void* perm_x,
                                        float* perm_scales, float* perm_w, int32_t* perm_src,
                                        int64_t cap, int32_t* error_flag, hipStream_t stream) {
-    if (T == 0) return hipSuccess;
-    const int64_t pairs = T * k;
-    const int64_t grid = (pairs + kWaves - 1) / kWaves;
-    if (!grid_fits(grid, kT)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(permute_fp8_kernel, dim3(static_cast<unsigned>(grid)), dim3(kT), 0, stream,
-                       static_cast<const u32x4*>(x_fp8), x_scales, topk_w, pairs, H / 16, H / 128,
-                       k, expert_slot, static_cast<u32x4*>(perm_x), perm_scales, perm_w, perm_src,
-                       cap, error_flag);
-    return hipGetLastError();
+    const int V = H / 16, G = H / kNormGroup;
+    const FastDiv fd = FastDiv::make(k);
+    const bool cached = T * k * G * static_cast<int64_t>(sizeof(float)) <= kCachedScaleBytes;
+    return by_token_range(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
+        with_row_width<14, false>(V, [&](auto wpl, auto multi) {
+            constexpr int w = decltype(wpl)::value;
+            constexpr bool m = decltype(multi)::value;
+            const auto kernel = cached ? permute_fp8_kernel<w, m, 0>
+                                       : permute_fp8_kernel<w, m, kPolicyNt>;
+            hipLaunchKernelGGL(kernel, dim3(grid), dim3(kT), 0, stream,
+                               static_cast<const u32x4*>(x_fp8), x_scales, topk_w, t0, t_end, V, G,
+                               k, expert_slot, fd, static_cast<u32x4*>(perm_x), perm_scales,
+                               perm_w, perm_src, cap, error_flag);
+        });
+    });
+}
+
+static hipError_t launch_unpermute(const void* rows, int64_t num_rows, const float* topk_w,
+                                   const int32_t* expert_slot, int64_t T, int H, int k,
+                                   const void* addend, void* out, const float* grad_perm_w,
+                                   float* grad_w, int32_t* error_flag, hipStream_t stream) {
+    const int V = H / 8;
+    const int C = (V + kWave - 1) / kWave;
+    const FastDiv fd = FastDiv::make(C);
+    const auto kernel = k <= 2   ? unpermute_kernel<2>
+                        : k <= 4 ? unpermute_kernel<4>
+                                 : unpermute_kernel<8>;
+    return by_token_range(T, C, [&](int64_t t0, int64_t t_end, unsigned grid) {
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(kT), 0, stream,
+                           static_cast<const u32x4*>(rows), num_rows, topk_w, expert_slot, t0,
+                           t_end, V, k, fd, static_cast<const u32x4*>(addend),
+                           static_cast<u32x4*>(out), grad_perm_w, grad_w, error_flag);
+    });
 }
 
 hipError_t launch_combine_unpermute(const void* rows, int64_t num_rows, const float* topk_w,
                                     const int32_t* expert_slot, int64_t T, int H, int k,
                                     const void* addend, void* out, int32_t* error_flag,
                                     hipStream_t stream) {
-    if (T == 0) return hipSuccess;
-    if (!grid_fits(T, kT)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(unpermute_kernel, dim3(static_cast<unsigned>(T)), dim3(kT), 0, stream,
-                       static_cast<const u32x4*>(rows), num_rows, topk_w, expert_slot, H / 8, k,
-                       static_cast<const u32x4*>(addend), static_cast<u32x4*>(out),
-                       static_cast<const float*>(nullptr), static_cast<float*>(nullptr),
-                       error_flag);
-    return hipGetLastError();
+    return launch_unpermute(rows, num_rows, topk_w, expert_slot, T, H, k, addend, out, nullptr,
+                            nullptr, error_flag, stream);
+}
+
+hipError_t launch_dispatch_permute_grad(const void* grad_rows, const float* grad_perm_w,
+                                        int64_t num_rows, const int32_t* expert_slot, int64_t T,
+                                        int H, int k, void* grad_x, float* grad_w,
+                                        int32_t* error_flag, hipStream_t stream) {
+    return launch_unpermute(grad_rows, num_rows, nullptr, expert_slot, T, H, k, nullptr, grad_x,
+                            grad_perm_w, grad_w, error_flag, stream);
 }
 
 hipError_t launch_combine_unpermute_grad(const void* grad_out, const void* rows,
@@ -152,27 +311,33 @@ hipError_t launch_combine_unpermute_grad(const void* grad_out, const void* rows,
                                          const int32_t* expert_slot, int64_t T, int H, int k,
                                          void* grad_rows, float* grad_w, int32_t* error_flag,
                                          hipStream_t stream) {
-    if (T == 0) return hipSuccess;
-    if (!grid_fits(T, kT)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(unpermute_grad_kernel, dim3(static_cast<unsigned>(T)), dim3(kT), 0, stream,
-                       static_cast<const u32x4*>(grad_out), static_cast<const u32x4*>(rows),
-                       num_rows, topk_w, expert_slot, H / 8, k, static_cast<u32x4*>(grad_rows),
-                       grad_w, error_flag);
-    return hipGetLastError();
-}
-
-hipError_t launch_dispatch_permute_grad(const void* grad_rows, const float* grad_perm_w,
-                                        int64_t num_rows, const int32_t* expert_slot, int64_t T,
-                                        int H, int k, void* grad_x, float* grad_w,
-                                        int32_t* error_flag, hipStream_t stream) {
-    if (T == 0) return hipSuccess;
-    if (!grid_fits(T, kT)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(unpermute_kernel, dim3(static_cast<unsigned>(T)), dim3(kT), 0, stream,
-                       static_cast<const u32x4*>(grad_rows), num_rows,
-                       static_cast<const float*>(nullptr), expert_slot, H / 8, k,
-                       static_cast<const u32x4*>(nullptr), static_cast<u32x4*>(grad_x),
-                       grad_perm_w, grad_w, error_flag);
-    return hipGetLastError();
+    const int V = H / 8;
+    const FastDiv fd = FastDiv::make(k);
+    // one pass over the pairs; the first pass, if there are two, only reads rows
+    const auto pass = [&](auto dot, auto write, auto policy) {
+        constexpr bool d = decltype(dot)::value, r = decltype(write)::value;
+        constexpr int p = decltype(policy)::value;
+        return by_token_range(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
+            with_row_width<7, false>(V, [&](auto wpl, auto) {
+                hipLaunchKernelGGL((unpermute_grad_kernel<decltype(wpl)::value, d, r, p>),
+                                   dim3(grid), dim3(kT), 0, stream,
+                                   static_cast<const u32x4*>(grad_out),
+                                   static_cast<const u32x4*>(rows), num_rows, topk_w, expert_slot,
+                                   t0, t_end, V, k, fd, static_cast<u32x4*>(grad_rows), grad_w,
+                                   error_flag);
+            });
+        });
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    using Nt = std::integral_constant<int, kPolicyNt>;
+    using Cached = std::integral_constant<int, 0>;
+    if (grad_w && T * k * V * 16 <= kOneLaunchBytes) return pass(Yes{}, Yes{}, Cached{});
+    if (grad_w) {
+        const hipError_t e = pass(Yes{}, No{}, Nt{});
+        if (e != hipSuccess) return e;
+    }
+    return pass(No{}, Yes{}, Nt{});
 }
 
 }  // namespace ep

@@ -9,6 +9,8 @@
 //   grad_y n. The two row sums, of h^2 and of g h, come from one pass: mean(g n) n r =
 //   h r^3 mean(g h).
 // Everything between the inputs and the outputs is fp32; each output is rounded once.
+#include <type_traits>
+
 #include "expert_ops.hpp"
 
 namespace ep {
@@ -62,8 +64,8 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int H, float eps) {
 // One block per token, the row read twice (the second time from the L2).
 template <bool kF32>
 __global__ __launch_bounds__(kNT) void rmsnorm_kernel(const u32x4* x, const u32x4* residual,
-                                                      const void* weight, float eps, int V,
-                                                      u32x4* residual_out, u32x4* y,
+                                                      const void* weight, float eps, int64_t T,
+                                                      int V, u32x4* residual_out, u32x4* y,
                                                       u32x2* y_fp8, float* y_scales) {
     __shared__ float red[kNWaves];
     const int64_t base = static_cast<int64_t>(blockIdx.x) * V;
@@ -102,6 +104,140 @@ __global__ __launch_bounds__(kNT) void rmsnorm_kernel(const u32x4* x, const u32x
             }
             y_fp8[base + v] = c;
             if (v % 16 == 0) y_scales[(base + v) / 16] = a / kE4m3Max;
+        }
+    }
+}
+
+#ifndef EP_NF_NV
+#define EP_NF_NV 2
+#endif
+#ifndef EP_NF_PAIR
+#define EP_NF_PAIR 0
+#endif
+#ifndef EP_NF_LP
+#define EP_NF_LP 0
+#endif
+#ifndef EP_NF_SP
+#define EP_NF_SP 0
+#endif
+
+constexpr int kMaxWaves = 16;  // per block
+
+// Sums of kN values over the W waves of a row, in every thread; red: one slot per wave.
+// The caller alternates between two such arrays, so one barrier per call is enough.
+template <int kN>
+__device__ __forceinline__ void waves_sum(float (&s)[kN], float (*red)[kN], int first, int W) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) s[n] = wave_sum(s[n]);
+    const int wave = threadIdx.x / kWave;
+    if (lane_id() == 0) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) red[wave][n] = s[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kN; ++n) s[n] = 0.0f;
+    for (int i = 0; i < W; ++i) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) s[n] += red[first + i][n];
+    }
+}
+
+// The weights of word v, zeros past the row.
+template <bool kF32>
+__device__ __forceinline__ void weight_word(__amdgpu_buffer_rsrc_t wb, int v, float (&f)[8]) {
+    if constexpr (kF32) {
+        const u32x4 a = load_word<0>(wb, 2 * v), b = load_word<0>(wb, 2 * v + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = __uint_as_float(a[i]);
+            f[4 + i] = __uint_as_float(b[i]);
+        }
+    } else {
+        widen8(load_word<0>(wb, v), f);
+    }
+}
+
+// The row in registers: NV words per lane, one row per wave (kOneWave: four rows per block of
+// 256) or per block.
+template <int NV, bool kF32, bool kOneWave>
+__global__ __launch_bounds__(kOneWave ? kNT : kMaxWaves * kWave) void rmsnorm_row_kernel(
+    const u32x4* x, const u32x4* residual, const void* weight, float eps, int64_t T, int V,
+    u32x4* residual_out, u32x4* y, u32x2* y_fp8, float* y_scales) {
+    __shared__ float red[kMaxWaves][1];
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+    const int64_t t = kOneWave ? static_cast<int64_t>(blockIdx.x) * kNWaves + wave : blockIdx.x;
+    if (kOneWave && t >= T) return;
+    const int tid = kOneWave ? lane_id() : threadIdx.x;
+    const int threads = kOneWave ? kWave : blockDim.x;
+    const auto word = [&](int i) {
+        return EP_NF_PAIR && NV > 1 ? 2 * (tid + (i / 2) * threads) + (i & 1) : tid + i * threads;
+    };
+    const __amdgpu_buffer_rsrc_t xb = row_buffer(x, t, V), rb = row_buffer(residual, t, V);
+    u32x4 xv[NV], rv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) xv[i] = load_word<EP_NF_LP>(xb, word(i));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) rv[i] = load_word<EP_NF_LP>(rb, word(i));
+    const __amdgpu_buffer_rsrc_t wb =
+        raw_buffer(weight, static_cast<uint32_t>(V) * (kF32 ? 32u : 16u));
+    float w[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) weight_word<kF32>(wb, word(i), w[i]);
+    float f[NV][8], ss[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float r[8];
+        widen8(xv[i], f[i]);
+        widen8(rv[i], r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[i][e] += r[e];
+            ss[0] += f[i][e] * f[i][e];
+        }
+    }
+    if constexpr (kOneWave) ss[0] = wave_sum(ss[0]);
+    else waves_sum<1>(ss, red, 0, blockDim.x / kWave);
+    const float r = inv_rms(ss[0], 8 * V, eps);
+    const __amdgpu_buffer_rsrc_t sb = row_buffer(residual_out, t, V), yb = row_buffer(y, t, V);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (residual_out) store_word<EP_NF_SP>(sb, word(i), narrow8(f[i]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * r * w[i][e];
+        if (y) store_word<EP_NF_SP>(yb, word(i), narrow8(f[i]));
+    }
+    if (y_fp8) {
+        const int64_t G = V / 16;
+        const __amdgpu_buffer_rsrc_t cb = raw_buffer(y_fp8 + t * V, static_cast<uint32_t>(V) * 8u);
+        const __amdgpu_buffer_rsrc_t gb = raw_buffer(y_scales + t * G, static_cast<uint32_t>(G) * 4u);
+        constexpr int kStep = EP_NF_PAIR && NV > 1 ? 2 : 1;
+#pragma unroll
+        for (int i = 0; i < NV; i += kStep) {
+            float a = 0.0f;
+#pragma unroll
+            for (int h = 0; h < kStep; ++h)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[i + h][e]));
+            a = kStep == 2 ? half_row_max(a) : row_max(a);
+            a = a > 0.0f ? fmaxf(a, kTinyAmax) : kE4m3Max;
+            const float inv = kE4m3Max / a;
+            uint32_t c[2 * kStep];
+#pragma unroll
+            for (int q = 0; q < 2 * kStep; ++q) {
+                const float* p = &f[i + q / 2][4 * (q & 1)];
+                const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(p[0] * inv, p[1] * inv, 0, false);
+                c[q] = static_cast<uint32_t>(
+                    __builtin_amdgcn_cvt_pk_fp8_f32(p[2] * inv, p[3] * inv, lo, true));
+            }
+            if constexpr (kStep == 2) {
+                store_word<EP_NF_SP>(cb, word(i) / 2, u32x4{c[0], c[1], c[2], c[3]});
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, cb, word(i) * 8, 0, EP_NF_SP);
+            }
+            if (word(i) % 16 == 0)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a / kE4m3Max), gb,
+                                                      word(i) / 16 * 4, 0, 0);
         }
     }
 }
@@ -201,6 +337,163 @@ __global__ __launch_bounds__(kNT) void rmsnorm_dx_kernel(const u32x4* dy, const 
     }
 }
 
+#ifndef EP_NG_B
+#define EP_NG_B 256
+#endif
+#ifndef EP_NG_LP
+#define EP_NG_LP 2
+#endif
+#ifndef EP_NG_SP
+#define EP_NG_SP 2
+#endif
+#ifndef EP_NG_NV
+#define EP_NG_NV 1
+#endif
+
+// The gradient with the rows in registers: a block holds G rows at a time, W waves and NV
+// words per lane for each, and walks rows G apart; the next rows' loads are in flight
+// while the present ones are reduced and written. Each lane keeps the sum of its words'
+// grad_w over the block's rows in registers; at the end the G rows' sums join in LDS and the
+// block writes one partial row of grad_w (part [gridDim.x][8 V]).
+template <int NV>
+struct GradRow {
+    u32x4 dy[NV], h[NV], dr[NV];
+
+    __device__ __forceinline__ void load(const u32x4* grad_y, const u32x4* hh, const u32x4* grad_res,
+                                         int64_t t, bool live, int V, int v, int step) {
+        const __amdgpu_buffer_rsrc_t a = row_buffer(live ? grad_y : nullptr, t, V);
+        const __amdgpu_buffer_rsrc_t b = row_buffer(live ? hh : nullptr, t, V);
+        const __amdgpu_buffer_rsrc_t c = row_buffer(live ? grad_res : nullptr, t, V);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) dy[i] = load_word<EP_NG_LP>(a, v + i * step);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) h[i] = load_word<EP_NG_LP>(b, v + i * step);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) dr[i] = load_word<EP_NG_LP>(c, v + i * step);
+    }
+};
+
+template <int NV, bool kF32, bool kDw>
+__global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
+    const u32x4* grad_y, const u32x4* grad_res, const u32x4* h, const void* weight, float eps,
+    int64_t T, int V, int W, u32x4* grad_x, float* part) {
+    __shared__ float red[2][kMaxWaves][2];
+    __shared__ float join[kDw && NV == 1 ? kMaxWaves * kWave * 8 : 1];
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+    const int G = static_cast<int>(blockDim.x) / (kWave * W);
+    const int g = wave / W;
+    const int v = (wave - g * W) * kWave + lane_id();
+    const int step = W * kWave;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * G;
+    const __amdgpu_buffer_rsrc_t wb =
+        raw_buffer(weight, static_cast<uint32_t>(V) * (kF32 ? 32u : 16u));
+    float w[NV][8], dw[NV][8] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) weight_word<kF32>(wb, v + i * step, w[i]);
+    int64_t t0 = static_cast<int64_t>(blockIdx.x) * G;
+    GradRow<NV> cur;
+    cur.load(grad_y, h, grad_res, t0 + g, t0 + g < T, V, v, step);
+    for (int par = 0; t0 < T; t0 += stride, par ^= 1) {
+        const int64_t t = t0 + g, tn = t + stride;
+        GradRow<NV> next;
+        next.load(grad_y, h, grad_res, tn, tn < T, V, v, step);
+        float f[NV][8], y[NV][8], s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            widen8(cur.h[i], f[i]);
+            widen8(cur.dy[i], y[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s[0] += f[i][e] * f[i][e];
+                s[1] += y[i][e] * w[i][e] * f[i][e];
+            }
+        }
+        waves_sum<2>(s, red[par], g * W, W);
+        const float r = inv_rms(s[0], 8 * V, eps);
+        const float c = s[1] / static_cast<float>(8 * V) * r * r;
+        const __amdgpu_buffer_rsrc_t xb = row_buffer(t < T ? grad_x : nullptr, t, V);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float d[8];
+            widen8(cur.dr[i], d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                d[e] += r * (y[i][e] * w[i][e] - f[i][e] * c);
+                if (kDw && t < T) dw[i][e] += y[i][e] * (f[i][e] * r);
+            }
+            store_word<EP_NG_SP>(xb, v + i * step, narrow8(d));
+        }
+        cur = next;
+    }
+    if constexpr (kDw) {
+        float* out = part + static_cast<int64_t>(blockIdx.x) * V * 8;
+        if (G == 1) {
+            const __amdgpu_buffer_rsrc_t ob = raw_buffer(out, static_cast<uint32_t>(V) * 32u);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    u32x4 o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(dw[i][4 * q + e]);
+                    store_word<0>(ob, 2 * (v + i * step) + q, o);
+                }
+            }
+        } else if constexpr (NV == 1) {
+            const int row = step * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) join[g * row + v * 8 + e] = dw[0][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < V * 8; c += blockDim.x) {
+                float s = 0.0f;
+                for (int i = 0; i < G; ++i) s += join[i * row + c];
+                out[c] = s;
+            }
+        }
+    }
+}
+
+// grad_w = the blocks' partial rows: block b takes 64 columns, its waves every sixteenth row
+// each, joined in wave order.
+__global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_dw_sum_kernel(const float* part, int H,
+                                                                          int rows, float* dw) {
+    __shared__ float acc[kMaxWaves][kWave];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int c = static_cast<int>(blockIdx.x) * kWave + lane;
+    float s = 0.0f;
+    if (c < H) {
+#pragma unroll 8
+        for (int p = wave; p < rows; p += kMaxWaves) s += part[static_cast<int64_t>(p) * H + c];
+    }
+    acc[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < H) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kMaxWaves; ++i) s += acc[i][lane];
+        dw[c] = s;
+    }
+}
+
+// Launch shape of the gradient with rows in registers; W == 0 for rows wider than that.
+struct GradShape {
+    int nv, W, G;
+    int64_t blocks;  // with grad_w
+};
+
+GradShape grad_shape(int64_t T, int V) {
+    GradShape s{};
+    const int words = (V + kWave - 1) / kWave;
+    if (words <= EP_NG_NV * kMaxWaves && words > kMaxWaves / 2) s.nv = EP_NG_NV;
+    else if (words <= kMaxWaves) s.nv = 1;
+    else if (words <= 2 * kMaxWaves) s.nv = 2;
+    else return s;
+    s.W = (words + s.nv - 1) / s.nv;
+    s.G = s.nv == 1 ? kMaxWaves / s.W : 1;
+    s.blocks = std::min<int64_t>(EP_NG_B, (T + s.G - 1) / s.G);
+    return s;
+}
+
 constexpr int kDwChunks = 64;  // partial rows of grad_w
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -211,19 +504,71 @@ hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weigh
                           bool weight_fp32, float eps, int64_t T, int H, void* residual_out,
                           void* y, uint8_t* y_fp8, float* y_scales, hipStream_t stream) {
     if (T == 0) return hipSuccess;
-    if (!grid_fits(T, kNT)) return hipErrorInvalidConfiguration;
-    const auto kernel = weight_fp32 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(T)), dim3(kNT), 0, stream,
-                       static_cast<const u32x4*>(x), static_cast<const u32x4*>(residual), weight,
-                       eps, H / 8, static_cast<u32x4*>(residual_out), static_cast<u32x4*>(y),
-                       reinterpret_cast<u32x2*>(y_fp8), y_scales);
-    return hipGetLastError();
+    const int V = H / 8;
+    const auto launch = [&](auto kernel, int64_t grid, int threads) {
+        if (!grid_fits(grid, threads)) return hipErrorInvalidConfiguration;
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, stream,
+                           static_cast<const u32x4*>(x), static_cast<const u32x4*>(residual),
+                           weight, eps, T, V, static_cast<u32x4*>(residual_out),
+                           static_cast<u32x4*>(y), reinterpret_cast<u32x2*>(y_fp8), y_scales);
+        return hipGetLastError();
+    };
+    const auto row = [&](auto nv, auto one_wave) {
+        constexpr int n = decltype(nv)::value;
+        constexpr bool one = decltype(one_wave)::value;
+        const int threads = one ? kNT : kWave * ((V + kWave * n - 1) / (kWave * n));
+        return launch(weight_fp32 ? rmsnorm_row_kernel<n, true, one>
+                                  : rmsnorm_row_kernel<n, false, one>,
+                      one ? (T + kNWaves - 1) / kNWaves : T, threads);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Four = std::integral_constant<int, 4>;
+    if (V <= kWave) return row(One{}, std::true_type{});
+    if (V <= 2 * kWave) return row(Two{}, std::true_type{});
+    if (V <= 4 * kWave) return row(Four{}, std::true_type{});
+    if (V <= EP_NF_NV * kMaxWaves * kWave) return row(std::integral_constant<int, EP_NF_NV>{}, std::false_type{});
+    if (V <= 2 * kMaxWaves * kWave) return row(Two{}, std::false_type{});
+    if (V <= 4 * kMaxWaves * kWave) return row(Four{}, std::false_type{});
+    return launch(weight_fp32 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>, T, kNT);
 }
 
 size_t rmsnorm_grad_workspace_bytes(int64_t T, int H) {
     if (T == 0) return 0;
+    const GradShape s = grad_shape(T, H / 8);
+    if (s.W) return sizeof(float) * static_cast<size_t>(s.blocks) * static_cast<size_t>(H);
     return align256(sizeof(float) * static_cast<size_t>(T)) +
            sizeof(float) * static_cast<size_t>(kDwChunks) * static_cast<size_t>(H);
+}
+
+// Rows wider than the registers hold: every row is read from memory as often as it is used.
+static hipError_t launch_wide_grad(const u32x4* dy, const u32x4* dres, const u32x4* h,
+                                   const void* weight, bool weight_fp32, float eps, int64_t T,
+                                   int H, u32x4* grad_x, float* grad_weight, void* workspace,
+                                   hipStream_t stream) {
+    if (!grid_fits(T, kNT)) return hipErrorInvalidConfiguration;
+    const int V = H / 8;
+    const unsigned grid = static_cast<unsigned>(T);
+    if (grad_weight) {  // before grad_x, which may take the place of any of its inputs
+        float* rstd = static_cast<float*>(workspace);
+        float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                               align256(sizeof(float) * static_cast<size_t>(T)));
+        const int64_t rows = (T + kDwChunks - 1) / kDwChunks;
+        const int chunks = static_cast<int>((T + rows - 1) / rows);
+        hipLaunchKernelGGL(rmsnorm_rstd_kernel, dim3(grid), dim3(kNT), 0, stream, h, eps, V, rstd);
+        EP_RETURN_IF_LAUNCH_FAILED();
+        hipLaunchKernelGGL(rmsnorm_dw_kernel,
+                           dim3((V + kWave - 1) / kWave, static_cast<unsigned>(chunks)), dim3(kNT),
+                           0, stream, dy, h, rstd, T, V, rows, part);
+        EP_RETURN_IF_LAUNCH_FAILED();
+        hipLaunchKernelGGL(rmsnorm_dw_join_kernel, dim3((H + kNT - 1) / kNT), dim3(kNT), 0, stream,
+                           part, H, chunks, grad_weight);
+        EP_RETURN_IF_LAUNCH_FAILED();
+    }
+    const auto kernel = weight_fp32 ? rmsnorm_dx_kernel<true> : rmsnorm_dx_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kNT), 0, stream, dy, dres, h, weight, eps, V,
+                       grad_x);
+    return hipGetLastError();
 }
 
 hipError_t launch_rmsnorm_grad(const void* grad_y, const void* grad_residual_out, const void* h,
@@ -234,31 +579,37 @@ hipError_t launch_rmsnorm_grad(const void* grad_y, const void* grad_residual_out
         if (!grad_weight) return hipSuccess;
         return launch_zero_ints(ZeroInts{{reinterpret_cast<int32_t*>(grad_weight)}, {H}}, stream);
     }
-    if (!grid_fits(T, kNT)) return hipErrorInvalidConfiguration;
     const int V = H / 8;
     const auto* dy = static_cast<const u32x4*>(grad_y);
+    const auto* dres = static_cast<const u32x4*>(grad_residual_out);
     const auto* hp = static_cast<const u32x4*>(h);
-    const unsigned grid = static_cast<unsigned>(T);
-    if (grad_weight) {  // before grad_x, which may take the place of any of its inputs
-        float* rstd = static_cast<float*>(workspace);
-        float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                               align256(sizeof(float) * static_cast<size_t>(T)));
-        const int64_t rows = (T + kDwChunks - 1) / kDwChunks;
-        const int chunks = static_cast<int>((T + rows - 1) / rows);
-        hipLaunchKernelGGL(rmsnorm_rstd_kernel, dim3(grid), dim3(kNT), 0, stream, hp, eps, V, rstd);
-        EP_RETURN_IF_LAUNCH_FAILED();
-        hipLaunchKernelGGL(rmsnorm_dw_kernel,
-                           dim3((V + kWave - 1) / kWave, static_cast<unsigned>(chunks)), dim3(kNT),
-                           0, stream, dy, hp, rstd, T, V, rows, part);
-        EP_RETURN_IF_LAUNCH_FAILED();
-        hipLaunchKernelGGL(rmsnorm_dw_join_kernel, dim3((H + kNT - 1) / kNT), dim3(kNT), 0, stream,
-                           part, H, chunks, grad_weight);
-        EP_RETURN_IF_LAUNCH_FAILED();
-    }
-    const auto kernel = weight_fp32 ? rmsnorm_dx_kernel<true> : rmsnorm_dx_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kNT), 0, stream, dy,
-                       static_cast<const u32x4*>(grad_residual_out), hp, weight, eps, V,
-                       static_cast<u32x4*>(grad_x));
+    auto* dx = static_cast<u32x4*>(grad_x);
+    const GradShape s = grad_shape(T, V);
+    if (!s.W)
+        return launch_wide_grad(dy, dres, hp, weight, weight_fp32, eps, T, H, dx, grad_weight,
+                                workspace, stream);
+    // without grad_w nothing ties a block to many rows
+    const int64_t grid = grad_weight ? s.blocks : std::min<int64_t>((T + s.G - 1) / s.G, 1 << 16);
+    // a single block's partial row is the sum (it leaves in 128-bit words)
+    const bool direct = s.blocks == 1 && reinterpret_cast<uintptr_t>(grad_weight) % 16 == 0;
+    float* part = direct ? grad_weight : static_cast<float*>(workspace);
+    const auto launch = [&](auto nv) {
+        constexpr int n = decltype(nv)::value;
+        const auto kernel =
+            weight_fp32 ? (grad_weight ? rmsnorm_grad_row_kernel<n, true, true>
+                                       : rmsnorm_grad_row_kernel<n, true, false>)
+                        : (grad_weight ? rmsnorm_grad_row_kernel<n, false, true>
+                                       : rmsnorm_grad_row_kernel<n, false, false>);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(kWave * s.W * s.G), 0,
+                           stream, dy, dres, hp, weight, eps, T, V, s.W, dx, part);
+        return hipGetLastError();
+    };
+    const hipError_t e = s.nv == 1 ? launch(std::integral_constant<int, 1>{})
+                                   : launch(std::integral_constant<int, 2>{});
+    if (e != hipSuccess || !grad_weight || direct) return e;
+    hipLaunchKernelGGL(rmsnorm_dw_sum_kernel, dim3((H + kWave - 1) / kWave),
+                       dim3(kMaxWaves * kWave), 0, stream, part, H, static_cast<int>(s.blocks),
+                       grad_weight);
     return hipGetLastError();
 }
 
