@@ -62,14 +62,6 @@ __device__ __forceinline__ float row_max(float v) {
     return fmaxf(v, dpp_or_zero<0x121>(v));
 }
 
-// Largest of 8 aligned lanes, in each of them: neighbours, pairs, then the halves mirrored.
-// v >= 0.
-__device__ __forceinline__ float half_row_max(float v) {
-    v = fmaxf(v, dpp_or_zero<0xb1>(v));   // quad_perm 1 0 3 2
-    v = fmaxf(v, dpp_or_zero<0x4e>(v));   // quad_perm 2 3 0 1
-    return fmaxf(v, dpp_or_zero<0x141>(v));  // row_half_mirror
-}
-
 // Word v (16 bytes) of a buffer; zeros past its end.
 template <int kPolicy>
 __device__ __forceinline__ u32x4 load_word(__amdgpu_buffer_rsrc_t b, int v) {

@@ -61,7 +61,28 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int H, float eps) {
     return 1.0f / sqrtf(sum_sq / static_cast<float>(H) + eps);
 }
 
-// One block per token, the row read twice (the second time from the L2).
+// The e4m3 codes of a lane's 8 channels, and the magnitude that its group of 128 channels (16
+// aligned lanes, all inside the row or all past it) is scaled to 448 by: the largest of the
+// group's numbers (a NaN is none, and keeps its NaN code), at least 2^-100, or 448 for a group
+// of zeros. No clamp: the largest product is 448 within 2 u, which rounds to 448.
+__device__ __forceinline__ float quantize8(const float (&f)[8], u32x2& code) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
+    a = row_max(a);
+    a = a > 0.0f ? fmaxf(a, kTinyAmax) : kE4m3Max;
+    const float inv = kE4m3Max / a;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * q] * inv, f[4 * q + 1] * inv, 0, false);
+        code[q] = static_cast<uint32_t>(
+            __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * q + 2] * inv, f[4 * q + 3] * inv, lo, true));
+    }
+    return a;
+}
+
+// Rows wider than the registers hold (past 32768 channels): one block per token, the row read
+// twice, the second time from the L2.
 template <bool kF32>
 __global__ __launch_bounds__(kNT) void rmsnorm_kernel(const u32x4* x, const u32x4* residual,
                                                       const void* weight, float eps, int64_t T,
@@ -86,40 +107,14 @@ __global__ __launch_bounds__(kNT) void rmsnorm_kernel(const u32x4* x, const u32x
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
         if (y) y[base + v] = narrow8(f);
-        if (y_fp8) {  // a group is 16 aligned lanes, all inside the row or all past it
-            float a = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
-#pragma unroll
-            for (int m = 8; m >= 1; m >>= 1) a = fmaxf(a, __shfl_xor(a, m, kWave));
-            a = a > 0.0f ? fmaxf(a, kTinyAmax) : kE4m3Max;
-            const float inv = kE4m3Max / a;
+        if (y_fp8) {
             u32x2 c;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * q] * inv, f[4 * q + 1] * inv,
-                                                               0, false);
-                c[q] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(
-                    f[4 * q + 2] * inv, f[4 * q + 3] * inv, lo, true));
-            }
+            const float a = quantize8(f, c);
             y_fp8[base + v] = c;
             if (v % 16 == 0) y_scales[(base + v) / 16] = a / kE4m3Max;
         }
     }
 }
-
-#ifndef EP_NF_NV
-#define EP_NF_NV 2
-#endif
-#ifndef EP_NF_PAIR
-#define EP_NF_PAIR 0
-#endif
-#ifndef EP_NF_LP
-#define EP_NF_LP 0
-#endif
-#ifndef EP_NF_SP
-#define EP_NF_SP 0
-#endif
 
 constexpr int kMaxWaves = 16;  // per block
 
@@ -159,8 +154,16 @@ __device__ __forceinline__ void weight_word(__amdgpu_buffer_rsrc_t wb, int v, fl
 }
 
 // The row in registers: NV words per lane, one row per wave (kOneWave: four rows per block of
-// 256) or per block.
-template <int NV, bool kF32, bool kOneWave>
+// 256) or one per block. Everything is read once and written once; bound by those bytes.
+// A missing residual or output is a buffer of no bytes. kPolicy: the cache policy of the
+// rows' loads and stores.
+//
+// Measured on MI355X at 7168 channels with residual, bf16 and e4m3 outputs: 46.7 us at 4096
+// tokens, 178.5 us at 16384 (5.9 TB/s), 4.0 us for one token. Two words per lane and 448
+// threads; one word 50.6 and 190 us, four 50.7 and 188 us (cached accesses, where two took
+// 49.3 and 184). Two neighbouring words per lane, for 128-bit code stores, 58.0 and 213 us:
+// their loads and stores of the bf16 rows leave every other 16 bytes to a second access.
+template <int NV, bool kF32, bool kOneWave, int kPolicy>
 __global__ __launch_bounds__(kOneWave ? kNT : kMaxWaves * kWave) void rmsnorm_row_kernel(
     const u32x4* x, const u32x4* residual, const void* weight, float eps, int64_t T, int V,
     u32x4* residual_out, u32x4* y, u32x2* y_fp8, float* y_scales) {
@@ -168,22 +171,19 @@ __global__ __launch_bounds__(kOneWave ? kNT : kMaxWaves * kWave) void rmsnorm_ro
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const int64_t t = kOneWave ? static_cast<int64_t>(blockIdx.x) * kNWaves + wave : blockIdx.x;
     if (kOneWave && t >= T) return;
-    const int tid = kOneWave ? lane_id() : threadIdx.x;
-    const int threads = kOneWave ? kWave : blockDim.x;
-    const auto word = [&](int i) {
-        return EP_NF_PAIR && NV > 1 ? 2 * (tid + (i / 2) * threads) + (i & 1) : tid + i * threads;
-    };
+    const int v = kOneWave ? lane_id() : threadIdx.x;
+    const int step = kOneWave ? kWave : blockDim.x;
     const __amdgpu_buffer_rsrc_t xb = row_buffer(x, t, V), rb = row_buffer(residual, t, V);
     u32x4 xv[NV], rv[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) xv[i] = load_word<EP_NF_LP>(xb, word(i));
+    for (int i = 0; i < NV; ++i) xv[i] = load_word<kPolicy>(xb, v + i * step);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) rv[i] = load_word<EP_NF_LP>(rb, word(i));
+    for (int i = 0; i < NV; ++i) rv[i] = load_word<kPolicy>(rb, v + i * step);
     const __amdgpu_buffer_rsrc_t wb =
         raw_buffer(weight, static_cast<uint32_t>(V) * (kF32 ? 32u : 16u));
     float w[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) weight_word<kF32>(wb, word(i), w[i]);
+    for (int i = 0; i < NV; ++i) weight_word<kF32>(wb, v + i * step, w[i]);
     float f[NV][8], ss[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -202,45 +202,30 @@ __global__ __launch_bounds__(kOneWave ? kNT : kMaxWaves * kWave) void rmsnorm_ro
     const __amdgpu_buffer_rsrc_t sb = row_buffer(residual_out, t, V), yb = row_buffer(y, t, V);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (residual_out) store_word<EP_NF_SP>(sb, word(i), narrow8(f[i]));
+        if (residual_out) store_word<kPolicy>(sb, v + i * step, narrow8(f[i]));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * r * w[i][e];
-        if (y) store_word<EP_NF_SP>(yb, word(i), narrow8(f[i]));
+        if (y) store_word<kPolicy>(yb, v + i * step, narrow8(f[i]));
     }
-    if (y_fp8) {
-        const int64_t G = V / 16;
-        const __amdgpu_buffer_rsrc_t cb = raw_buffer(y_fp8 + t * V, static_cast<uint32_t>(V) * 8u);
-        const __amdgpu_buffer_rsrc_t gb = raw_buffer(y_scales + t * G, static_cast<uint32_t>(G) * 4u);
-        constexpr int kStep = EP_NF_PAIR && NV > 1 ? 2 : 1;
+    if (!y_fp8) return;
+    const int64_t G = V / 16;
+    const __amdgpu_buffer_rsrc_t cb = raw_buffer(y_fp8 + t * V, static_cast<uint32_t>(V) * 8u);
+    const __amdgpu_buffer_rsrc_t gb = raw_buffer(y_scales + t * G, static_cast<uint32_t>(G) * 4u);
 #pragma unroll
-        for (int i = 0; i < NV; i += kStep) {
-            float a = 0.0f;
-#pragma unroll
-            for (int h = 0; h < kStep; ++h)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[i + h][e]));
-            a = kStep == 2 ? half_row_max(a) : row_max(a);
-            a = a > 0.0f ? fmaxf(a, kTinyAmax) : kE4m3Max;
-            const float inv = kE4m3Max / a;
-            uint32_t c[2 * kStep];
-#pragma unroll
-            for (int q = 0; q < 2 * kStep; ++q) {
-                const float* p = &f[i + q / 2][4 * (q & 1)];
-                const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(p[0] * inv, p[1] * inv, 0, false);
-                c[q] = static_cast<uint32_t>(
-                    __builtin_amdgcn_cvt_pk_fp8_f32(p[2] * inv, p[3] * inv, lo, true));
-            }
-            if constexpr (kStep == 2) {
-                store_word<EP_NF_SP>(cb, word(i) / 2, u32x4{c[0], c[1], c[2], c[3]});
-            } else {
-                __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, cb, word(i) * 8, 0, EP_NF_SP);
-            }
-            if (word(i) % 16 == 0)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a / kE4m3Max), gb,
-                                                      word(i) / 16 * 4, 0, 0);
-        }
+    for (int i = 0; i < NV; ++i) {  // a group is a row of 16 lanes
+        const int vi = v + i * step;
+        u32x2 c;
+        const float a = quantize8(f[i], c);
+        __builtin_amdgcn_raw_buffer_store_b64(c, cb, vi * 8, 0, kPolicy);
+        if (vi % 16 == 0)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a / kE4m3Max), gb, vi / 16 * 4, 0, 0);
     }
 }
+
+// From this many bytes of x on, the rows' loads and stores are non-temporal. Measured at 7168
+// channels with all outputs, cached against non-temporal: 11.1 against 12.9 us at 1024 tokens
+// (15 MB), 28.1 against 25.4 us at 2048 (29 MB), 49.5 against 46.7 us at 4096 (59 MB).
+constexpr int64_t kNormStreamBytes = int64_t{24} << 20;
 
 // ---- gradient
 
@@ -337,25 +322,15 @@ __global__ __launch_bounds__(kNT) void rmsnorm_dx_kernel(const u32x4* dy, const 
     }
 }
 
-#ifndef EP_NG_B
-#define EP_NG_B 256
-#endif
-#ifndef EP_NG_LP
-#define EP_NG_LP 2
-#endif
-#ifndef EP_NG_SP
-#define EP_NG_SP 2
-#endif
-#ifndef EP_NG_NV
-#define EP_NG_NV 1
-#endif
+// The same word, unknown to the compiler: what was computed from it before is computed again
+// instead of being kept in registers.
+__device__ __forceinline__ u32x4 anew(u32x4 w) {
+    asm volatile("" : "+v"(w));
+    return w;
+}
 
-// The gradient with the rows in registers: a block holds G rows at a time, W waves and NV
-// words per lane for each, and walks rows G apart; the next rows' loads are in flight
-// while the present ones are reduced and written. Each lane keeps the sum of its words'
-// grad_w over the block's rows in registers; at the end the G rows' sums join in LDS and the
-// block writes one partial row of grad_w (part [gridDim.x][8 V]).
-template <int NV>
+// One row's words of a lane; zeros where there is no row.
+template <int NV, int kPolicy>
 struct GradRow {
     u32x4 dy[NV], h[NV], dr[NV];
 
@@ -365,20 +340,25 @@ struct GradRow {
         const __amdgpu_buffer_rsrc_t b = row_buffer(live ? hh : nullptr, t, V);
         const __amdgpu_buffer_rsrc_t c = row_buffer(live ? grad_res : nullptr, t, V);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) dy[i] = load_word<EP_NG_LP>(a, v + i * step);
+        for (int i = 0; i < NV; ++i) dy[i] = load_word<kPolicy>(a, v + i * step);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) h[i] = load_word<EP_NG_LP>(b, v + i * step);
+        for (int i = 0; i < NV; ++i) h[i] = load_word<kPolicy>(b, v + i * step);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) dr[i] = load_word<EP_NG_LP>(c, v + i * step);
+        for (int i = 0; i < NV; ++i) dr[i] = load_word<kPolicy>(c, v + i * step);
     }
 };
 
-template <int NV, bool kF32, bool kDw>
+// The gradient with the rows in registers: a block holds G rows at a time, W waves and NV
+// words per lane for each, and walks rows G apart; the next rows' loads are in flight
+// while the present ones are reduced and written. Each lane keeps the sum of its words'
+// grad_w over the block's rows in registers; at the end the G rows' sums join in LDS and the
+// block writes one partial row of grad_w (part [gridDim.x][8 V]).
+template <int NV, bool kF32, bool kDw, int kPolicy>
 __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
     const u32x4* grad_y, const u32x4* grad_res, const u32x4* h, const void* weight, float eps,
     int64_t T, int V, int W, u32x4* grad_x, float* part) {
     __shared__ float red[2][kMaxWaves][2];
-    __shared__ float join[kDw && NV == 1 ? kMaxWaves * kWave * 8 : 1];
+    __shared__ float join[kDw ? kMaxWaves * kWave * NV * 8 : 1];
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const int G = static_cast<int>(blockDim.x) / (kWave * W);
     const int g = wave / W;
@@ -391,21 +371,22 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) weight_word<kF32>(wb, v + i * step, w[i]);
     int64_t t0 = static_cast<int64_t>(blockIdx.x) * G;
-    GradRow<NV> cur;
+    GradRow<NV, kPolicy> cur;
     cur.load(grad_y, h, grad_res, t0 + g, t0 + g < T, V, v, step);
     for (int par = 0; t0 < T; t0 += stride, par ^= 1) {
         const int64_t t = t0 + g, tn = t + stride;
-        GradRow<NV> next;
+        GradRow<NV, kPolicy> next;
         next.load(grad_y, h, grad_res, tn, tn < T, V, v, step);
-        float f[NV][8], y[NV][8], s[2] = {0.0f, 0.0f};
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            widen8(cur.h[i], f[i]);
-            widen8(cur.dy[i], y[i]);
+            float f[8], y[8];
+            widen8(cur.h[i], f);
+            widen8(cur.dy[i], y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                s[0] += f[i][e] * f[i][e];
-                s[1] += y[i][e] * w[i][e] * f[i][e];
+                s[0] += f[e] * f[e];
+                s[1] += y[e] * w[i][e] * f[e];
             }
         }
         waves_sum<2>(s, red[par], g * W, W);
@@ -414,14 +395,16 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
         const __amdgpu_buffer_rsrc_t xb = row_buffer(t < T ? grad_x : nullptr, t, V);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float d[8];
+            float d[8], f[8], y[8];
             widen8(cur.dr[i], d);
+            widen8(anew(cur.h[i]), f);
+            widen8(anew(cur.dy[i]), y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                d[e] += r * (y[i][e] * w[i][e] - f[i][e] * c);
-                if (kDw && t < T) dw[i][e] += y[i][e] * (f[i][e] * r);
+                d[e] += r * (y[e] * w[i][e] - f[e] * c);
+                if (kDw && t < T) dw[i][e] += y[e] * (f[e] * r);
             }
-            store_word<EP_NG_SP>(xb, v + i * step, narrow8(d));
+            store_word<kPolicyNt>(xb, v + i * step, narrow8(d));
         }
         cur = next;
     }
@@ -439,10 +422,12 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
                     store_word<0>(ob, 2 * (v + i * step) + q, o);
                 }
             }
-        } else if constexpr (NV == 1) {
-            const int row = step * 8;
+        } else {
+            const int row = step * NV * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) join[g * row + v * 8 + e] = dw[0][e];
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) join[g * row + (v + i * step) * 8 + e] = dw[i][e];
             __syncthreads();
             for (int c = threadIdx.x; c < V * 8; c += blockDim.x) {
                 float s = 0.0f;
@@ -453,27 +438,40 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
     }
 }
 
-// grad_w = the blocks' partial rows: block b takes 64 columns, its waves every sixteenth row
-// each, joined in wave order.
+// grad_w = the blocks' partial rows: block b takes 32 columns (a cache line of each row), its
+// half waves every 32nd row each, joined in their order.
+constexpr int kSumCols = 32;
+constexpr int kSumRows = kMaxWaves * kWave / kSumCols;
 __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_dw_sum_kernel(const float* part, int H,
                                                                           int rows, float* dw) {
-    __shared__ float acc[kMaxWaves][kWave];
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
-    const int c = static_cast<int>(blockIdx.x) * kWave + lane;
+    __shared__ float acc[kSumRows][kSumCols];
+    const int x = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+    const int c = static_cast<int>(blockIdx.x) * kSumCols + x;
     float s = 0.0f;
     if (c < H) {
 #pragma unroll 8
-        for (int p = wave; p < rows; p += kMaxWaves) s += part[static_cast<int64_t>(p) * H + c];
+        for (int p = r; p < rows; p += kSumRows) s += part[static_cast<int64_t>(p) * H + c];
     }
-    acc[wave][lane] = s;
+    acc[r][x] = s;
     __syncthreads();
-    if (wave == 0 && c < H) {
+    if (r == 0 && c < H) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kMaxWaves; ++i) s += acc[i][lane];
+        for (int i = 0; i < kSumRows; ++i) s += acc[i][x];
         dw[c] = s;
     }
 }
+
+// Blocks with grad_w: one per CU, each with as many rows at a time as 16 waves hold, so that
+// the partial rows stay few. Measured at 7168 channels, two words per lane: 256 blocks of two
+// rows at a time 46.8 us at 4096 tokens and 138.4 us at 14000; 512 blocks of one row 47.2 and
+// 146.9 us (one word per lane: 256 blocks 52.6 and 157.7 us, 1024 blocks 64.5 and 168.2 us).
+// Batches of up to 256 rows take a row per block: 256 tokens 11.1 us against 12.4 us.
+constexpr int64_t kGradBlocks = 256;
+// From this many bytes of h on, the rows' loads are non-temporal. Cached against
+// non-temporal: 17.6 against 18.2 us at 1024 tokens of 7168 channels (15 MB), 23.8 against
+// 25.0 us at 14000 of 1024 (29 MB), 51.3 against 46.8 us at 4096 of 7168 (59 MB).
+constexpr int64_t kGradStreamBytes = int64_t{40} << 20;
 
 // Launch shape of the gradient with rows in registers; W == 0 for rows wider than that.
 struct GradShape {
@@ -484,13 +482,11 @@ struct GradShape {
 GradShape grad_shape(int64_t T, int V) {
     GradShape s{};
     const int words = (V + kWave - 1) / kWave;
-    if (words <= EP_NG_NV * kMaxWaves && words > kMaxWaves / 2) s.nv = EP_NG_NV;
-    else if (words <= kMaxWaves) s.nv = 1;
-    else if (words <= 2 * kMaxWaves) s.nv = 2;
-    else return s;
+    if (words > 2 * kMaxWaves) return s;
+    s.nv = words > kMaxWaves / 2 ? 2 : 1;
     s.W = (words + s.nv - 1) / s.nv;
-    s.G = s.nv == 1 ? kMaxWaves / s.W : 1;
-    s.blocks = std::min<int64_t>(EP_NG_B, (T + s.G - 1) / s.G);
+    s.G = static_cast<int>(std::min<int64_t>(kMaxWaves / s.W, (T + kGradBlocks - 1) / kGradBlocks));
+    s.blocks = std::min<int64_t>(kGradBlocks, (T + s.G - 1) / s.G);
     return s;
 }
 
@@ -513,13 +509,19 @@ hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weigh
                            static_cast<u32x4*>(y), reinterpret_cast<u32x2*>(y_fp8), y_scales);
         return hipGetLastError();
     };
+    using Nt = std::integral_constant<int, kPolicyNt>;
+    using Cached = std::integral_constant<int, 0>;
     const auto row = [&](auto nv, auto one_wave) {
         constexpr int n = decltype(nv)::value;
         constexpr bool one = decltype(one_wave)::value;
         const int threads = one ? kNT : kWave * ((V + kWave * n - 1) / (kWave * n));
-        return launch(weight_fp32 ? rmsnorm_row_kernel<n, true, one>
-                                  : rmsnorm_row_kernel<n, false, one>,
-                      one ? (T + kNWaves - 1) / kNWaves : T, threads);
+        const int64_t grid = one ? (T + kNWaves - 1) / kNWaves : T;
+        const auto with = [&](auto policy) {
+            constexpr int p = decltype(policy)::value;
+            return launch(weight_fp32 ? rmsnorm_row_kernel<n, true, one, p>
+                                      : rmsnorm_row_kernel<n, false, one, p>, grid, threads);
+        };
+        return T * V * 16 >= kNormStreamBytes ? with(Nt{}) : with(Cached{});
     };
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
@@ -527,7 +529,6 @@ hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weigh
     if (V <= kWave) return row(One{}, std::true_type{});
     if (V <= 2 * kWave) return row(Two{}, std::true_type{});
     if (V <= 4 * kWave) return row(Four{}, std::true_type{});
-    if (V <= EP_NF_NV * kMaxWaves * kWave) return row(std::integral_constant<int, EP_NF_NV>{}, std::false_type{});
     if (V <= 2 * kMaxWaves * kWave) return row(Two{}, std::false_type{});
     if (V <= 4 * kMaxWaves * kWave) return row(Four{}, std::false_type{});
     return launch(weight_fp32 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>, T, kNT);
@@ -589,25 +590,31 @@ hipError_t launch_rmsnorm_grad(const void* grad_y, const void* grad_residual_out
         return launch_wide_grad(dy, dres, hp, weight, weight_fp32, eps, T, H, dx, grad_weight,
                                 workspace, stream);
     // without grad_w nothing ties a block to many rows
-    const int64_t grid = grad_weight ? s.blocks : std::min<int64_t>((T + s.G - 1) / s.G, 1 << 16);
+    const int64_t grid =
+        grad_weight ? s.blocks : std::min<int64_t>((T + s.G - 1) / s.G, int64_t{1} << 16);
     // a single block's partial row is the sum (it leaves in 128-bit words)
     const bool direct = s.blocks == 1 && reinterpret_cast<uintptr_t>(grad_weight) % 16 == 0;
     float* part = direct ? grad_weight : static_cast<float*>(workspace);
-    const auto launch = [&](auto nv) {
-        constexpr int n = decltype(nv)::value;
+    const auto launch = [&](auto nv, auto policy) {
+        constexpr int n = decltype(nv)::value, p = decltype(policy)::value;
         const auto kernel =
-            weight_fp32 ? (grad_weight ? rmsnorm_grad_row_kernel<n, true, true>
-                                       : rmsnorm_grad_row_kernel<n, true, false>)
-                        : (grad_weight ? rmsnorm_grad_row_kernel<n, false, true>
-                                       : rmsnorm_grad_row_kernel<n, false, false>);
+            weight_fp32 ? (grad_weight ? rmsnorm_grad_row_kernel<n, true, true, p>
+                                       : rmsnorm_grad_row_kernel<n, true, false, p>)
+                        : (grad_weight ? rmsnorm_grad_row_kernel<n, false, true, p>
+                                       : rmsnorm_grad_row_kernel<n, false, false, p>);
         hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(kWave * s.W * s.G), 0,
                            stream, dy, dres, hp, weight, eps, T, V, s.W, dx, part);
         return hipGetLastError();
     };
-    const hipError_t e = s.nv == 1 ? launch(std::integral_constant<int, 1>{})
-                                   : launch(std::integral_constant<int, 2>{});
+    const auto with = [&](auto policy) {
+        return s.nv == 1 ? launch(std::integral_constant<int, 1>{}, policy)
+                         : launch(std::integral_constant<int, 2>{}, policy);
+    };
+    const hipError_t e = T * V * 16 >= kGradStreamBytes
+                             ? with(std::integral_constant<int, kPolicyNt>{})
+                             : with(std::integral_constant<int, 0>{});
     if (e != hipSuccess || !grad_weight || direct) return e;
-    hipLaunchKernelGGL(rmsnorm_dw_sum_kernel, dim3((H + kWave - 1) / kWave),
+    hipLaunchKernelGGL(rmsnorm_dw_sum_kernel, dim3((H + kSumCols - 1) / kSumCols),
                        dim3(kMaxWaves * kWave), 0, stream, part, H, static_cast<int>(s.blocks),
                        grad_weight);
     return hipGetLastError();
