@@ -13,17 +13,19 @@ namespace ep {
 namespace {
 
 constexpr int kT = 256;  // threads per block: a few waves, each with its own piece of work
-constexpr int kWaves = kT / kWave;
+constexpr int kUnpermuteThreads = 128;
 constexpr int64_t kMaxWaves = int64_t{1} << 24;  // per launch: a wave's index stays 32 bits
 
-// Launches f(t0, t_end, grid) over token ranges of at most kMaxWaves waves.
-template <typename F>
+// Launches f(t0, t_end, grid) over token ranges of at most kMaxWaves waves, kThreads / 64 of
+// them per block.
+template <int kThreads, typename F>
 hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
+    constexpr int kWaves = kThreads / kWave;
     const int64_t step = std::max<int64_t>(1, kMaxWaves / waves_per_token);
     for (int64_t t0 = 0; t0 < T; t0 += step) {
         const int64_t t_end = std::min(T, t0 + step);
         const int64_t grid = ((t_end - t0) * waves_per_token + kWaves - 1) / kWaves;
-        if (!grid_fits(grid, kT)) return hipErrorInvalidConfiguration;
+        if (!grid_fits(grid, kThreads)) return hipErrorInvalidConfiguration;
         f(t0, t_end, static_cast<unsigned>(grid));
         EP_RETURN_IF_LAUNCH_FAILED();
     }
@@ -122,19 +124,20 @@ struct Pairs {
 
 // Wave (t, c) sums words [64 c, 64 c + 64) of token t's rows, one word per lane, kB rows'
 // loads in flight together. Bound by the rows' reads (8 per row written at top-8). Measured
-// on MI355X at 7168 channels, top-8 of 256 experts: 91.1 us at 4096 tokens and 410.7 us at
-// 16384 with an addend (5.8 and 5.7 TB/s); 64 tokens 4.2 us. Two words per lane ran 90.9,
-// 419.7 and 5.3 us; cached row loads 97.2 and 434.9 us; a block per token walking its pairs
-// one after the other 99.2, 456.2 and 12.7 us.
+// on MI355X at 7168 channels, top-8 of 256 experts: 88.9 us at 4096 tokens and 398.3 us at
+// 16384 with an addend (5.9 TB/s); 64 tokens 4.3 us. Blocks of 256 threads took 90.1 and
+// 410.7 us, of 448 90.2 and 416.8 us; two words per lane 90.9 and 419.7 us; cached row loads
+// 97.2 and 434.9 us; a block per token walking its pairs one after the other 99.2, 456.2 and
+// (64 tokens) 12.7 us.
 template <int kB>
-__global__ __launch_bounds__(kT) void unpermute_kernel(
+__global__ __launch_bounds__(kUnpermuteThreads) void unpermute_kernel(
     const u32x4* __restrict__ rows, int64_t num_rows, const float* __restrict__ topk_w,
     const int32_t* __restrict__ expert_slot, int64_t t0, int64_t t_end, int V, int k, FastDiv C,
     const u32x4* addend, u32x4* out, const float* __restrict__ grad_perm_w,
     float* __restrict__ grad_w, int32_t* __restrict__ error_flag) {
     int64_t t;
     int c;
-    if (!dest_wave<kT>(t0, t_end, C, t, c)) return;
+    if (!dest_wave<kUnpermuteThreads>(t0, t_end, C, t, c)) return;
     const int lane = lane_id();
     const int v = c * kWave + lane;
     const u32x4 ad = load_word<kPolicyNt>(row_buffer(addend, t, V), v);
@@ -177,16 +180,16 @@ __global__ __launch_bounds__(kT) void unpermute_kernel(
 // memory: a block per token, all its pairs at once (one read of grad_out, dots joined
 // through LDS), took 191.5 against 187.5 us at 4096 tokens and 9.3 against 8.2 us at 64.
 //
-// kPolicy: the cache policy of the rows' loads.
-template <int WPL, bool kDot, bool kRows, int kPolicy>
-__global__ __launch_bounds__(kT) void unpermute_grad_kernel(
+// kLoad: the cache policy of the rows' loads. kStore: of their stores.
+template <int WPL, bool kDot, bool kRows, int kLoad, int kStore, int kThreads>
+__global__ __launch_bounds__(kThreads) void unpermute_grad_kernel(
     const u32x4* __restrict__ grad_out, const u32x4* rows, int64_t num_rows,
     const float* __restrict__ topk_w, const int32_t* __restrict__ expert_slot, int64_t t0,
     int64_t t_end, int V, int k, FastDiv D, u32x4* grad_rows, float* __restrict__ grad_w,
     int32_t* __restrict__ error_flag) {
     int64_t t;
     int j;
-    if (!dest_wave<kT>(t0, t_end, D, t, j)) return;
+    if (!dest_wave<kThreads>(t0, t_end, D, t, j)) return;
     const int lane = lane_id();
     const int64_t at = t * k + j;
     const int64_t q = expert_slot[at];
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(kT) void unpermute_grad_kernel(
         u32x4 y[WPL];
         if constexpr (kDot) {
 #pragma unroll
-            for (int i = 0; i < WPL; ++i) y[i] = load_word<kPolicy>(yb, v0 + i * kWave + lane);
+            for (int i = 0; i < WPL; ++i) y[i] = load_word<kLoad>(yb, v0 + i * kWave + lane);
         }
         if (v0 != 0) {
 #pragma unroll
@@ -228,7 +231,7 @@ __global__ __launch_bounds__(kT) void unpermute_grad_kernel(
             if constexpr (kRows) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) gf[e] *= w;
-                store_word<kPolicyNt>(ob, v0 + i * kWave + lane, narrow8(gf));
+                store_word<kStore>(ob, v0 + i * kWave + lane, narrow8(gf));
             }
         }
     }
@@ -241,12 +244,17 @@ __global__ __launch_bounds__(kT) void unpermute_grad_kernel(
 // Above this many bytes of routed rows the dots and the rows are two launches, one that
 // mostly reads and one that mostly writes: HBM moves a stream of reads and then a stream of
 // writes faster than the two mixed over scattered rows. Measured on MI355X, one launch
-// against two: 188.1 against 172.3 us at 4096 tokens (470 MB of rows), 394 against 343 us at
-// 8192, 48.5 against 46.1 us at 1024 (117 MB). Below it one launch with cached row loads,
-// since a set this small may still lie in the 256 MB Infinity Cache, where the experts
-// left it: 22.7 us against 28.1 us with non-temporal loads at 512 tokens (59 MB), and the
-// second launch would be a larger share.
+// against two: 188.1 against 168.1 us at 4096 tokens (470 MB of rows; 5.9 TB/s, of which the
+// dots 6.4 and the rows 5.7), 394 against 338 us at 8192, 48.5 against 44.7 us at 1024
+// (117 MB). Below it one launch with cached row loads, since a set this small may still lie
+// in the 256 MB Infinity Cache, where the experts left it: 22.7 us against 28.1 us with
+// non-temporal loads at 512 tokens (59 MB), and the second launch would be a larger share.
 constexpr int64_t kOneLaunchBytes = int64_t{64} << 20;
+// The launches that read rows take blocks of 512 threads, so that a top-8 token's waves share
+// an XCD and its L2 fetches grad_out's row once: 10.6 against 11.1 us at 256 tokens, 169.8
+// against 172.9 us at 4096 (128 threads 198.4 us). Below this many pairs that would leave CUs
+// without a block, and blocks of 256 take over: 5.1 against 6.4 us at 64 tokens.
+constexpr int64_t kWideBlockPairs = 2048;
 
 }  // namespace
 
@@ -258,7 +266,7 @@ hipError_t launch_dispatch_permute_fp8(const void* x_fp8, const float* x_scales,
     const int V = H / 16, G = H / kNormGroup;
     const FastDiv fd = FastDiv::make(k);
     const bool cached = T * k * G * static_cast<int64_t>(sizeof(float)) <= kCachedScaleBytes;
-    return by_token_range(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
+    return by_token_range<kT>(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
         with_row_width<14, false>(V, [&](auto wpl, auto multi) {
             constexpr int w = decltype(wpl)::value;
             constexpr bool m = decltype(multi)::value;
@@ -282,8 +290,8 @@ static hipError_t launch_unpermute(const void* rows, int64_t num_rows, const flo
     const auto kernel = k <= 2   ? unpermute_kernel<2>
                         : k <= 4 ? unpermute_kernel<4>
                                  : unpermute_kernel<8>;
-    return by_token_range(T, C, [&](int64_t t0, int64_t t_end, unsigned grid) {
-        hipLaunchKernelGGL(kernel, dim3(grid), dim3(kT), 0, stream,
+    return by_token_range<kUnpermuteThreads>(T, C, [&](int64_t t0, int64_t t_end, unsigned grid) {
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(kUnpermuteThreads), 0, stream,
                            static_cast<const u32x4*>(rows), num_rows, topk_w, expert_slot, t0,
                            t_end, V, k, fd, static_cast<const u32x4*>(addend),
                            static_cast<u32x4*>(out), grad_perm_w, grad_w, error_flag);
@@ -313,14 +321,14 @@ hipError_t launch_combine_unpermute_grad(const void* grad_out, const void* rows,
                                          hipStream_t stream) {
     const int V = H / 8;
     const FastDiv fd = FastDiv::make(k);
-    // one pass over the pairs; the first pass, if there are two, only reads rows
-    const auto pass = [&](auto dot, auto write, auto policy) {
+    const auto pass = [&](auto dot, auto write, auto load, auto store, auto threads, auto width) {
         constexpr bool d = decltype(dot)::value, r = decltype(write)::value;
-        constexpr int p = decltype(policy)::value;
-        return by_token_range(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
-            with_row_width<7, false>(V, [&](auto wpl, auto) {
-                hipLaunchKernelGGL((unpermute_grad_kernel<decltype(wpl)::value, d, r, p>),
-                                   dim3(grid), dim3(kT), 0, stream,
+        constexpr int ld = decltype(load)::value, st = decltype(store)::value;
+        constexpr int n = decltype(threads)::value;
+        return by_token_range<n>(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
+            with_row_width<decltype(width)::value, false>(V, [&](auto wpl, auto) {
+                hipLaunchKernelGGL((unpermute_grad_kernel<decltype(wpl)::value, d, r, ld, st, n>),
+                                   dim3(grid), dim3(n), 0, stream,
                                    static_cast<const u32x4*>(grad_out),
                                    static_cast<const u32x4*>(rows), num_rows, topk_w, expert_slot,
                                    t0, t_end, V, k, fd, static_cast<u32x4*>(grad_rows), grad_w,
@@ -328,16 +336,23 @@ hipError_t launch_combine_unpermute_grad(const void* grad_out, const void* rows,
             });
         });
     };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    using Nt = std::integral_constant<int, kPolicyNt>;
-    using Cached = std::integral_constant<int, 0>;
-    if (grad_w && T * k * V * 16 <= kOneLaunchBytes) return pass(Yes{}, Yes{}, Cached{});
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    constexpr std::integral_constant<int, 0> cached{};
+    constexpr std::integral_constant<int, kPolicyNt> nt{};
+    constexpr std::integral_constant<int, kPolicyNt | kPolicySc1> nt_device{};
+    constexpr std::integral_constant<int, 256> t256{};
+    constexpr std::integral_constant<int, 512> t512{};
+    constexpr std::integral_constant<int, 7> w7{};
+    constexpr std::integral_constant<int, 14> w14{};
+    if (grad_w && T * k * V * 16 <= kOneLaunchBytes)
+        return T * k >= kWideBlockPairs ? pass(yes, yes, cached, nt, t512, w14)
+                                        : pass(yes, yes, cached, nt, t256, w14);
     if (grad_w) {
-        const hipError_t e = pass(Yes{}, No{}, Nt{});
+        const hipError_t e = pass(yes, no, nt, nt, t512, w7);
         if (e != hipSuccess) return e;
     }
-    return pass(No{}, Yes{}, Nt{});
+    return pass(no, yes, nt, nt_device, t256, w7);
 }
 
 }  // namespace ep

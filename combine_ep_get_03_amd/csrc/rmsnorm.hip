@@ -323,7 +323,9 @@ __global__ __launch_bounds__(kNT) void rmsnorm_dx_kernel(const u32x4* dy, const 
 }
 
 // The same word, unknown to the compiler: what was computed from it before is computed again
-// instead of being kept in registers.
+// instead of being kept in registers. On grad_y's words after the reduction it frees the
+// registers that two words per lane lack by one (46.3 against 46.7 us at 4096 tokens of 7168
+// channels); on h's words as well 48.9 us.
 __device__ __forceinline__ u32x4 anew(u32x4 w) {
     asm volatile("" : "+v"(w));
     return w;
@@ -397,7 +399,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
         for (int i = 0; i < NV; ++i) {
             float d[8], f[8], y[8];
             widen8(cur.dr[i], d);
-            widen8(anew(cur.h[i]), f);
+            widen8(cur.h[i], f);
             widen8(anew(cur.dy[i]), y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
