@@ -645,7 +645,7 @@ def _rows_2d(t: torch.Tensor, name: str):
 # share is kept small: one look at the current device per call, one combined check per
 # tensor (a failed one is explained by _shape and _ptr), device addresses as plain ints.
 # One call of ep_rmsnorm with four outputs, kernel launch included: 16.4 us with _shape and
-# _ptr per tensor, HOST_AFTER us so (AMD EPYC host).
+# _ptr per tensor, 7.7 us so, 3.4 of them in the C call (AMD EPYC host).
 def _row_ptr(t: Optional[torch.Tensor], dtype, shape, name: str, cur: int):
     """Device address of a required tensor of exactly this type and shape."""
     if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == cur and \

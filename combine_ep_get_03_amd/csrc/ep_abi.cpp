@@ -56,7 +56,7 @@ int check_layout_args(const int64_t* topk_idx, int64_t T, int k, int E, int R, i
 
 // Sizes shared by the calls over expert_slot.
 int check_expert_rows(int64_t T, int H, int k, int64_t rows, int row_multiple) {
-    if (T < 0 || H < 1 || k < 1 || rows < 0) return EP_ERR_ARG;
+    if (T < 0 || H < 1 || k < 1 || k > EP_MAX_EXPERTS || rows < 0) return EP_ERR_ARG;
     if (T > static_cast<int64_t>(INT32_MAX) / k) return EP_ERR_ARG;
     if (H % row_multiple != 0) return EP_ERR_ALIGN;
     if (static_cast<int64_t>(H) / 8 * 64 > INT32_MAX) return EP_ERR_ARG;

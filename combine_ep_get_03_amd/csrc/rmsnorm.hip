@@ -85,11 +85,12 @@ __device__ __forceinline__ float quantize8(const float (&f)[8], u32x2& code) {
 // twice, the second time from the L2.
 template <bool kF32>
 __global__ __launch_bounds__(kNT) void rmsnorm_kernel(const u32x4* x, const u32x4* residual,
-                                                      const void* weight, float eps, int64_t T,
-                                                      int V, u32x4* residual_out, u32x4* y,
+                                                      const void* weight, float eps, int64_t t0,
+                                                      int64_t /*t_end*/, int V,
+                                                      u32x4* residual_out, u32x4* y,
                                                       u32x2* y_fp8, float* y_scales) {
     __shared__ float red[kNWaves];
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * V;
+    const int64_t base = (t0 + blockIdx.x) * V;
     const u32x4* res = residual ? residual + base : nullptr;
     float ss = 0.0f;
     for (int v = threadIdx.x; v < V; v += kNT) {
@@ -165,12 +166,13 @@ __device__ __forceinline__ void weight_word(__amdgpu_buffer_rsrc_t wb, int v, fl
 // their loads and stores of the bf16 rows leave every other 16 bytes to a second access.
 template <int NV, bool kF32, bool kOneWave, int kPolicy>
 __global__ __launch_bounds__(kOneWave ? kNT : kMaxWaves * kWave) void rmsnorm_row_kernel(
-    const u32x4* x, const u32x4* residual, const void* weight, float eps, int64_t T, int V,
-    u32x4* residual_out, u32x4* y, u32x2* y_fp8, float* y_scales) {
+    const u32x4* x, const u32x4* residual, const void* weight, float eps, int64_t t0, int64_t t_end,
+    int V, u32x4* residual_out, u32x4* y, u32x2* y_fp8, float* y_scales) {
     __shared__ float red[kMaxWaves][1];
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const int64_t t = kOneWave ? static_cast<int64_t>(blockIdx.x) * kNWaves + wave : blockIdx.x;
-    if (kOneWave && t >= T) return;
+    const int64_t t =
+        t0 + (kOneWave ? static_cast<int64_t>(blockIdx.x) * kNWaves + wave : blockIdx.x);
+    if (kOneWave && t >= t_end) return;
     const int v = kOneWave ? lane_id() : threadIdx.x;
     const int step = kOneWave ? kWave : blockDim.x;
     const __amdgpu_buffer_rsrc_t xb = row_buffer(x, t, V), rb = row_buffer(residual, t, V);
@@ -226,6 +228,7 @@ __global__ __launch_bounds__(kOneWave ? kNT : kMaxWaves * kWave) void rmsnorm_ro
 // channels with all outputs, cached against non-temporal: 11.1 against 12.9 us at 1024 tokens
 // (15 MB), 28.1 against 25.4 us at 2048 (29 MB), 49.5 against 46.7 us at 4096 (59 MB).
 constexpr int64_t kNormStreamBytes = int64_t{24} << 20;
+constexpr int64_t kMaxRows = int64_t{1} << 21;  // per launch
 
 // ---- gradient
 
@@ -503,13 +506,18 @@ hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weigh
                           void* y, uint8_t* y_fp8, float* y_scales, hipStream_t stream) {
     if (T == 0) return hipSuccess;
     const int V = H / 8;
-    const auto launch = [&](auto kernel, int64_t grid, int threads) {
-        if (!grid_fits(grid, threads)) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, stream,
-                           static_cast<const u32x4*>(x), static_cast<const u32x4*>(residual),
-                           weight, eps, T, V, static_cast<u32x4*>(residual_out),
-                           static_cast<u32x4*>(y), reinterpret_cast<u32x2*>(y_fp8), y_scales);
-        return hipGetLastError();
+    // launches of at most kMaxRows rows: a dispatch packet counts threads in 32 bits
+    const auto launch = [&](auto kernel, int rows_per_block, int threads) {
+        for (int64_t t0 = 0; t0 < T; t0 += kMaxRows) {
+            const int64_t t_end = std::min(T, t0 + kMaxRows);
+            const int64_t grid = (t_end - t0 + rows_per_block - 1) / rows_per_block;
+            hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, stream,
+                               static_cast<const u32x4*>(x), static_cast<const u32x4*>(residual),
+                               weight, eps, t0, t_end, V, static_cast<u32x4*>(residual_out),
+                               static_cast<u32x4*>(y), reinterpret_cast<u32x2*>(y_fp8), y_scales);
+            EP_RETURN_IF_LAUNCH_FAILED();
+        }
+        return hipSuccess;
     };
     using Nt = std::integral_constant<int, kPolicyNt>;
     using Cached = std::integral_constant<int, 0>;
@@ -517,11 +525,11 @@ hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weigh
         constexpr int n = decltype(nv)::value;
         constexpr bool one = decltype(one_wave)::value;
         const int threads = one ? kNT : kWave * ((V + kWave * n - 1) / (kWave * n));
-        const int64_t grid = one ? (T + kNWaves - 1) / kNWaves : T;
         const auto with = [&](auto policy) {
             constexpr int p = decltype(policy)::value;
             return launch(weight_fp32 ? rmsnorm_row_kernel<n, true, one, p>
-                                      : rmsnorm_row_kernel<n, false, one, p>, grid, threads);
+                                      : rmsnorm_row_kernel<n, false, one, p>,
+                          one ? kNWaves : 1, threads);
         };
         return T * V * 16 >= kNormStreamBytes ? with(Nt{}) : with(Cached{});
     };
@@ -533,7 +541,7 @@ hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weigh
     if (V <= 4 * kWave) return row(Four{}, std::true_type{});
     if (V <= 2 * kMaxWaves * kWave) return row(Two{}, std::false_type{});
     if (V <= 4 * kMaxWaves * kWave) return row(Four{}, std::false_type{});
-    return launch(weight_fp32 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>, T, kNT);
+    return launch(weight_fp32 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>, 1, kNT);
 }
 
 size_t rmsnorm_grad_workspace_bytes(int64_t T, int H) {

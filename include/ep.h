@@ -503,7 +503,7 @@ int ep_combine_recv(const void *stage, int num_nodes, int64_t max_tokens_per_ran
  *
  * Common to the four calls over expert_slot (int32 [T][k], from ep_get_layout or
  * ep_dispatch_permute_layout): a negative entry is a pair that is not routed; entries >= 0
- * of one call must be distinct rows (as ep_get_layout makes them). Any k >= 1 with
+ * of one call must be distinct rows (as ep_get_layout makes them). 1 <= k <= EP_MAX_EXPERTS,
  * T * k <= INT32_MAX.
  *
  * ep_rmsnorm -- with s = float(x) + float(residual) (fp32, not rounded; s = x without a

@@ -94,7 +94,8 @@ def perm_grad(lib, gp=A16, gpw=A16, n=8, T=4, H=256, k=2, slot=A16, gx=A16, gw=A
 
 def test_expert_rows_size_refusals(lib):
     for f, rows in ((perm8, "cap"), (unperm, "n"), (unperm_grad, "n"), (perm_grad, "n")):
-        for bad in (dict(T=-1), dict(H=0), dict(k=0), dict(k=-1), {rows: -1}, dict(T=2**30, k=4),
+        for bad in (dict(T=-1), dict(H=0), dict(k=0), dict(k=-1), dict(k=8193), {rows: -1},
+                    dict(T=2**30, k=4),
                     dict(H=2**30)):
             assert f(lib, **bad) == ep.EP_ERR_ARG, (f.__name__, bad)
         assert f(lib, H=252) == ep.EP_ERR_ALIGN

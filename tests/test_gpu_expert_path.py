@@ -213,6 +213,34 @@ def test_training_step_replays_in_a_graph_beside_an_eager_one():
         assert int(a.error_flag) == 0 and int(b.error_flag) == 0
 
 
+def test_duplicate_and_bad_expert_ids():
+    """A token that names an expert twice has two rows of it; ids out of range are dropped and
+    reported, and their gate's gradient is zero."""
+    T, H, E, k = 60, 256, 8, 4
+    print("\ncase: duplicate and bad ids", flush=True)
+    d = inputs(9, T, H, E, k, dropped=0.0)
+    d["idx"][3] = 5
+    d["idx"][10, 1] = E + 2
+    d["idx"][11, 0] = -7
+    p = ExpertPath(T, H, E, k, training=True)
+    p.norm(d["x"], d["weight"])
+    assert p.h is d["x"]
+    p.dispatch(d["idx"], d["gate"])
+    M = int(p.expert_offset[-1])
+    assert M == T * k - 2 and int(p.error_flag) == ep.EP_DEVERR_TOPK_RANGE
+    p.combine(p.perm_x, d["gate"])
+    _, y = P.rmsnorm(P.f64(d["x"]), None, P.f64(d["weight"]), p.eps)
+    routed = (d["idx"].cpu() >= 0) & (d["idx"].cpu() < E)
+    gate = torch.where(routed, P.f64(d["gate"]), torch.zeros((), dtype=torch.float64))
+    want = y * gate.sum(dim=1, keepdim=True)
+    # every row of a token is its y, rounded once; the sum once more
+    P.assert_within(p.out, want, 2.1 * P.BF16 * want.abs() + 1e-30, "out")
+    p.combine_grad(d["grad_out"], p.perm_x, d["gate"])
+    gw = p.grad_topk_weights.cpu()
+    assert torch.all(gw[~routed] == 0) and torch.all(gw[routed] != 0)
+    assert torch.equal(gw[3], gw[3, :1].expand(k))
+
+
 def test_gradients_need_a_training_path():
     p = ExpertPath(4, 128, 16, 2)
     x = torch.zeros((4, 128), dtype=BF16, device="cuda")

@@ -173,6 +173,54 @@ def test_permute_fp8(T, H, k):
         assert int(err) == 0
 
 
+@pytest.mark.parametrize("T,H,k", [(601, 7168, 8), (8300, 1024, 4), (1200, 8200, 4)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_unpermute_grad_in_two_launches(T, H, k, in_place):
+    """More than 64 MB of rows: the dots and the rows are separate launches."""
+    print(f"\ncase: unpermute_grad in two launches T={T} H={H} k={k}", flush=True)
+    assert T * k * H * 2 > 64 << 20
+    g, cap, slot, rows, w = case(T, T, H, k)
+    go = rand(g, T, H)
+    y = rows.clone()
+    gr = y if in_place else sentinel(cap, H)
+    gw, err = torch.full((T, k), -9.0, device="cuda"), flag()
+    ep.ep_combine_unpermute_grad(go, y, w, slot, grad_expert_out=gr, grad_topk_weights=gw,
+                                 error_flag=err)
+    s, r, wd = slot.cpu(), P.f64(rows), wsafe(w, slot.cpu())
+    hit = s >= 0
+    want, want_w = P.unpermute_grad(P.f64(go), r, wd, s)
+    got = gr.cpu()
+    P.assert_within(got[s[hit].long()], want[hit], (P.BF16 + 4 * P.U) * want[hit].abs()
+                    + P.TINY_BF16, "grad_expert_out")
+    left = torch.ones(cap, dtype=torch.bool)
+    left[s[hit].long()] = False
+    assert torch.all(got[left].view(torch.int16) == SENT)
+    r0 = torch.where(torch.isnan(r), torch.zeros((), dtype=torch.float64), r)
+    P.assert_within(gw, want_w, P.dot_bound(P.f64(go), r0, s), "grad_topk_weights")
+    assert torch.all(gw.cpu()[~hit].view(torch.int32) == 0) and int(err) == 0
+
+
+@pytest.mark.parametrize("T,H,k", [(10_000, 7168, 8), (70_001, 512, 16)])
+def test_permute_fp8_of_many_scales(T, H, k):
+    """More than 16 MB of scales, which leave with another store."""
+    print(f"\ncase: permute_fp8 T={T} H={H} k={k}", flush=True)
+    assert T * k * (H // 128) * 4 > 16 << 20
+    g = gen(T)
+    slot = slots(g, T, k, T * k + 3)
+    x = torch.randint(1, 256, (T, H), generator=g, device="cuda").to(torch.uint8)
+    sc = torch.rand((T, H // 128), generator=g, device="cuda") + 1
+    px = torch.zeros((T * k + 3, H), dtype=torch.uint8, device="cuda")
+    ps = torch.zeros((T * k + 3, H // 128), device="cuda")
+    pi = torch.full((T * k + 3,), -1, dtype=torch.int32, device="cuda")
+    ep.ep_dispatch_permute_fp8(x, sc, None, slot, perm_x_fp8=px, perm_scales=ps, perm_src_idx=pi)
+    t, j = torch.nonzero(slot >= 0, as_tuple=True)
+    q = slot[t, j].long()
+    assert torch.equal(px[q], x[t]) and torch.equal(ps[q], sc[t]) and torch.equal(pi[q].long(), t)
+    left = torch.ones(T * k + 3, dtype=torch.bool, device="cuda")
+    left[q] = False
+    assert not px[left].any() and not ps[left].any() and torch.all(pi[left] == -1)
+
+
 def test_rows_out_of_range_are_skipped_and_reported():
     T, H, k = 50, 256, 4
     print("\ncase: rows out of range", flush=True)

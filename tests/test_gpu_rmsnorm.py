@@ -68,7 +68,8 @@ def test_norm_widths(T, H):
             check_norm(x, res, w, **o)
 
 
-@pytest.mark.parametrize("T,H", [(4096, 7168), (2049, 2048), (8193, 256), (20000, 64), (70000, 8)])
+@pytest.mark.parametrize("T,H", [(4096, 7168), (2049, 2048), (8193, 256), (20000, 64), (70000, 8),
+                                 (60000, 264), (30001, 1032), (2_100_000, 8)])
 def test_norm_many_rows(T, H):
     print(f"\ncase: rmsnorm T={T} H={H}", flush=True)
     g = gen(T)
@@ -201,7 +202,8 @@ def test_grad_widths(T, H):
             check_grad(dy, dres, h, w, dx, dw)
 
 
-@pytest.mark.parametrize("T,H", [(2000, 1024), (4099, 256), (1021, 2056), (9001, 40), (600, 7168)])
+@pytest.mark.parametrize("T,H", [(2000, 1024), (4099, 256), (1021, 2056), (9001, 40), (600, 7168),
+                                 (3001, 7168), (2600, 8200), (257, 520), (1300, 16384)])
 def test_grad_many_rows_and_the_same_bits_twice(T, H):
     print(f"\ncase: rmsnorm_grad T={T} H={H}", flush=True)
     g = gen(T + H)
@@ -247,6 +249,36 @@ def test_grad_of_a_row_of_zeros_and_a_nan_row():
     assert torch.isnan(dx[2]).all() and torch.isnan(dw).all()
     rest = [0, 1, 3, 4, 5]
     check_grad(dy[rest], None, h[rest], w, dx[rest], None)
+
+
+def test_grad_weight_off_the_16_byte_grid():
+    """grad_weight needs 4-byte alignment only; one block's sum leaves in wide words where it
+    may."""
+    for T, H in ((1, 1024), (2, 7168), (300, 512)):
+        print(f"\ncase: rmsnorm_grad T={T} H={H}, grad_weight at 4 bytes", flush=True)
+        g = gen(T)
+        dy, h, w = rand(g, T, H), rand(g, T, H), weight_of(g, H, BF16)
+        room = torch.full((H + 2,), 7.0, device="cuda")
+        dx = torch.zeros_like(h)
+        ep.ep_rmsnorm_grad(dy, h, w, grad_x=dx, grad_weight=room[1:H + 1], workspace=workspace(T, H),
+                           eps=EPS)
+        check_grad(dy, None, h, w, dx, room[1:H + 1])
+        assert float(room[0]) == 7.0 and float(room[H + 1]) == 7.0
+
+
+def test_grad_with_eps_zero_and_a_last_block_half_empty():
+    """Rows that are not there (a block holds several) leave no 0 / 0 in the sums."""
+    T, H = 5, 64
+    g = gen(1)
+    dy, h, w = rand(g, T, H), rand(g, T, H), weight_of(g, H, BF16)
+    dx, dw = torch.zeros_like(h), torch.zeros(H, device="cuda")
+    ep.ep_rmsnorm_grad(dy, h, w, grad_x=dx, grad_weight=dw, workspace=workspace(T, H), eps=0.0)
+    check_grad(dy, None, h, w, dx, dw, eps=0.0)
+    for T, H in ((259, 64), (1021, 2056)):
+        dy, h, w = rand(g, T, H), rand(g, T, H), weight_of(g, H, BF16)
+        dx, dw = torch.zeros_like(h), torch.zeros(H, device="cuda")
+        ep.ep_rmsnorm_grad(dy, h, w, grad_x=dx, grad_weight=dw, workspace=workspace(T, H), eps=0.0)
+        check_grad(dy, None, h, w, dx, dw, eps=0.0)
 
 
 def test_no_tokens():
