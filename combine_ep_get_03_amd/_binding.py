@@ -641,22 +641,24 @@ def _rows_2d(t: torch.Tensor, name: str):
     return t.shape
 
 
+_BF16, _F32, _I32, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
+                                 torch.float8_e4m3fn)
+
+
 # The calls below take a few microseconds on the GPU at decode-sized batches, so the host's
 # share is kept small: one look at the current device per call, one combined check per
 # tensor (a failed one is explained by _shape and _ptr), device addresses as plain ints.
 # One call of ep_rmsnorm with four outputs, kernel launch included: 16.4 us with _shape and
 # _ptr per tensor, 7.7 us so, 3.4 of them in the C call (AMD EPYC host).
-def _row_ptr(t: Optional[torch.Tensor], dtype, shape, name: str, cur: int):
-    """Device address of a required tensor of exactly this type and shape."""
-    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == cur and \
-            t.is_contiguous():
+def _row_ptr(t: Optional[torch.Tensor], dtype, shape, name: str, cur: int, need: bool = True):
+    """Device address of a tensor of exactly this type and shape; NULL for None unless it is
+    needed."""
+    if t is None:
+        return _ptr(t, dtype, name, not need)
+    if t.dtype is dtype and t.shape == shape and t.get_device() == cur and t.is_contiguous():
         return t.data_ptr()
     _shape(t, shape, name)
     _ptr(t, dtype, name)  # raises
-
-
-def _row_ptr_or_null(t: Optional[torch.Tensor], dtype, shape, name: str, cur: int):
-    return None if t is None else _row_ptr(t, dtype, shape, name, cur)
 
 
 def _flag_ptr(t: Optional[torch.Tensor], cur: int):
@@ -664,7 +666,7 @@ def _flag_ptr(t: Optional[torch.Tensor], cur: int):
     if t is None:
         return None
     _at_least(t, 1, "error_flag")
-    return _row_ptr(t, torch.int32, t.shape, "error_flag", cur)
+    return _row_ptr(t, _I32, t.shape, "error_flag", cur)
 
 
 def _current(stream):
@@ -676,19 +678,16 @@ def _current(stream):
     return cur, torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
 
 
-def _codes_ptr(t: Optional[torch.Tensor], shape, name: str, cur: int, nullable: bool = False):
+def _codes_ptr(t: Optional[torch.Tensor], shape, name: str, cur: int, need: bool = True):
     """Device address of e4m3 codes: uint8, or float8_e4m3fn."""
-    if t is None and nullable:
-        return None
-    dtype = torch.float8_e4m3fn if t is not None and t.dtype is torch.float8_e4m3fn else torch.uint8
-    return _row_ptr(t, dtype, shape, name, cur)
+    return _row_ptr(t, _E4M3 if t is not None and t.dtype is _E4M3 else _U8, shape, name, cur, need)
 
 
 def _norm_weight(weight: torch.Tensor, H: int, cur: int):
     dtype = weight.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    if dtype is not _BF16 and dtype is not _F32:
         raise TypeError(f"weight: expected torch.bfloat16 or torch.float32, got {dtype}")
-    return _row_ptr(weight, dtype, (H,), "weight", cur), int(dtype is torch.float32)
+    return _row_ptr(weight, dtype, (H,), "weight", cur), int(dtype is _F32)
 
 
 def ep_rmsnorm(x, weight, *, residual=None, residual_out=None, y=None, y_fp8=None, y_scales=None,
@@ -700,13 +699,12 @@ def ep_rmsnorm(x, weight, *, residual=None, residual_out=None, y=None, y_fp8=Non
     rows = T, H = _rows_2d(x, "x")
     cur, st = _current(stream)
     w, w_fp32 = _norm_weight(weight, H, cur)
-    bf16 = torch.bfloat16
     _check(load().ep_rmsnorm(
-        _row_ptr(x, bf16, rows, "x", cur), _row_ptr_or_null(residual, bf16, rows, "residual", cur),
-        w, w_fp32, eps, T, H, _row_ptr_or_null(residual_out, bf16, rows, "residual_out", cur),
-        _row_ptr_or_null(y, bf16, rows, "y", cur),
-        _codes_ptr(y_fp8, rows, "y_fp8", cur, True),
-        _row_ptr_or_null(y_scales, torch.float32, (T, H // 128), "y_scales", cur), st),
+        _row_ptr(x, _BF16, rows, "x", cur), _row_ptr(residual, _BF16, rows, "residual", cur, False),
+        w, w_fp32, eps, T, H, _row_ptr(residual_out, _BF16, rows, "residual_out", cur, False),
+        _row_ptr(y, _BF16, rows, "y", cur, False),
+        _codes_ptr(y_fp8, rows, "y_fp8", cur, False),
+        _row_ptr(y_scales, _F32, (T, H // 128), "y_scales", cur, False), st),
         "ep_rmsnorm")
 
 
@@ -724,16 +722,16 @@ def ep_rmsnorm_grad(grad_y, h, weight, *, grad_x, grad_residual_out=None, grad_w
     rows = T, H = _rows_2d(h, "h")
     cur, st = _current(stream)
     w, w_fp32 = _norm_weight(weight, H, cur)
-    bf16 = torch.bfloat16
-    ws = None if workspace is None else _row_ptr(workspace, torch.uint8, workspace.shape,
-                                                 "workspace", cur)
+    ws_shape = () if workspace is None else workspace.shape
+    ws = _row_ptr(workspace, _U8, ws_shape, "workspace", cur, False)
+    ws_bytes = 0 if workspace is None else workspace.numel()
     _check(load().ep_rmsnorm_grad(
-        _row_ptr(grad_y, bf16, rows, "grad_y", cur),
-        _row_ptr_or_null(grad_residual_out, bf16, rows, "grad_residual_out", cur),
-        _row_ptr(h, bf16, rows, "h", cur), w, w_fp32, eps, T, H,
-        _row_ptr(grad_x, bf16, rows, "grad_x", cur),
-        _row_ptr_or_null(grad_weight, torch.float32, (H,), "grad_weight", cur),
-        ws, 0 if workspace is None else workspace.numel(), st), "ep_rmsnorm_grad")
+        _row_ptr(grad_y, _BF16, rows, "grad_y", cur),
+        _row_ptr(grad_residual_out, _BF16, rows, "grad_residual_out", cur, False),
+        _row_ptr(h, _BF16, rows, "h", cur), w, w_fp32, eps, T, H,
+        _row_ptr(grad_x, _BF16, rows, "grad_x", cur),
+        _row_ptr(grad_weight, _F32, (H,), "grad_weight", cur, False),
+        ws, ws_bytes, st), "ep_rmsnorm_grad")
 
 
 def ep_dispatch_permute_fp8(x_fp8, x_scales, topk_weights, expert_slot, *, perm_x_fp8,
@@ -746,16 +744,16 @@ def ep_dispatch_permute_fp8(x_fp8, x_scales, topk_weights, expert_slot, *, perm_
     cap, _ = _rows_2d(perm_x_fp8, "perm_x_fp8")
     cur, st = _current(stream)
     G = H // 128
-    f32, i32 = torch.float32, torch.int32
     _check(load().ep_dispatch_permute_fp8(
         _codes_ptr(x_fp8, (T, H), "x_fp8", cur),
-        _row_ptr(x_scales, f32, (T, G), "x_scales", cur),
-        _row_ptr_or_null(topk_weights, f32, (T, k), "topk_weights", cur), T, H, k,
-        _row_ptr(expert_slot, i32, (T, k), "expert_slot", cur),
+        _row_ptr(x_scales, _F32, (T, G), "x_scales", cur),
+        _row_ptr(topk_weights, _F32, (T, k), "topk_weights", cur, False),
+        T, H, k,
+        _row_ptr(expert_slot, _I32, (T, k), "expert_slot", cur),
         _codes_ptr(perm_x_fp8, (cap, H), "perm_x_fp8", cur),
-        _row_ptr(perm_scales, f32, (cap, G), "perm_scales", cur),
-        _row_ptr_or_null(perm_weights, f32, (cap,), "perm_weights", cur),
-        _row_ptr_or_null(perm_src_idx, i32, (cap,), "perm_src_idx", cur), cap,
+        _row_ptr(perm_scales, _F32, (cap, G), "perm_scales", cur),
+        _row_ptr(perm_weights, _F32, (cap,), "perm_weights", cur, False),
+        _row_ptr(perm_src_idx, _I32, (cap,), "perm_src_idx", cur, False), cap,
         _flag_ptr(error_flag, cur), st), "ep_dispatch_permute_fp8")
 
 
@@ -767,13 +765,13 @@ def ep_combine_unpermute(expert_out, topk_weights, expert_slot, *, out, addend=N
     rows, H = _rows_2d(expert_out, "expert_out")
     T, k = _rows_2d(expert_slot, "expert_slot")
     cur, st = _current(stream)
-    bf16 = torch.bfloat16
     _check(load().ep_combine_unpermute(
-        _row_ptr(expert_out, bf16, (rows, H), "expert_out", cur), rows,
-        _row_ptr_or_null(topk_weights, torch.float32, (T, k), "topk_weights", cur), T, H, k,
-        _row_ptr(expert_slot, torch.int32, (T, k), "expert_slot", cur),
-        _row_ptr_or_null(addend, bf16, (T, H), "addend", cur),
-        _row_ptr(out, bf16, (T, H), "out", cur), _flag_ptr(error_flag, cur), st),
+        _row_ptr(expert_out, _BF16, (rows, H), "expert_out", cur), rows,
+        _row_ptr(topk_weights, _F32, (T, k), "topk_weights", cur, False),
+        T, H, k,
+        _row_ptr(expert_slot, _I32, (T, k), "expert_slot", cur),
+        _row_ptr(addend, _BF16, (T, H), "addend", cur, False),
+        _row_ptr(out, _BF16, (T, H), "out", cur), _flag_ptr(error_flag, cur), st),
         "ep_combine_unpermute")
 
 
@@ -787,16 +785,16 @@ def ep_combine_unpermute_grad(grad_out, expert_out, topk_weights, expert_slot, *
     _, k = _rows_2d(expert_slot, "expert_slot")
     rows, _ = _rows_2d(grad_expert_out, "grad_expert_out")
     cur, st = _current(stream)
-    bf16 = torch.bfloat16
     if expert_out is None and grad_topk_weights is not None:
         raise ValueError("expert_out is required with grad_topk_weights")
     _check(load().ep_combine_unpermute_grad(
-        _row_ptr(grad_out, bf16, (T, H), "grad_out", cur),
-        _row_ptr_or_null(expert_out, bf16, (rows, H), "expert_out", cur), rows,
-        _row_ptr_or_null(topk_weights, torch.float32, (T, k), "topk_weights", cur), T, H, k,
-        _row_ptr(expert_slot, torch.int32, (T, k), "expert_slot", cur),
-        _row_ptr(grad_expert_out, bf16, (rows, H), "grad_expert_out", cur),
-        _row_ptr_or_null(grad_topk_weights, torch.float32, (T, k), "grad_topk_weights", cur),
+        _row_ptr(grad_out, _BF16, (T, H), "grad_out", cur),
+        _row_ptr(expert_out, _BF16, (rows, H), "expert_out", cur, False), rows,
+        _row_ptr(topk_weights, _F32, (T, k), "topk_weights", cur, False),
+        T, H, k,
+        _row_ptr(expert_slot, _I32, (T, k), "expert_slot", cur),
+        _row_ptr(grad_expert_out, _BF16, (rows, H), "grad_expert_out", cur),
+        _row_ptr(grad_topk_weights, _F32, (T, k), "grad_topk_weights", cur, False),
         _flag_ptr(error_flag, cur), st), "ep_combine_unpermute_grad")
 
 
@@ -810,11 +808,11 @@ def ep_dispatch_permute_grad(grad_perm_x, expert_slot, *, grad_x, grad_perm_weig
     if grad_perm_weights is None and grad_topk_weights is not None:
         raise ValueError("grad_perm_weights is required with grad_topk_weights")
     _check(load().ep_dispatch_permute_grad(
-        _row_ptr(grad_perm_x, torch.bfloat16, (rows, H), "grad_perm_x", cur),
-        _row_ptr_or_null(grad_perm_weights, torch.float32, (rows,), "grad_perm_weights", cur),
-        rows, T, H, k, _row_ptr(expert_slot, torch.int32, (T, k), "expert_slot", cur),
-        _row_ptr(grad_x, torch.bfloat16, (T, H), "grad_x", cur),
-        _row_ptr_or_null(grad_topk_weights, torch.float32, (T, k), "grad_topk_weights", cur),
+        _row_ptr(grad_perm_x, _BF16, (rows, H), "grad_perm_x", cur),
+        _row_ptr(grad_perm_weights, _F32, (rows,), "grad_perm_weights", cur, False),
+        rows, T, H, k, _row_ptr(expert_slot, _I32, (T, k), "expert_slot", cur),
+        _row_ptr(grad_x, _BF16, (T, H), "grad_x", cur),
+        _row_ptr(grad_topk_weights, _F32, (T, k), "grad_topk_weights", cur, False),
         _flag_ptr(error_flag, cur), st), "ep_dispatch_permute_grad")
 
 
