@@ -240,7 +240,7 @@ class Path:
 
 class ExpertPath:
     """The expert-major block on one GPU: buffers and calls for T tokens of H channels over E
-    experts, top-k.
+    experts, top-k (k <= EP_EXPERT_SLOT_MAX_K; H a multiple of 128 with fp8=True).
 
         norm(x, weight, residual)        ep_rmsnorm: residual_out, y (and e4m3 with fp8=True)
         dispatch(topk_idx, topk_weights) ep_get_layout with expert slots, then

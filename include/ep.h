@@ -503,8 +503,9 @@ int ep_combine_recv(const void *stage, int num_nodes, int64_t max_tokens_per_ran
  *
  * Common to the four calls over expert_slot (int32 [T][k], from ep_get_layout or
  * ep_dispatch_permute_layout): a negative entry is a pair that is not routed; entries >= 0
- * of one call must be distinct rows (as ep_get_layout makes them). 1 <= k <= EP_MAX_EXPERTS,
- * T * k <= INT32_MAX.
+ * of one call must be distinct rows (as ep_get_layout makes them; the two sums over a token's
+ * rows also take repeated ones). 1 <= k <= EP_MAX_EXPERTS, T * k <= INT32_MAX. Outputs may
+ * share memory with inputs only where a call says so.
  *
  * ep_rmsnorm -- with s = float(x) + float(residual) (fp32, not rounded; s = x without a
  * residual) and n = s / sqrt(mean over the row of s^2 + eps):
@@ -518,12 +519,14 @@ int ep_combine_recv(const void *stage, int num_nodes, int64_t max_tokens_per_ran
  *                   a = max |n * weight| over the group's numbers: scale = max(a, 2^-100) /
  *                   448, code = e4m3 (E4M3FN) of n * weight * (448 / max(a, 2^-100)), rounded
  *                   to nearest even from fp32 (not from y); an all-zero group has scale 1.0
- *                   and codes 0. A NaN gets the NaN code.           (nullable, both or none)
+ *                   and codes 0. A NaN gets the NaN code. A group that holds an infinity has
+ *                   scale infinity, NaN codes for its infinities and codes 0 for the rest.
+ *                   (nullable, both or none)
  *      At least one output must be asked for.
  * Sums and the norm are fp32: |s| up to about 1e18 (squares that pass fp32 give n = 0).
  * residual_out may be x's or residual's memory and y may be the other's (the same start
  * address); any other overlap of outputs and inputs is undefined.
- * Sizes: T >= 0; H % 8 == 0, H % 128 == 0 with y_fp8 (else EP_ERR_ALIGN); rows 16-byte
+ * Sizes: 0 <= T <= INT32_MAX; H % 8 == 0, H % 128 == 0 with y_fp8 (else EP_ERR_ALIGN); rows 16-byte
  *   aligned, y_fp8 8-byte aligned, weight 16-byte aligned, y_scales 4-byte aligned.
  * Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_HIP. */
 int ep_rmsnorm(const void *x, const void *residual, const void *weight, int weight_is_fp32,

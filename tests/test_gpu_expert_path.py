@@ -213,6 +213,22 @@ def test_training_step_replays_in_a_graph_beside_an_eager_one():
         assert int(a.error_flag) == 0 and int(b.error_flag) == 0
 
 
+def test_an_empty_batch():
+    p = ExpertPath(0, 256, 16, 2, training=True)
+    x = torch.empty((0, 256), dtype=BF16, device="cuda")
+    w = torch.ones(256, device="cuda")
+    gate = torch.empty((0, 2), device="cuda")
+    p.grad_weight.fill_(4.0)
+    p.norm(x, w, x)
+    p.dispatch(torch.empty((0, 2), dtype=torch.int64, device="cuda"), gate)
+    assert int(p.expert_offset[-1]) == 0
+    p.combine(p.perm_x, gate)
+    p.combine_grad(x, p.perm_x, gate)
+    p.dispatch_grad(p.grad_expert_out)
+    p.norm_grad(w)
+    assert torch.all(p.grad_weight == 0) and int(p.error_flag) == 0
+
+
 def test_duplicate_and_bad_expert_ids():
     """A token that names an expert twice has two rows of it; ids out of range are dropped and
     reported, and their gate's gradient is zero."""

@@ -304,6 +304,37 @@ def test_no_rows_and_no_tokens():
     torch.cuda.synchronize()
 
 
+def test_sums_take_a_row_that_several_pairs_name():
+    T, H, k = 30, 256, 4
+    g = gen(21)
+    rows = rand(g, 10, H)
+    slot = torch.randint(-1, 10, (T, k), generator=g, device="cuda").to(torch.int32)
+    w = torch.rand((T, k), generator=g, device="cuda")
+    out, gx = sentinel(T, H), sentinel(T, H)
+    ep.ep_combine_unpermute(rows, w, slot, out=out)
+    ep.ep_dispatch_permute_grad(rows, slot, grad_x=gx)
+    s, r = slot.cpu(), P.f64(rows)
+    want = P.unpermute(r, P.f64(w), s, None)
+    P.assert_within(out, want, P.unpermute_bound(want, r, P.f64(w), s, None), "out")
+    want = P.unpermute(r, None, s, None)
+    P.assert_within(gx, want, P.unpermute_bound(want, r, None, s, None), "grad_x")
+
+
+def test_the_same_bits_twice():
+    T, H, k = 700, 7168, 8
+    print("\ncase: the same bits twice", flush=True)
+    g, cap, slot, rows, w = case(22, T, H, k)
+    go = rand(g, T, H)
+    got = []
+    for _ in range(2):
+        out, gr, gw = sentinel(T, H), sentinel(cap, H), torch.zeros((T, k), device="cuda")
+        ep.ep_combine_unpermute(rows, w, slot, out=out)
+        ep.ep_combine_unpermute_grad(go, rows, w, slot, grad_expert_out=gr, grad_topk_weights=gw)
+        got.append((out.view(torch.int16), gr.view(torch.int16), gw.view(torch.int32)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_unpermute_out_in_the_addends_place():
     for T, H, k in [(64, 7168, 8), (33, 520, 3)]:
         g, cap, slot, rows, w = case(14, T, H, k)

@@ -159,6 +159,61 @@ def test_norm_nan_weight_poisons_its_channel_alone():
                     P.fp8_bound(want, P.fp8_scales(want))[:, keep], "codes beside a NaN")
 
 
+def test_norm_infinite_weight_takes_its_group():
+    """An infinity in a group of 128: scale infinity, the NaN code for itself, 0 for the rest;
+    the other groups are as they would be."""
+    T, H = 3, 384
+    g = gen(14)
+    x, w = rand(g, T, H), weight_of(g, H, torch.float32)
+    x[:, 200] = 2.0
+    w[200] = float("inf")
+    y = torch.zeros_like(x)
+    codes = torch.full((T, H), 0x55, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((T, H // 128), device="cuda")
+    ep.ep_rmsnorm(x, w, y=y, y_fp8=codes, y_scales=scales, eps=EPS)
+    v = codes.view(torch.float8_e4m3fn).float()
+    assert torch.isinf(y[:, 200]).all() and torch.isinf(scales[:, 1]).all()
+    assert torch.isnan(v[:, 200]).all()
+    rest = [c for c in range(128, 256) if c != 200]
+    assert torch.all(v[:, rest] == 0)
+    keep = list(range(128)) + list(range(256, 384))
+    w[200] = 0.0
+    _, want = P.rmsnorm(P.f64(x), None, P.f64(w), EPS)
+    step = P.f64(scales)[:, [0, 2]].repeat_interleave(128, dim=1)
+    P.assert_within(e4m3(codes)[:, keep] * step, want[:, keep],
+                    P.fp8_bound(want, P.fp8_scales(want))[:, keep], "the other groups")
+
+
+def test_norm_of_squares_past_fp32_is_zero():
+    x = torch.full((2, 256), 1e25, dtype=BF16, device="cuda")
+    x[1] = 1.0
+    y = torch.ones_like(x)
+    ep.ep_rmsnorm(x, torch.ones(256, device="cuda"), y=y, eps=EPS)
+    assert torch.all(y[0] == 0) and torch.all((y[1].float() - 1).abs() <= P.BF16)
+
+
+def test_strided_host_and_wrongly_typed_tensors_are_refused():
+    T, H = 8, 256
+    x, w = torch.zeros((T, H), dtype=BF16, device="cuda"), torch.ones(H, device="cuda")
+    wide = torch.zeros((T, 2 * H), dtype=BF16, device="cuda")
+    y = torch.full_like(x, 3.0)
+    for bad, exc in ((dict(residual=wide[:, ::2]), ValueError), (dict(residual=wide[:, :H]), ValueError),
+                     (dict(residual=x.cpu()), ValueError), (dict(residual=x.half()), TypeError),
+                     (dict(residual=x.float()), TypeError)):
+        with pytest.raises(exc):
+            ep.ep_rmsnorm(x, w, y=y, **bad)
+    with pytest.raises(ValueError):
+        ep.ep_rmsnorm(x, w.cpu(), y=y)
+    with pytest.raises(ValueError):
+        ep.ep_rmsnorm(x, torch.ones(2 * H, device="cuda")[::2], y=y)
+    with pytest.raises(ep.EPError) as e:  # rows off the 16-byte grid
+        off = torch.zeros(T * H + 4, dtype=BF16, device="cuda")[4:].view(T, H)
+        ep.ep_rmsnorm(off, w, y=y)
+    assert e.value.status == ep.EP_ERR_ALIGN
+    torch.cuda.synchronize()
+    assert torch.all(y == 3.0)  # nothing ran
+
+
 def test_norm_tiny_weights_keep_finite_codes():
     T, H = 2, 128
     g = gen(6)
