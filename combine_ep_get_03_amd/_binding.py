@@ -1,12 +1,14 @@
 """ctypes binding over libep.so: one Python function per C entry point of include/ep.h,
 with the same names. Argument marshalling only: shapes, dtypes and devices of the torch
-tensors are checked, their device pointers and the current HIP stream are passed on,
-and a non-zero status becomes an ``EPError``. Every step of the path runs in the HIP
-kernels behind the C ABI; there is no fallback when the library is missing.
+tensors are checked (in the norm and expert-row calls by _tensor_ptr.so), their device
+pointers and the current HIP stream are passed on, and a non-zero status becomes an
+``EPError``. Every step of the path runs in the HIP kernels behind the C ABI; there is no
+fallback when a library is missing.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -14,6 +16,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libep.so")
+TENSOR_PTR_PATH = os.path.join(_PKG, "_tensor_ptr.so")
 
 EP_OK, EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_CAPACITY, EP_ERR_HIP = 0, -1, -2, -3, -4
 EP_DEVERR_TOPK_RANGE, EP_DEVERR_RECV_OVERFLOW, EP_DEVERR_SLOT_RANGE = 1, 2, 4
@@ -38,8 +41,10 @@ def load() -> ctypes.CDLL:
     global _lib
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIB_PATH):
-        raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
+    for path in (LIB_PATH, TENSOR_PTR_PATH):
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run __graft_entry__.build() first")
+    _load_tensor_ptr()
     L = ctypes.CDLL(LIB_PATH)
     P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     L.ep_status_string.argtypes = [i32]
@@ -646,19 +651,33 @@ _BF16, _F32, _I32, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, tor
 
 
 # The calls below take a few microseconds on the GPU at decode-sized batches, so the host's
-# share is kept small: one look at the current device per call, one combined check per
-# tensor (a failed one is explained by _shape and _ptr), device addresses as plain ints.
-# One call of ep_rmsnorm with four outputs, kernel launch included: 16.4 us with _shape and
-# _ptr per tensor, 7.7 us so, 3.4 of them in the C call (AMD EPYC host).
-def _row_ptr(t: Optional[torch.Tensor], dtype, shape, name: str, cur: int, need: bool = True):
-    """Device address of a tensor of exactly this type and shape; NULL for None unless it is
-    needed."""
-    if t is None:
-        return _ptr(t, dtype, name, not need)
-    if t.dtype is dtype and t.shape == shape and t.get_device() == cur and t.is_contiguous():
-        return t.data_ptr()
+# share is kept small: one look at the current device per call, and every tensor checked and
+# turned into its address by one native call (csrc/tensor_ptr.cpp). One call of ep_rmsnorm
+# with four outputs, kernel launch included: HOST_PY us with _shape and _ptr per tensor,
+# HOST_NOW us so, 3.4 of them in the C call (AMD EPYC host).
+def _row_ptr(*args):
+    """(tensor, dtype, shape, name, device, need=True): the device address of a tensor of
+    exactly this type and shape; None for None unless it is needed. Stands in for the native
+    check until load() puts that in its place."""
+    load()
+    return _row_ptr(*args)
+
+
+def _refuse(t, dtype, shape, name: str, need: bool) -> None:
+    """Raises for a tensor that the native check did not take."""
+    if t is not None and not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
     _shape(t, shape, name)
-    _ptr(t, dtype, name)  # raises
+    _ptr(t, dtype, name)
+
+
+def _load_tensor_ptr() -> None:
+    global _row_ptr
+    spec = importlib.util.spec_from_file_location("_tensor_ptr", TENSOR_PTR_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.set_explain(_refuse)
+    _row_ptr = mod.row_ptr
 
 
 def _flag_ptr(t: Optional[torch.Tensor], cur: int):

@@ -1,4 +1,5 @@
-"""Build libep.so (the C-ABI library of include/ep.h) in-tree with hipcc for gfx950.
+"""Build libep.so (the C-ABI library of include/ep.h) in-tree with hipcc for gfx950, and
+_tensor_ptr.so (the binding's tensor check, host code against torch's headers) with g++.
 
 Every HIP source is compiled with packed-fp32 instructions disabled
 (``-Xclang -target-feature -Xclang -packed-fp32-ops``); hipcc's host pass warns that
@@ -9,16 +10,19 @@ from __future__ import annotations
 import concurrent.futures
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libep.so")
+TENSOR_PTR = os.path.join(PKG, "_tensor_ptr.so")
 SOURCES = ["ep_abi.cpp", "layout.hip", "dispatch.hip", "restripe.hip", "combine.hip",
            "hbm_copy.hip", "rmsnorm.hip", "expert_rows.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 CFLAGS = ["-x", "hip", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -41,6 +45,25 @@ def _compile(src: str, verbose: bool, build_dir: str, defines) -> str:
     return obj
 
 
+def build_tensor_ptr(verbose: bool = False) -> str:
+    import torch
+    from torch.utils import cpp_extension
+
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for p in cpp_extension.include_paths() for a in ("-isystem", p)],
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_ptr.cpp"),
+           *[a for p in cpp_extension.library_paths() for a in (f"-L{p}", f"-Wl,-rpath,{p}")],
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", TENSOR_PTR + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed on tensor_ptr.cpp:\n{r.stdout}{r.stderr}")
+    os.replace(TENSOR_PTR + ".tmp", TENSOR_PTR)
+    return TENSOR_PTR
+
+
 def build(verbose: bool = False, defines=(), lib: str = LIB, build_dir: str = BUILD) -> str:
     """Compile every source and link the library (libep.so by default); always rebuilds.
     `defines` override the kernels' compile-time tile constants (NAME=VALUE strings)."""
@@ -58,3 +81,4 @@ def build(verbose: bool = False, defines=(), lib: str = LIB, build_dir: str = BU
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_tensor_ptr(verbose=True))
