@@ -447,15 +447,24 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_grad_row_kernel(
 // half waves every 32nd row each, joined in their order.
 constexpr int kSumCols = 32;
 constexpr int kSumRows = kMaxWaves * kWave / kSumCols;
+constexpr int kSumLoads = 8;  // in flight per lane: every row of 256 blocks
 __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_dw_sum_kernel(const float* part, int H,
                                                                           int rows, float* dw) {
     __shared__ float acc[kSumRows][kSumCols];
     const int x = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
     const int c = static_cast<int>(blockIdx.x) * kSumCols + x;
+    // loads past the last row are zeros: no load waits behind a branch or a loop's rest
+    const __amdgpu_buffer_rsrc_t pb =
+        raw_buffer(part, static_cast<uint32_t>(rows) * static_cast<uint32_t>(H) * 4u);
     float s = 0.0f;
-    if (c < H) {
-#pragma unroll 8
-        for (int p = r; p < rows; p += kSumRows) s += part[static_cast<int64_t>(p) * H + c];
+    for (int p0 = r; p0 < rows; p0 += kSumRows * kSumLoads) {
+        float v[kSumLoads];
+#pragma unroll
+        for (int i = 0; i < kSumLoads; ++i)
+            v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                pb, ((p0 + i * kSumRows) * H + min(c, H - 1)) * 4, 0, 0));
+#pragma unroll
+        for (int i = 0; i < kSumLoads; ++i) s += v[i];
     }
     acc[r][x] = s;
     __syncthreads();
