@@ -43,7 +43,9 @@ hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
 // its share of a line; past about half of the L2s' 32 MB they are evicted half-filled, and
 // non-temporal stores take over. Measured, cached against non-temporal: 46.0 against
 // 51.5 us at 4096 tokens (7 MB of scales), 93.3 against 103.4 us at 8192 (15 MB), 172.8
-// against 152.1 us at 12000 (22 MB), 236.6 against 229.3 us at 16384 (29 MB).
+// against 152.1 us at 12000 (22 MB), 236.6 against 229.3 us at 16384 (29 MB). Blocks dealt so
+// that each XCD writes an eighth of the rows, and its L2 gathers whole lines, took 59.9 us at
+// 4096 tokens, since a token's row is then fetched by five XCDs instead of two.
 constexpr int64_t kCachedScaleBytes = int64_t{16} << 20;
 
 template <int WPL, bool kMulti, int kScalePolicy>
