@@ -221,6 +221,55 @@ def test_permute_fp8_of_many_scales(T, H, k):
     assert not px[left].any() and not ps[left].any() and torch.all(pi[left] == -1)
 
 
+def test_calls_of_several_launches():
+    """More than 2^24 waves: each call runs over several token ranges. Small integers and
+    weights that are powers of two, so that every result is exact."""
+    print("\ncase: several launches per call", flush=True)
+    g = gen(31)
+
+    def ints(*shape):
+        return torch.randint(-8, 9, shape, generator=g, device="cuda").to(BF16)
+
+    def pow2(*shape):
+        return torch.randint(-1, 2, shape, generator=g, device="cuda").float().exp2()
+
+    T, H = 17_000_001, 8  # one wave per token
+    slot = torch.randperm(T, generator=g, device="cuda").to(torch.int32).reshape(T, 1)
+    slot[5::11] = -1
+    rows, w, hit = ints(T, H), pow2(T, 1), slot[:, 0] >= 0
+    want = torch.where(hit[:, None], rows[slot[:, 0].clamp(min=0).long()].float() * w, 0.0).to(BF16)
+    out = sentinel(T, H)
+    ep.ep_combine_unpermute(rows, w, slot, out=out)
+    assert torch.equal(out, want)
+    del out, want, rows, slot, w, hit
+
+    T, k, H = 2_100_001, 8, 8  # eight waves per token
+    slot = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).reshape(T, k)
+    slot[3::7, 2] = -1
+    rows, go, w = ints(T * k, H), ints(T, H), pow2(T, k)
+    gr, gw = torch.zeros((T * k, H), dtype=BF16, device="cuda"), torch.full((T, k), 99.0, device="cuda")
+    ep.ep_combine_unpermute_grad(go, rows, w, slot, grad_expert_out=gr, grad_topk_weights=gw)
+    for j in range(k):
+        t = torch.nonzero(slot[:, j] >= 0).squeeze(1)
+        q = slot[t, j].long()
+        assert torch.equal(gr[q], (go[t].float() * w[t, j, None]).to(BF16))
+        assert torch.equal(gw[t, j], (go[t].float() * rows[q].float()).sum(dim=1))
+    assert torch.all(gw[slot < 0] == 0)
+    del rows, go, gr, gw
+
+    H = 128
+    x = torch.randint(0, 256, (T, H), generator=g, device="cuda").to(torch.uint8)
+    sc = torch.rand((T, 1), generator=g, device="cuda")
+    px = torch.zeros((T * k, H), dtype=torch.uint8, device="cuda")
+    ps = torch.zeros((T * k, 1), device="cuda")
+    pi = torch.full((T * k,), -1, dtype=torch.int32, device="cuda")
+    ep.ep_dispatch_permute_fp8(x, sc, None, slot, perm_x_fp8=px, perm_scales=ps, perm_src_idx=pi)
+    for j in range(k):
+        t = torch.nonzero(slot[:, j] >= 0).squeeze(1)
+        q = slot[t, j].long()
+        assert torch.equal(px[q], x[t]) and torch.equal(ps[q], sc[t]) and torch.equal(pi[q].long(), t)
+
+
 def test_rows_out_of_range_are_skipped_and_reported():
     T, H, k = 50, 256, 4
     print("\ncase: rows out of range", flush=True)
