@@ -32,11 +32,17 @@ hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
     return hipSuccess;
 }
 
-// Wave (t, j) copies token t's codes and scales to row q, in the form of the bf16 permute:
-// the row's loads are issued before the slot arrives, the codes leave as one burst of
-// 128-bit stores (store_row_pass) and the token's other waves find the row in the L2.
-// HBM-write bound: 8 rows written per row read at top-8. 4096 tokens of 7168 channels over
+// Wave (t, d) copies token t's codes and scales to the rows of its pairs d kPairs ..
+// (d + 1) kPairs - 1, in the form of the bf16 permute: the row's loads are issued before the
+// slots arrive, the codes leave as one burst of 128-bit stores (store_row_pass) and the
+// token's other waves find the row in the L2. HBM-write bound: 8 rows written per row read at top-8. 4096 tokens of 7168 channels over
 // 256 experts: 46.1-46.9 us, 5.9 TB/s; guarded stores in a loop 47.2 us.
+//
+// One pair per wave from 2176 channels on. Narrower rows would be bound by the rate at which
+// waves start, about four per nanosecond, so a wave takes two pairs, and up to 1024 channels
+// four. Measured at 12000 tokens, top-8, with one, two and four: 24.5, 18.1, 15.8 us at 256
+// channels; 27.0, 21.8, 21.0 at 1024; 32.1, 28.6, 29.9 at 1536; 38.9, 38.4, 39.9 at 2048; 75.8,
+// 76.4, 77.8 at 4096.
 //
 // A row's scales (224 bytes at 7168 channels) fill no whole cache line, so neighbouring rows,
 // written by waves of different XCDs, share lines. Cached scale stores let each L2 gather
@@ -48,7 +54,7 @@ hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
 // 4096 tokens, since a token's row is then fetched by five XCDs instead of two.
 constexpr int64_t kCachedScaleBytes = int64_t{16} << 20;
 
-template <int WPL, bool kMulti, int kScalePolicy>
+template <int WPL, bool kMulti, int kScalePolicy, int kPairs>
 __global__ __launch_bounds__(kT) void permute_fp8_kernel(
     const u32x4* __restrict__ codes, const float* __restrict__ scales,
     const float* __restrict__ topk_w, int64_t t0, int64_t t_end, int V, int G, int k,
@@ -56,35 +62,45 @@ __global__ __launch_bounds__(kT) void permute_fp8_kernel(
     float* __restrict__ perm_scales, float* __restrict__ perm_w, int32_t* __restrict__ perm_src,
     int64_t cap, int32_t* __restrict__ error_flag) {
     int64_t t;
-    int j;
-    if (!dest_wave<kT>(t0, t_end, D, t, j)) return;
+    int d;
+    if (!dest_wave<kT>(t0, t_end, D, t, d)) return;
     const int lane = lane_id();
-    const int64_t q = expert_slot[t * k + j];
-    const float w = perm_w ? topk_w[t * k + j] : 0.0f;
+    int32_t q[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const int j = d * kPairs + i;
+        q[i] = kPairs == 1 || j < k ? expert_slot[t * k + min(j, k - 1)] : -1;
+    }
     const u32x4* xr = codes + t * V;
     const float* sr = scales + t * G;
     u32x4 v[WPL];
-    load_row_cached(v, xr, 0, V);  // first pass, issued before the slot is known
-    float s = sr[min(lane, G - 1)];
-    if (q < 0) return;
-    if (q >= cap) {
-        if (lane == 0) raise_error(error_flag, kErrRecvOverflow);
-        return;
-    }
-    u32x4* row = perm_codes + q * V;
-    for (int v0 = 0; v0 < V; v0 += kWave * WPL) {
-        if (v0 != 0) load_row_cached(v, xr, v0, V);
-        store_row_pass(row, V, v0, v);
-        if constexpr (!kMulti) break;
-    }
-    const __amdgpu_buffer_rsrc_t sb = raw_buffer(perm_scales + q * G, static_cast<uint32_t>(G) * 4u);
-    for (int g = lane; g - lane < G; g += kWave) {  // stores past G are dropped
-        if (g != lane) s = sr[min(g, G - 1)];
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), sb, g * 4, 0, kScalePolicy);
-    }
-    if (lane == 0) {
-        if (perm_w) perm_w[q] = w;
-        if (perm_src) perm_src[q] = static_cast<int32_t>(t);
+    load_row_cached(v, xr, 0, V);  // first pass, issued before the slots are known
+    const float s0 = sr[min(lane, G - 1)];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        if (q[i] < 0) continue;
+        if (q[i] >= cap) {
+            if (lane == 0) raise_error(error_flag, kErrRecvOverflow);
+            continue;
+        }
+        const int64_t qi = q[i];
+        u32x4* row = perm_codes + qi * V;
+        for (int v0 = 0; v0 < V; v0 += kWave * WPL) {
+            if (v0 != 0) load_row_cached(v, xr, v0, V);
+            store_row_pass(row, V, v0, v);
+            if constexpr (!kMulti) break;
+        }
+        const __amdgpu_buffer_rsrc_t sb =
+            raw_buffer(perm_scales + qi * G, static_cast<uint32_t>(G) * 4u);
+        float s = s0;
+        for (int g = lane; g - lane < G; g += kWave) {  // stores past G are dropped
+            if (g != lane) s = sr[min(g, G - 1)];
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), sb, g * 4, 0, kScalePolicy);
+        }
+        if (lane == 0) {
+            if (perm_w) perm_w[qi] = topk_w[t * k + d * kPairs + i];
+            if (perm_src) perm_src[qi] = static_cast<int32_t>(t);
+        }
     }
 }
 
@@ -266,20 +282,31 @@ hipError_t launch_dispatch_permute_fp8(const void* x_fp8, const float* x_scales,
                                        float* perm_scales, float* perm_w, int32_t* perm_src,
                                        int64_t cap, int32_t* error_flag, hipStream_t stream) {
     const int V = H / 16, G = H / kNormGroup;
-    const FastDiv fd = FastDiv::make(k);
     const bool cached = T * k * G * static_cast<int64_t>(sizeof(float)) <= kCachedScaleBytes;
-    return by_token_range<kT>(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
-        with_row_width<14, false>(V, [&](auto wpl, auto multi) {
-            constexpr int w = decltype(wpl)::value;
-            constexpr bool m = decltype(multi)::value;
-            const auto kernel = cached ? permute_fp8_kernel<w, m, 0>
-                                       : permute_fp8_kernel<w, m, kPolicyNt>;
-            hipLaunchKernelGGL(kernel, dim3(grid), dim3(kT), 0, stream,
-                               static_cast<const u32x4*>(x_fp8), x_scales, topk_w, t0, t_end, V, G,
-                               k, expert_slot, fd, static_cast<u32x4*>(perm_x), perm_scales,
-                               perm_w, perm_src, cap, error_flag);
+    const auto with = [&](auto pairs) {
+        constexpr int n = decltype(pairs)::value;
+        const int waves = (k + n - 1) / n;
+        const FastDiv fd = FastDiv::make(waves);
+        return by_token_range<kT>(T, waves, [&](int64_t t0, int64_t t_end, unsigned grid) {
+            with_row_width<14, false>(V, [&](auto wpl, auto multi) {
+                constexpr int w = decltype(wpl)::value;
+                constexpr bool m = decltype(multi)::value;
+                // the widths that take n pairs per wave: one word per lane four, two words two
+                if constexpr (n == (w == 1 ? 4 : w == 2 ? 2 : 1)) {
+                    const auto kernel = cached ? permute_fp8_kernel<w, m, 0, n>
+                                               : permute_fp8_kernel<w, m, kPolicyNt, n>;
+                    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kT), 0, stream,
+                                       static_cast<const u32x4*>(x_fp8), x_scales, topk_w, t0,
+                                       t_end, V, G, k, expert_slot, fd,
+                                       static_cast<u32x4*>(perm_x), perm_scales, perm_w, perm_src,
+                                       cap, error_flag);
+                }
+            });
         });
-    });
+    };
+    if (V <= kWave) return with(std::integral_constant<int, 4>{});
+    if (V <= 2 * kWave) return with(std::integral_constant<int, 2>{});
+    return with(std::integral_constant<int, 1>{});
 }
 
 static hipError_t launch_unpermute(const void* rows, int64_t num_rows, const float* topk_w,
