@@ -35,8 +35,8 @@ hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
 // Wave (t, d) copies token t's codes and scales to the rows of its pairs d kPairs ..
 // (d + 1) kPairs - 1, in the form of the bf16 permute: the row's loads are issued before the
 // slots arrive, the codes leave as one burst of 128-bit stores (store_row_pass) and the
-// token's other waves find the row in the L2. HBM-write bound: 8 rows written per row read at top-8. 4096 tokens of 7168 channels over
-// 256 experts: 46.1-46.9 us, 5.9 TB/s; guarded stores in a loop 47.2 us.
+// token's other waves find the row in the L2. HBM-write bound: 8 rows written per row read at
+// top-8. 4096 tokens of 7168 channels over 256 experts: 46.1-46.9 us, 5.9 TB/s; guarded stores in a loop 47.2 us.
 //
 // One pair per wave from 2176 channels on. Narrower rows would be bound by the rate at which
 // waves start, about four per nanosecond, so a wave takes two pairs, and up to 1024 channels
