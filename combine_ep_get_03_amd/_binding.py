@@ -640,12 +640,6 @@ def ep_combine_recv(stage, node_slot, *, out, error_flag=None, stream=None) -> N
         _stream(stream)), "ep_combine_recv")
 
 
-def _rows_2d(t: torch.Tensor, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
-    return t.shape
-
-
 _BF16, _F32, _I32, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
                                  torch.float8_e4m3fn)
 
@@ -653,7 +647,7 @@ _BF16, _F32, _I32, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, tor
 # The calls below take a few microseconds on the GPU at decode-sized batches, so the host's
 # share is kept small: one look at the current device per call, and every tensor checked and
 # turned into its address by one native call (csrc/tensor_ptr.cpp). One call of ep_rmsnorm
-# with four outputs, kernel launch included: 16.4 us with _shape and _ptr per tensor, 5.8 us
+# with four outputs, kernel launch included: 16.4 us with _shape and _ptr per tensor, 5.5 us
 # so, about 3.5 of them in the C call (AMD EPYC host).
 def _row_ptr(*args):
     """(tensor, dtype, shape, name, device, need=True): the device address of a tensor of
@@ -663,29 +657,34 @@ def _row_ptr(*args):
     return _row_ptr(*args)
 
 
+def _rows_2d(*args):
+    """(tensor, name): the sizes of a tensor of two dimensions; as _row_ptr."""
+    load()
+    return _rows_2d(*args)
+
+
 def _refuse(t, dtype, shape, name: str, need: bool) -> None:
     """Raises for a tensor that the native check did not take."""
-    if t is not None and not isinstance(t, torch.Tensor):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
-    _shape(t, shape, name)
+    if dtype is None:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
+    if shape is None:
+        _at_least(t, 1, name)
+    else:
+        _shape(t, shape, name)
     _ptr(t, dtype, name)
 
 
 def _load_tensor_ptr() -> None:
-    global _row_ptr
+    global _row_ptr, _rows_2d
     spec = importlib.util.spec_from_file_location("_tensor_ptr", TENSOR_PTR_PATH)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.set_explain(_refuse)
-    _row_ptr = mod.row_ptr
-
-
-def _flag_ptr(t: Optional[torch.Tensor], cur: int):
-    """Device address of the error flag (one int32 or more), or NULL."""
-    if t is None:
-        return None
-    _at_least(t, 1, "error_flag")
-    return _row_ptr(t, _I32, t.shape, "error_flag", cur)
+    _row_ptr, _rows_2d = mod.row_ptr, mod.dims2
 
 
 def _current(stream):
@@ -693,7 +692,7 @@ def _current(stream):
     the first use of the GPU."""
     if not torch.cuda.is_initialized():
         return -2, None
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()
     return cur, torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
 
 
@@ -741,9 +740,9 @@ def ep_rmsnorm_grad(grad_y, h, weight, *, grad_x, grad_residual_out=None, grad_w
     rows = T, H = _rows_2d(h, "h")
     cur, st = _current(stream)
     w, w_fp32 = _norm_weight(weight, H, cur)
-    ws_shape = () if workspace is None else workspace.shape
-    ws = _row_ptr(workspace, _U8, ws_shape, "workspace", cur, False)
-    ws_bytes = 0 if workspace is None else workspace.numel()
+    ws, ws_bytes = None, 0
+    if workspace is not None:  # empty where there are no tokens
+        ws, ws_bytes = _row_ptr(workspace, _U8, workspace.shape, "workspace", cur), workspace.numel()
     _check(load().ep_rmsnorm_grad(
         _row_ptr(grad_y, _BF16, rows, "grad_y", cur),
         _row_ptr(grad_residual_out, _BF16, rows, "grad_residual_out", cur, False),
@@ -773,7 +772,7 @@ def ep_dispatch_permute_fp8(x_fp8, x_scales, topk_weights, expert_slot, *, perm_
         _row_ptr(perm_scales, _F32, (cap, G), "perm_scales", cur),
         _row_ptr(perm_weights, _F32, (cap,), "perm_weights", cur, False),
         _row_ptr(perm_src_idx, _I32, (cap,), "perm_src_idx", cur, False), cap,
-        _flag_ptr(error_flag, cur), st), "ep_dispatch_permute_fp8")
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_dispatch_permute_fp8")
 
 
 def ep_combine_unpermute(expert_out, topk_weights, expert_slot, *, out, addend=None,
@@ -790,7 +789,8 @@ def ep_combine_unpermute(expert_out, topk_weights, expert_slot, *, out, addend=N
         T, H, k,
         _row_ptr(expert_slot, _I32, (T, k), "expert_slot", cur),
         _row_ptr(addend, _BF16, (T, H), "addend", cur, False),
-        _row_ptr(out, _BF16, (T, H), "out", cur), _flag_ptr(error_flag, cur), st),
+        _row_ptr(out, _BF16, (T, H), "out", cur),
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st),
         "ep_combine_unpermute")
 
 
@@ -814,7 +814,8 @@ def ep_combine_unpermute_grad(grad_out, expert_out, topk_weights, expert_slot, *
         _row_ptr(expert_slot, _I32, (T, k), "expert_slot", cur),
         _row_ptr(grad_expert_out, _BF16, (rows, H), "grad_expert_out", cur),
         _row_ptr(grad_topk_weights, _F32, (T, k), "grad_topk_weights", cur, False),
-        _flag_ptr(error_flag, cur), st), "ep_combine_unpermute_grad")
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st),
+        "ep_combine_unpermute_grad")
 
 
 def ep_dispatch_permute_grad(grad_perm_x, expert_slot, *, grad_x, grad_perm_weights=None,
@@ -832,7 +833,7 @@ def ep_dispatch_permute_grad(grad_perm_x, expert_slot, *, grad_x, grad_perm_weig
         rows, T, H, k, _row_ptr(expert_slot, _I32, (T, k), "expert_slot", cur),
         _row_ptr(grad_x, _BF16, (T, H), "grad_x", cur),
         _row_ptr(grad_topk_weights, _F32, (T, k), "grad_topk_weights", cur, False),
-        _flag_ptr(error_flag, cur), st), "ep_dispatch_permute_grad")
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_dispatch_permute_grad")
 
 
 def ep_hbm_copy(src, dst, nbytes: Optional[int] = None, stream=None) -> None:

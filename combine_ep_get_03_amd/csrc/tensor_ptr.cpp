@@ -3,11 +3,14 @@
 // ctypes over libep.so.
 //
 //   row_ptr(tensor, dtype, shape, name, device, need=True) -> int or None
+//   dims2(tensor, name) -> (rows, columns)
 //
-// The address of a dense tensor of exactly this type and shape on this device; None for None
-// unless it is needed. Anything else goes to the callable given to set_explain, with the same
-// arguments but the device, which raises. A check costs 0.1 us here and 0.43 us as five
-// attribute and method calls in Python, and a call of the norm makes eight of them.
+// row_ptr: the address of a dense tensor of exactly this type and shape (None: any shape of
+// one element or more) on this device; None for None unless it is needed. dims2: the sizes of
+// a tensor of two dimensions. Anything else goes to the callable given to set_explain, which
+// raises, with the same arguments but the device (from dims2 with None for what it does not
+// have). A check costs 0.1 us here and 0.43 us as five attribute and method calls in Python,
+// and a call of the norm makes eight of them.
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -33,6 +36,7 @@ PyObject* complain(PyObject* tensor, PyObject* dtype, PyObject* shape, PyObject*
 
 // 1 if the tensor has exactly this shape, 0 if not, -1 with a Python error set.
 int same_shape(const at::Tensor& t, PyObject* shape) {
+    if (shape == Py_None) return t.numel() >= 1;
     if (!PyTuple_Check(shape)) return 0;
     const Py_ssize_t n = PyTuple_GET_SIZE(shape);
     if (n != t.dim()) return 0;
@@ -51,7 +55,8 @@ PyObject* row_ptr(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     PyObject* need = n == 6 ? a[5] : Py_True;
     if (a[0] == Py_None && need != Py_True) Py_RETURN_NONE;
-    if (!THPVariable_Check(a[0]) || !THPDtype_Check(a[1])) return complain(a[0], a[1], a[2], a[3], need);
+    if (!THPVariable_Check(a[0]) || !THPDtype_Check(a[1]))
+        return complain(a[0], a[1], a[2], a[3], need);
     const long device = PyLong_AsLong(a[4]);
     if (device == -1 && PyErr_Occurred()) return nullptr;
     try {  // a tensor without plain storage (sparse, fake) throws on some of these
@@ -67,6 +72,23 @@ PyObject* row_ptr(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return complain(a[0], a[1], a[2], a[3], need);
 }
 
+PyObject* dims2(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 2) {
+        PyErr_SetString(PyExc_TypeError, "dims2(tensor, name)");
+        return nullptr;
+    }
+    if (THPVariable_Check(a[0])) {
+        try {
+            const at::Tensor& t = THPVariable_Unpack(a[0]);
+            if (t.dim() == 2)
+                return Py_BuildValue("(LL)", static_cast<long long>(t.size(0)),
+                                     static_cast<long long>(t.size(1)));
+        } catch (const std::exception&) {
+        }
+    }
+    return complain(a[0], Py_None, Py_None, a[1], Py_True);
+}
+
 PyObject* set_explain(PyObject*, PyObject* f) {
     Py_INCREF(f);
     Py_XSETREF(explain, f);
@@ -76,6 +98,8 @@ PyObject* set_explain(PyObject*, PyObject* f) {
 PyMethodDef methods[] = {
     {"row_ptr", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(row_ptr)),
      METH_FASTCALL, "row_ptr(tensor, dtype, shape, name, device, need=True) -> int or None"},
+    {"dims2", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(dims2)), METH_FASTCALL,
+     "dims2(tensor, name) -> (rows, columns)"},
     {"set_explain", set_explain, METH_O, "the callable that refuses a tensor"},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -333,6 +333,30 @@ def test_error_bits_are_added_to_the_flag():
     assert int(err) == ep.EP_DEVERR_TOPK_RANGE | ep.EP_DEVERR_SLOT_RANGE
 
 
+def test_refusals_of_the_binding():
+    T, H, k = 4, 64, 2
+    g, cap, slot, rows, w = case(33, T, H, k, dropped=0.0, empty_tokens=False)
+    out = sentinel(T, H)
+    for kw, exc in ((dict(error_flag=torch.zeros(1, device="cuda")), TypeError),
+                    (dict(error_flag=torch.zeros(0, dtype=torch.int32, device="cuda")), ValueError),
+                    (dict(error_flag=torch.zeros(1, dtype=torch.int32)), ValueError),
+                    (dict(addend=out[:2]), ValueError), (dict(addend=out.float()), TypeError)):
+        with pytest.raises(exc):
+            ep.ep_combine_unpermute(rows, w, slot, out=out, **kw)
+    for args in ((rows, w.t().contiguous().t(), slot), (rows, w, slot.long()), (rows, w.cpu(), slot),
+                 (rows[:, ::2], w, slot), (rows.view(-1), w, slot), (None, w, slot), (rows, w, 3)):
+        with pytest.raises((ValueError, TypeError)):
+            ep.ep_combine_unpermute(*args, out=out)
+    torch.cuda.synchronize()
+    assert torch.all(out.view(torch.int16) == SENT)  # nothing ran
+    ep.ep_combine_unpermute(rows, torch.nn.Parameter(w.clone()), slot, out=out,
+                            error_flag=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    s, r = slot.cpu(), P.f64(rows)
+    r0 = torch.where(torch.isnan(r), torch.zeros((), dtype=torch.float64), r)
+    want = P.unpermute(r, P.f64(w), s, None)
+    P.assert_within(out, want, P.unpermute_bound(want, r0, P.f64(w), s, None), "out")
+
+
 def test_no_rows_and_no_tokens():
     T, H, k = 5, 128, 3
     slot = torch.full((T, k), -1, dtype=torch.int32, device="cuda")

@@ -344,6 +344,10 @@ def test_no_tokens():
     dw = torch.full((H,), 5.0, device="cuda")
     ep.ep_rmsnorm_grad(x, x, w, grad_x=torch.empty_like(x), grad_weight=dw)
     assert torch.all(dw == 0)
+    dw.fill_(5.0)
+    ep.ep_rmsnorm_grad(x, x, w, grad_x=torch.empty_like(x), grad_weight=dw,
+                       workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    assert torch.all(dw == 0)
     assert ep.ep_rmsnorm_grad_workspace_bytes(0, H) == 0
 
 
