@@ -16,8 +16,8 @@ constexpr int kT = 256;  // threads per block: a few waves, each with its own pi
 constexpr int kUnpermuteThreads = 128;
 constexpr int64_t kMaxWaves = int64_t{1} << 24;  // per launch: a wave's index stays 32 bits
 
-// Launches f(t0, t_end, grid) over token ranges of at most kMaxWaves waves, kThreads / 64 of
-// them per block.
+// f(t0, t_end, grid) launches over token ranges of at most kMaxWaves waves, kThreads / 64 of
+// them per block, and returns its launch's status; the first failure ends the call.
 template <int kThreads, typename F>
 hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
     constexpr int kWaves = kThreads / kWave;
@@ -26,8 +26,8 @@ hipError_t by_token_range(int64_t T, int waves_per_token, F&& f) {
         const int64_t t_end = std::min(T, t0 + step);
         const int64_t grid = ((t_end - t0) * waves_per_token + kWaves - 1) / kWaves;
         if (!grid_fits(grid, kThreads)) return hipErrorInvalidConfiguration;
-        f(t0, t_end, static_cast<unsigned>(grid));
-        EP_RETURN_IF_LAUNCH_FAILED();
+        const hipError_t e = f(t0, t_end, static_cast<unsigned>(grid));
+        if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
@@ -288,7 +288,7 @@ hipError_t launch_dispatch_permute_fp8(const void* x_fp8, const float* x_scales,
         const int waves = (k + n - 1) / n;
         const FastDiv fd = FastDiv::make(waves);
         return by_token_range<kT>(T, waves, [&](int64_t t0, int64_t t_end, unsigned grid) {
-            with_row_width<14, false>(V, [&](auto wpl, auto multi) {
+            return with_row_width<14, false>(V, [&](auto wpl, auto multi) {
                 constexpr int w = decltype(wpl)::value;
                 constexpr bool m = decltype(multi)::value;
                 // the widths that take n pairs per wave: one word per lane four, two words two
@@ -324,6 +324,7 @@ static hipError_t launch_unpermute(const void* rows, int64_t num_rows, const flo
                            static_cast<const u32x4*>(rows), num_rows, topk_w, expert_slot, t0,
                            t_end, V, k, fd, static_cast<const u32x4*>(addend),
                            static_cast<u32x4*>(out), grad_perm_w, grad_w, error_flag);
+        return hipGetLastError();
     });
 }
 
@@ -355,7 +356,7 @@ hipError_t launch_combine_unpermute_grad(const void* grad_out, const void* rows,
         constexpr int ld = decltype(load)::value, st = decltype(store)::value;
         constexpr int n = decltype(threads)::value;
         return by_token_range<n>(T, k, [&](int64_t t0, int64_t t_end, unsigned grid) {
-            with_row_width<decltype(width)::value, false>(V, [&](auto wpl, auto) {
+            return with_row_width<decltype(width)::value, false>(V, [&](auto wpl, auto) {
                 hipLaunchKernelGGL((unpermute_grad_kernel<decltype(wpl)::value, d, r, ld, st, n>),
                                    dim3(grid), dim3(n), 0, stream,
                                    static_cast<const u32x4*>(grad_out),

@@ -122,6 +122,29 @@ def test_expert_rows_pointer_refusals(lib):
             assert f(lib, **{name: MIS}) == ep.EP_ERR_ALIGN, (f.__name__, name)
 
 
+@pytest.mark.skipif(torch.cuda.is_available() or os.path.exists("/dev/kfd"),
+                    reason="the stand-in pointers are only safe where no kernel can start")
+def test_a_launch_that_fails_is_reported(lib):
+    """Without a GPU every launch fails: each call that gets past its checks says so, in each
+    of its forms."""
+    big = 1 << 40
+    for kw in (dict(), dict(H=64, c=None, s=None), dict(H=1024), dict(H=2048), dict(H=32768),
+               dict(H=40960), dict(T=5_000_000, H=1024)):
+        assert norm(lib, **kw) == ep.EP_ERR_HIP, kw
+    for kw in (dict(), dict(dw=None), dict(T=5000, H=8192), dict(H=40960), dict(H=40960, dw=None),
+               dict(T=1, H=64), dict(T=0)):
+        assert norm_grad(lib, wsb=big, **kw) == ep.EP_ERR_HIP, kw
+    for kw in (dict(), dict(H=2048), dict(H=8192), dict(H=40960), dict(T=100000, k=8, H=7168),
+               dict(T=2**24, k=8)):
+        assert perm8(lib, cap=2**40, **kw) == ep.EP_ERR_HIP, kw
+    for kw in (dict(), dict(k=1), dict(k=3), dict(k=8), dict(T=2**24 + 1, k=1)):
+        assert unperm(lib, n=2**40, **kw) == ep.EP_ERR_HIP, kw
+        assert perm_grad(lib, n=2**40, **kw) == ep.EP_ERR_HIP, kw
+    for kw in (dict(), dict(gw=None), dict(T=5000, k=8, H=7168), dict(T=3000, k=2),
+               dict(T=2**22, k=8)):
+        assert unperm_grad(lib, n=2**40, **kw) == ep.EP_ERR_HIP, kw
+
+
 def test_binding_refuses_shapes_types_and_host_tensors():
     T, H, k = 4, 256, 2
     x = torch.zeros((T, H), dtype=torch.bfloat16)
