@@ -533,8 +533,9 @@ int ep_rmsnorm(const void *x, const void *residual, const void *weight, int weig
                float eps, int64_t num_tokens, int hidden, void *residual_out, void *y,
                uint8_t *y_fp8, float *y_scales, void *stream);
 
-/* Bytes of device workspace ep_rmsnorm_grad needs when grad_weight is asked for. Returns 0
- * when num_tokens == 0 and for sizes ep_rmsnorm_grad rejects. */
+/* Bytes of device workspace ep_rmsnorm_grad needs when grad_weight is asked for; never less
+ * for more tokens of the same hidden size. Returns 0 when num_tokens == 0 and for sizes
+ * ep_rmsnorm_grad rejects. */
 size_t ep_rmsnorm_grad_workspace_bytes(int64_t num_tokens, int hidden);
 
 /* ep_rmsnorm_grad -- the gradient of y = norm(h) * weight and of the residual's addition,

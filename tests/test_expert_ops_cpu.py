@@ -70,6 +70,10 @@ def test_norm_grad_workspace_query(lib):
     assert ep.ep_rmsnorm_grad_workspace_bytes(0, 256) == 0
     for T, H in [(-1, 256), (4, 0), (4, 252), (4, 2**30), (2**31, 256)]:
         assert ep.ep_rmsnorm_grad_workspace_bytes(T, H) == 0
+    for H in (8, 512, 1024, 2056, 7168, 16384, 40960):  # enough for a larger batch is enough
+        sizes = [ep.ep_rmsnorm_grad_workspace_bytes(T, H) for T in
+                 [*range(1, 1100), 2047, 2048, 2049, 4096, 4099, 100000]]
+        assert sizes == sorted(sizes), H
     for T in (1, 100, 4096, 100000):
         assert 0 < ep.ep_rmsnorm_grad_workspace_bytes(T, 7168) < 64 << 20
 

@@ -306,6 +306,19 @@ def test_grad_of_a_row_of_zeros_and_a_nan_row():
     check_grad(dy[rest], None, h[rest], w, dx[rest], None)
 
 
+@pytest.mark.parametrize("H", [64, 1024, 7168])
+def test_grad_of_shorter_batches_in_the_longest_ones_workspace(H):
+    print(f"\ncase: rmsnorm_grad H={H}, one workspace for many lengths", flush=True)
+    g = gen(H)
+    w = weight_of(g, H, BF16)
+    ws = workspace(700, H)
+    for T in (700, 255, 256, 257, 1, 699, 512, 3, 513):
+        dy, h = rand(g, T, H), rand(g, T, H)
+        dx, dw = torch.zeros_like(h), torch.zeros(H, device="cuda")
+        ep.ep_rmsnorm_grad(dy, h, w, grad_x=dx, grad_weight=dw, workspace=ws, eps=EPS)
+        check_grad(dy, None, h, w, dx, dw)
+
+
 def test_grad_weight_off_the_16_byte_grid():
     """grad_weight needs 4-byte alignment only; one block's sum leaves in wide words where it
     may."""
