@@ -243,7 +243,7 @@ class ExpertPath:
     experts, top-k (k <= EP_EXPERT_SLOT_MAX_K; H a multiple of 128 with fp8=True).
 
         norm(x, weight, residual)        ep_rmsnorm: residual_out, y (and e4m3 with fp8=True)
-        dispatch(topk_idx, topk_weights) ep_get_layout with expert slots, then
+        dispatch(topk_idx)               ep_get_layout with expert slots, then
                                          ep_dispatch_permute, or with fp8=True
                                          ep_dispatch_permute_fp8, of the norm's output
         ... the caller's experts on rows expert_offset[e] .. expert_offset[e + 1] - 1 of
@@ -306,17 +306,17 @@ class ExpertPath:
                      y_scales=self.y_scales if self.fp8 else None, eps=self.eps, stream=stream)
         self.h = self.residual_out if with_sum else x
 
-    def dispatch(self, topk_idx, topk_weights=None, stream=None) -> None:
+    def dispatch(self, topk_idx, stream=None) -> None:
         """The layout of the batch and the norm's rows in expert-major order."""
         lb = self.layout_buf
         lb.compute(topk_idx, self.E, self.R, self.N, stream=stream)
         if self.fp8:
-            B.ep_dispatch_permute_fp8(self.y_fp8, self.y_scales, topk_weights, lb.expert_slot,
+            B.ep_dispatch_permute_fp8(self.y_fp8, self.y_scales, None, lb.expert_slot,
                                       perm_x_fp8=self.perm_x_fp8, perm_scales=self.perm_scales,
                                       perm_src_idx=self.perm_src_idx,
                                       error_flag=self.error_flag, stream=stream)
         else:
-            B.ep_dispatch_permute(self.y, topk_weights, lb.expert_slot, perm_x=self.perm_x,
+            B.ep_dispatch_permute(self.y, None, lb.expert_slot, perm_x=self.perm_x,
                                   perm_src_idx=self.perm_src_idx, error_flag=self.error_flag,
                                   stream=stream)
 

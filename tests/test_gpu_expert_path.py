@@ -67,7 +67,7 @@ def test_block_forward_and_backward(T, H, E, k, R, N):
     d = inputs(T + H, T, H, E, k)
     p = ExpertPath(T, H, E, k, R=R, N=N, training=True)
     p.norm(d["x"], d["weight"], d["residual"])
-    p.dispatch(d["idx"], d["gate"])
+    p.dispatch(d["idx"])
     M = int(p.expert_offset[-1])
     assert M == int((d["idx"] >= 0).sum())
     e = expert_rows(p.expert_offset, T, k, E)
@@ -159,7 +159,7 @@ def test_decode_loop_of_single_tokens():
         s, y = P.rmsnorm(P.f64(x), P.f64(res), P.f64(d["weight"]), p.eps)
         P.assert_within(p.y, y, P.y_bound(y), f"y of step {step}")
         idx = torch.rand((T, E), generator=gen(step), device="cuda").topk(k, dim=1).indices
-        p.dispatch(idx, d["gate"])
+        p.dispatch(idx)
         e = expert_rows(p.expert_offset, T, k, E)
         expert_out = experts(p.perm_x, e, d["scale"])
         p.combine(expert_out, d["gate"])
@@ -180,7 +180,7 @@ def test_training_step_replays_in_a_graph_beside_an_eager_one():
 
     def step(p):
         p.norm(d["x"], d["weight"], d["residual"])
-        p.dispatch(d["idx"], d["gate"])
+        p.dispatch(d["idx"])
         p.combine(p.perm_x, d["gate"], addend=d["shared"])
         p.combine_grad(d["grad_out"], p.perm_x, d["gate"])
         p.dispatch_grad(p.grad_expert_out)
@@ -220,7 +220,7 @@ def test_an_empty_batch():
     gate = torch.empty((0, 2), device="cuda")
     p.grad_weight.fill_(4.0)
     p.norm(x, w, x)
-    p.dispatch(torch.empty((0, 2), dtype=torch.int64, device="cuda"), gate)
+    p.dispatch(torch.empty((0, 2), dtype=torch.int64, device="cuda"))
     assert int(p.expert_offset[-1]) == 0
     p.combine(p.perm_x, gate)
     p.combine_grad(x, p.perm_x, gate)
@@ -241,7 +241,7 @@ def test_duplicate_and_bad_expert_ids():
     p = ExpertPath(T, H, E, k, training=True)
     p.norm(d["x"], d["weight"])
     assert p.h is d["x"]
-    p.dispatch(d["idx"], d["gate"])
+    p.dispatch(d["idx"])
     M = int(p.expert_offset[-1])
     assert M == T * k - 2 and int(p.error_flag) == ep.EP_DEVERR_TOPK_RANGE
     p.combine(p.perm_x, d["gate"])
