@@ -139,6 +139,29 @@ def test_norm_rows_of_zeros_infinities_and_nan():
     assert torch.isnan(codes[3].view(torch.float8_e4m3fn).float()).sum() == 1
 
 
+@pytest.mark.parametrize("H", [128, 1024, 7168, 40960])
+def test_codes_are_those_of_the_fp8_dispatch(H):
+    """Rows of +-1 with eps 0 have r = 1 and y = +-weight, exact in bf16: the norm's codes and
+    scales are then, bit for bit, what ep_dispatch_fp8 makes of y."""
+    T = 9
+    print(f"\ncase: codes against ep_dispatch_fp8 H={H}", flush=True)
+    g = gen(H + 3)
+    x = (torch.randint(0, 2, (T, H), generator=g, device="cuda") * 2 - 1).to(BF16)
+    w = (torch.randn(H, generator=g, device="cuda") * torch.randn(H, generator=g, device="cuda").exp()).to(BF16)
+    w[:128] = 0 if H > 128 else w[:128]
+    y = torch.zeros_like(x)
+    codes = torch.zeros((T, H), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((T, H // 128), device="cuda")
+    ep.ep_rmsnorm(x, w, y=y, y_fp8=codes, y_scales=scales, eps=0.0)
+    assert torch.equal(y.float(), x.float() * w.float())
+    slot = torch.arange(T, dtype=torch.int32, device="cuda").reshape(T, 1)
+    idx = torch.zeros((T, 1), dtype=torch.int64, device="cuda")
+    want, want_scales = torch.zeros_like(codes), torch.zeros_like(scales)
+    ep.ep_dispatch_fp8(y, idx, None, 1, 1, slot, recv_x_fp8=want, recv_scales=want_scales)
+    assert torch.equal(codes, want)
+    assert torch.equal(scales.view(torch.int32), want_scales.view(torch.int32))
+
+
 def test_norm_nan_weight_poisons_its_channel_alone():
     T, H = 3, 256
     g = gen(4)
