@@ -41,10 +41,8 @@ def load() -> ctypes.CDLL:
     global _lib
     if _lib is not None:
         return _lib
-    for path in (LIB_PATH, TENSOR_PTR_PATH):
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is not built; run __graft_entry__.build() first")
-    _load_tensor_ptr()
+    if not os.path.exists(LIB_PATH):
+        raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
     L = ctypes.CDLL(LIB_PATH)
     P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     L.ep_status_string.argtypes = [i32]
@@ -652,14 +650,14 @@ _BF16, _F32, _I32, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, tor
 def _row_ptr(*args):
     """(tensor, dtype, shape, name, device, need=True): the device address of a tensor of
     exactly this type and shape; None for None unless it is needed. Stands in for the native
-    check until load() puts that in its place."""
-    load()
+    check until the first use, which puts that in its place."""
+    _load_tensor_ptr()
     return _row_ptr(*args)
 
 
 def _rows_2d(*args):
     """(tensor, name): the sizes of a tensor of two dimensions; as _row_ptr."""
-    load()
+    _load_tensor_ptr()
     return _rows_2d(*args)
 
 
@@ -679,7 +677,11 @@ def _refuse(t, dtype, shape, name: str, need: bool) -> None:
 
 
 def _load_tensor_ptr() -> None:
+    """Loads _tensor_ptr.so, which is bound to one build of torch: apart from load(), so that
+    the calls without it need libep.so alone."""
     global _row_ptr, _rows_2d
+    if not os.path.exists(TENSOR_PTR_PATH):
+        raise RuntimeError(f"{TENSOR_PTR_PATH} is not built; run __graft_entry__.build() first")
     spec = importlib.util.spec_from_file_location("_tensor_ptr", TENSOR_PTR_PATH)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
