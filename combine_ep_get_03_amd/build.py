@@ -65,8 +65,10 @@ def build_tensor_ptr(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False, defines=(), lib: str = LIB, build_dir: str = BUILD) -> str:
-    """Compile every source and link the library (libep.so by default); always rebuilds.
-    `defines` override the kernels' compile-time tile constants (NAME=VALUE strings)."""
+    """Compile every source and link the library; always rebuilds. The package's own libep.so
+    (the default) comes with _tensor_ptr.so, which the binding's calls need beside it; a
+    library elsewhere is built alone. `defines` override the kernels' compile-time tile
+    constants (NAME=VALUE strings)."""
     os.makedirs(build_dir, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose, build_dir, defines), SOURCES))
@@ -76,9 +78,10 @@ def build(verbose: bool = False, defines=(), lib: str = LIB, build_dir: str = BU
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, lib)
+    if lib == LIB:
+        build_tensor_ptr(verbose)
     return lib
 
 
 if __name__ == "__main__":
     print(build(verbose=True))
-    print(build_tensor_ptr(verbose=True))

@@ -7,6 +7,7 @@ import sys
 import pytest
 
 from combine_ep_get_03_amd import _binding
+from combine_ep_get_03_amd import build as hip_build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -51,3 +52,21 @@ def test_only_the_calls_that_use_the_tensor_check_need_it():
     r = subprocess.run([sys.executable, "-c", WITHOUT_THE_TENSOR_CHECK], cwd=ROOT,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "done", r.stdout + r.stderr
+
+
+def test_building_the_library_builds_the_tensor_check(monkeypatch, tmp_path):
+    """One call makes all that the binding loads; a library elsewhere is built alone. The
+    compilers are a stand-in that creates its output."""
+    fake = tmp_path / "cc"
+    fake.write_text('#!/bin/sh\nwhile [ "$1" != -o ]; do shift; done\n: > "$2"\n')
+    fake.chmod(0o755)
+    lib, check = tmp_path / "libep.so", tmp_path / "_tensor_ptr.so"
+    monkeypatch.setattr(hip_build, "HIPCC", str(fake))
+    monkeypatch.setattr(hip_build, "CXX", str(fake))
+    monkeypatch.setattr(hip_build, "LIB", str(lib))
+    monkeypatch.setattr(hip_build, "TENSOR_PTR", str(check))
+    other = tmp_path / "other.so"
+    hip_build.build(lib=str(other), build_dir=str(tmp_path / "objects"))
+    assert other.exists() and not check.exists()
+    hip_build.build(lib=str(lib), build_dir=str(tmp_path / "objects"))
+    assert lib.exists() and check.exists()
