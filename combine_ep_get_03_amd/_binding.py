@@ -700,12 +700,15 @@ def _current(stream):
 
 def _codes_ptr(t: Optional[torch.Tensor], shape, name: str, cur: int, need: bool = True):
     """Device address of e4m3 codes: uint8, or float8_e4m3fn."""
-    return _row_ptr(t, _E4M3 if t is not None and t.dtype is _E4M3 else _U8, shape, name, cur, need)
+    dtype = _E4M3 if getattr(t, "dtype", None) is _E4M3 else _U8
+    return _row_ptr(t, dtype, shape, name, cur, need)
 
 
 def _norm_weight(weight: torch.Tensor, H: int, cur: int):
-    dtype = weight.dtype
+    dtype = getattr(weight, "dtype", None)
     if dtype is not _BF16 and dtype is not _F32:
+        if not isinstance(weight, torch.Tensor):
+            _refuse(weight, _BF16, (H,), "weight", True)
         raise TypeError(f"weight: expected torch.bfloat16 or torch.float32, got {dtype}")
     return _row_ptr(weight, dtype, (H,), "weight", cur), int(dtype is _F32)
 
@@ -744,7 +747,8 @@ def ep_rmsnorm_grad(grad_y, h, weight, *, grad_x, grad_residual_out=None, grad_w
     w, w_fp32 = _norm_weight(weight, H, cur)
     ws, ws_bytes = None, 0
     if workspace is not None:  # empty where there are no tokens
-        ws, ws_bytes = _row_ptr(workspace, _U8, workspace.shape, "workspace", cur), workspace.numel()
+        ws = _row_ptr(workspace, _U8, getattr(workspace, "shape", None), "workspace", cur)
+        ws_bytes = workspace.numel()
     _check(load().ep_rmsnorm_grad(
         _row_ptr(grad_y, _BF16, rows, "grad_y", cur),
         _row_ptr(grad_residual_out, _BF16, rows, "grad_residual_out", cur, False),
