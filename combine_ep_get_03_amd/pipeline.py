@@ -253,10 +253,15 @@ class ExpertPath:
     and with training=True, in reverse,
 
         combine_grad(grad_out, expert_out, topk_weights)  grad_expert_out, grad_topk_weights
-        dispatch_grad(grad_perm_x)                        grad_y
+        dispatch_grad(grad_perm_x, addend=...)            grad_y
         norm_grad(weight, grad_residual_out)              grad_x, grad_weight
 
     The gate weights are applied once, by combine(), so their gradient is combine_grad()'s.
+    y feeds more than the dispatch: the router that the gate weights come from, and a shared
+    expert where there is one. The caller takes grad_topk_weights back through the router and
+    grad_out (combine()'s addend's gradient) back through the shared expert, and gives
+    dispatch_grad() the sum of both as its addend; without them grad_y, and with it grad_x and
+    grad_weight, is the expert rows' share alone.
     h is what the norm was taken of as the backward reads it: residual_out, or x without a
     residual. Rows of perm_x behind the last routed pair are left as they were."""
 
@@ -337,8 +342,16 @@ class ExpertPath:
                                     grad_topk_weights=self.grad_topk_weights,
                                     error_flag=self.error_flag, stream=stream)
 
-    def dispatch_grad(self, grad_perm_x, stream=None) -> None:
+    def dispatch_grad(self, grad_perm_x, stream=None, *, addend=None) -> None:
+        """grad_y = the sum of each token's routed rows of grad_perm_x, + addend (bf16 [T][H]:
+        what reaches y through the router and a shared expert; may be grad_y itself), in fp32
+        and rounded once. It is the sum that ep_combine_unpermute makes with every weight 1."""
         self._needs_training()
+        if addend is not None:
+            B.ep_combine_unpermute(grad_perm_x, None, self.layout_buf.expert_slot,
+                                   out=self.grad_y, addend=addend, error_flag=self.error_flag,
+                                   stream=stream)
+            return
         B.ep_dispatch_permute_grad(grad_perm_x, self.layout_buf.expert_slot, grad_x=self.grad_y,
                                    error_flag=self.error_flag, stream=stream)
 

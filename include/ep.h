@@ -620,7 +620,9 @@ int ep_combine_unpermute_grad(const void *grad_out, const void *expert_out, int6
                               int num_topk, const int32_t *expert_slot, void *grad_expert_out,
                               float *grad_topk_weights, int32_t *error_flag, void *stream);
 
-/* ep_dispatch_permute_grad -- the gradient of ep_dispatch_permute.
+/* ep_dispatch_permute_grad -- the gradient of ep_dispatch_permute. Where x has further uses
+ * (a router, a shared expert), ep_combine_unpermute with topk_weights NULL, expert_out =
+ * grad_perm_x and addend = the other uses' gradient gives the whole of x's in one call.
  *
  * In:  grad_perm_x       bf16 [num_rows][H]
  *      grad_perm_weights fp32 [num_rows]; needed with grad_topk_weights, else may be NULL

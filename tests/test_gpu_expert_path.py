@@ -266,3 +266,107 @@ def test_gradients_need_a_training_path():
     with pytest.raises(ValueError, match="norm"):
         q.norm_grad(torch.ones(128, device="cuda"))
     assert ep.EP_OK == 0
+
+
+def whole_block_64(d, eps):
+    """The block whose gate and shared expert are functions of y, in 64 bits with autograd:
+    gate[t][j] = <y[t], router[:, idx[t][j]]>, shared = y * shared_scale."""
+    leaf = {n: P.f64(d[n]).requires_grad_() for n in ("x", "residual", "weight")}
+    s, y = P.rmsnorm(leaf["x"], leaf["residual"], leaf["weight"], eps)
+    idx = d["idx"].cpu()
+    hit = (idx >= 0).unsqueeze(2)
+    zero = torch.zeros((), dtype=torch.float64)
+    gate = (y @ P.f64(d["router"])).gather(1, idx.clamp(min=0))
+    per = y.unsqueeze(1) * P.f64(d["scale"])[idx.clamp(min=0)]
+    out = torch.where(hit, per * gate.unsqueeze(2), zero).sum(dim=1) + y * P.f64(d["shared_scale"])
+    return s, y, gate, out, leaf
+
+
+@pytest.mark.parametrize("T,H,E,k,apart", [(1, 7168, 256, 8, True), (130, 512, 64, 6, True),
+                                           (257, 1024, 16, 4, True), (257, 1024, 16, 4, False),
+                                           (1000, 128, 16, 2, True)])
+def test_block_whose_gate_and_shared_expert_come_from_the_norm(T, H, E, k, apart):
+    """All three ways of y's gradient: expert rows, router, shared expert. The addend is a
+    tensor of its own, or what grad_y holds."""
+    print(f"\ncase: whole block T={T} H={H} E={E} k={k} own addend {apart}", flush=True)
+    d = inputs(T + H + 3, T, H, E, k)
+    g = gen(T + H + 4)
+    d["router"] = torch.randn((H, E), generator=g, device="cuda") / H**0.5
+    d["shared_scale"] = torch.rand(H, generator=g, device="cuda") + 0.5
+    idx = d["idx"].clamp(min=0)
+    hit = d["idx"] >= 0
+    p = ExpertPath(T, H, E, k, training=True)
+    p.norm(d["x"], d["weight"], d["residual"])
+    gate = (p.y.double() @ d["router"].double()).gather(1, idx).float().contiguous()
+    p.dispatch(d["idx"])
+    M = int(p.expert_offset[-1])
+    e = expert_rows(p.expert_offset, T, k, E)
+    expert_out = torch.full((T * k, H), float("nan"), dtype=BF16, device="cuda")
+    expert_out[:M] = experts(p.perm_x[:M], e, d["scale"])
+    p.combine(expert_out, gate, addend=(p.y.float() * d["shared_scale"]).to(BF16))
+    # backwards
+    p.combine_grad(d["grad_out"], expert_out, gate)
+    to_router = torch.zeros((T, E), dtype=torch.float64, device="cuda")
+    to_router.scatter_add_(1, idx, torch.where(hit, p.grad_topk_weights.double(), 0.0))
+    rest = (to_router @ d["router"].double().t().contiguous()
+            + d["grad_out"].double() * d["shared_scale"].double()).to(BF16)
+    grad_perm = torch.full((T * k, H), float("nan"), dtype=BF16, device="cuda")
+    grad_perm[:M] = experts(p.grad_expert_out[:M], e, d["scale"])
+    if apart:
+        p.dispatch_grad(grad_perm, addend=rest)
+    else:
+        p.grad_y.copy_(rest)
+        p.dispatch_grad(grad_perm, addend=p.grad_y)
+    slot = p.layout_buf.expert_slot.cpu()
+    want = P.unpermute(P.f64(grad_perm), None, slot, P.f64(rest))
+    P.assert_within(p.grad_y, want, P.unpermute_bound(want, P.f64(grad_perm), None, slot, P.f64(rest)),
+                    "grad_y of its inputs")
+    p.norm_grad(d["weight"], d["grad_res"])
+    assert int(p.error_flag) == 0
+
+    s, y, gate64, out, leaf = whole_block_64(d, p.eps)
+    y.retain_grad()
+    (out * P.f64(d["grad_out"])).sum().add((s * P.f64(d["grad_res"])).sum()).backward()
+    with torch.no_grad():
+        idx, hit = idx.cpu(), hit.cpu().unsqueeze(2)
+        zero = torch.zeros((), dtype=torch.float64)
+        go, scale = P.f64(d["grad_out"]), P.f64(d["scale"])[idx]
+        router = P.f64(d["router"])
+        # Roundings, each BF16 relative. y was rounded once, so a gate weight is off by
+        # BF16 gm at most, gm the sum of its terms' magnitudes. On the expert rows' way:
+        # the gate weight, its product with grad_out, the expert's product. On the router's:
+        # y and the expert's row under the dot product, the addend's. On the shared expert's:
+        # the addend's. At last grad_y's own. 0.2 BF16 more for fp32 and second-order terms.
+        gm = (y.abs() @ router.abs()).gather(1, idx)
+        rows = torch.where(hit, (scale * go.abs().unsqueeze(1)) * gm.unsqueeze(2), zero).sum(dim=1)
+        dot = torch.where(hit, (y.unsqueeze(1) * scale * go.unsqueeze(1)).abs(), zero).sum(dim=2)
+        way = torch.zeros((T, E), dtype=torch.float64).scatter_add_(1, idx, dot) @ router.abs().t()
+        gy = y.grad
+        gy_off = P.BF16 * (3.2 * rows + 3.2 * way + 1.2 * P.f64(d["shared_scale"]) * go.abs() + 1.01 * gy.abs())
+        P.assert_within(p.grad_y, gy, gy_off, "grad_y")
+        # The same gradient at the values that the forward pass held (its roundings apart): what
+        # is left are the backward pass's own roundings, two on the expert rows' way (row and
+        # expert), one of the addend, grad_y's; and the dot product's in fp32 on the router's.
+        # This bound sees each of the two further ways: grad_y without it fails.
+        by_expert = torch.where(hit, P.gather(P.f64(expert_out), slot) * go.unsqueeze(1), zero)
+        to_e = torch.zeros((T, E), dtype=torch.float64)
+        by_router = to_e.scatter_add(1, idx, by_expert.sum(dim=2)) @ router.t()
+        way = to_e.scatter_add(1, idx, by_expert.abs().sum(dim=2)) @ router.abs().t()
+        by_shared = go * P.f64(d["shared_scale"])
+        by_rows = torch.where(hit, scale * P.f64(gate).unsqueeze(2) * go.unsqueeze(1), zero)
+        held = by_rows.sum(dim=1) + by_router + by_shared
+        off = P.BF16 * (2.1 * by_rows.abs().sum(dim=1) + 1.1 * (by_router + by_shared).abs()
+                        + 1.01 * held.abs()) + 2.0**-13 * way
+        P.assert_within(p.grad_y, held, off, "grad_y at the values held")
+        for part in (by_router, by_shared):
+            with pytest.raises(AssertionError):
+                P.assert_within(held - part, held, off, "grad_y without a part")
+        # the norm's gradient of it, as in the block above
+        w = P.f64(d["weight"]).abs()
+        r = 1 / torch.sqrt(s.square().mean(dim=1, keepdim=True) + p.eps)
+        n, g_, g_off = (s * r).abs(), gy.abs() * w, gy_off * w
+        first, second = r * g_, r * n * (g_ * n).mean(dim=1, keepdim=True)
+        off = r * (g_off + n * (g_off * n).mean(dim=1, keepdim=True)) + P.BF16 * 1.1 * first + 5 * P.BF16 * second
+        P.assert_within(p.grad_x, leaf["x"].grad, 1.05 * off + P.BF16 * 1.01 * leaf["x"].grad.abs(), "grad_x")
+        woff = ((gy_off + 2.2 * P.BF16 * gy.abs()) * n).sum(dim=0)
+        P.assert_within(p.grad_weight, leaf["weight"].grad, 1.05 * woff, "grad_weight")
