@@ -262,8 +262,10 @@ class ExpertPath:
     grad_out (combine()'s addend's gradient) back through the shared expert, and gives
     dispatch_grad() the sum of both as its addend; without them grad_y, and with it grad_x and
     grad_weight, is the expert rows' share alone.
-    h is what the norm was taken of as the backward reads it: residual_out, or x without a
-    residual. Rows of perm_x behind the last routed pair are left as they were."""
+    h is what the norm was taken of as the backward reads it: residual_out, or x itself without
+    a residual. That x has to keep its rows until norm_grad(); where it is one of the path's
+    own buffers (p.norm(p.out, ...) in a chain) and a call has written over it, norm_grad()
+    refuses. Rows of perm_x behind the last routed pair are left as they were."""
 
     def __init__(self, T: int, H: int, E: int, k: int, *, R: int = 1, N: int = 1,
                  eps: float = 1e-6, fp8: bool = False, training: bool = False, device="cuda"):
@@ -279,6 +281,7 @@ class ExpertPath:
         self.out = torch.empty((T, H), **bf16)
         self.perm_src_idx = torch.empty(cap, dtype=torch.int32, device=device)
         self.h: Optional[torch.Tensor] = None  # set by norm()
+        self._h_overwritten_by = ""
         if fp8:
             self.y_fp8 = torch.empty((T, H), **u8)
             self.y_scales = torch.empty((T, H // 128), **f32)
@@ -310,6 +313,16 @@ class ExpertPath:
                      y_fp8=self.y_fp8 if self.fp8 else None,
                      y_scales=self.y_scales if self.fp8 else None, eps=self.eps, stream=stream)
         self.h = self.residual_out if with_sum else x
+        self._wrote(self.y, "norm")
+
+    def _wrote(self, buffer, call: str) -> None:
+        """A call has written `buffer`: h is gone if it lies there."""
+        h = self.h
+        if not self.training or h is None or h is self.residual_out:
+            return
+        at, by = h.data_ptr(), buffer.data_ptr()
+        if at < by + buffer.numel() * buffer.element_size() and by < at + h.numel() * h.element_size():
+            self.h, self._h_overwritten_by = None, call
 
     def dispatch(self, topk_idx, stream=None) -> None:
         """The layout of the batch and the norm's rows in expert-major order."""
@@ -324,11 +337,13 @@ class ExpertPath:
             B.ep_dispatch_permute(self.y, None, lb.expert_slot, perm_x=self.perm_x,
                                   perm_src_idx=self.perm_src_idx, error_flag=self.error_flag,
                                   stream=stream)
+            self._wrote(self.perm_x, "dispatch")
 
     def combine(self, expert_out, topk_weights, addend=None, stream=None) -> None:
         B.ep_combine_unpermute(expert_out, topk_weights, self.layout_buf.expert_slot,
                                out=self.out, addend=addend, error_flag=self.error_flag,
                                stream=stream)
+        self._wrote(self.out, "combine")
 
     def _needs_training(self) -> None:
         if not self.training:
@@ -341,6 +356,7 @@ class ExpertPath:
                                     grad_expert_out=self.grad_expert_out,
                                     grad_topk_weights=self.grad_topk_weights,
                                     error_flag=self.error_flag, stream=stream)
+        self._wrote(self.grad_expert_out, "combine_grad")
 
     def dispatch_grad(self, grad_perm_x, stream=None, *, addend=None) -> None:
         """grad_y = the sum of each token's routed rows of grad_perm_x, + addend (bf16 [T][H]:
@@ -351,14 +367,20 @@ class ExpertPath:
             B.ep_combine_unpermute(grad_perm_x, None, self.layout_buf.expert_slot,
                                    out=self.grad_y, addend=addend, error_flag=self.error_flag,
                                    stream=stream)
-            return
-        B.ep_dispatch_permute_grad(grad_perm_x, self.layout_buf.expert_slot, grad_x=self.grad_y,
-                                   error_flag=self.error_flag, stream=stream)
+        else:
+            B.ep_dispatch_permute_grad(grad_perm_x, self.layout_buf.expert_slot,
+                                       grad_x=self.grad_y, error_flag=self.error_flag,
+                                       stream=stream)
+        self._wrote(self.grad_y, "dispatch_grad")
 
     def norm_grad(self, weight, grad_residual_out=None, stream=None) -> None:
         self._needs_training()
+        if self.h is None and self._h_overwritten_by:
+            raise ValueError(f"norm_grad needs the rows that norm() was taken of, and "
+                             f"{self._h_overwritten_by}() has written over them: give norm() a copy")
         if self.h is None:
             raise ValueError("norm_grad needs norm() first")
         B.ep_rmsnorm_grad(self.grad_y, self.h, weight, grad_x=self.grad_x,
                           grad_residual_out=grad_residual_out, grad_weight=self.grad_weight,
                           workspace=self.norm_workspace, eps=self.eps, stream=stream)
+        self._wrote(self.grad_x, "norm_grad")
