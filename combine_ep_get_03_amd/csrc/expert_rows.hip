@@ -106,9 +106,10 @@ __global__ __launch_bounds__(kT) void permute_fp8_kernel(
 
 // kB of token t's pairs, j0 .. j0 + kB - 1, for every lane of a wave alike: their weights, and
 // their rows' places as buffers of V words. A pair that is not routed, out of range or past
-// k gets a buffer of no bytes and the weight 0, so that its load returns zeros and its
+// k gets a buffer of no bytes and the weight -0.0, so that its load returns zeros and its
 // store is dropped without a branch: behind a branch of its own, each load would first
-// wait for every load before it. t has to be the same in all lanes.
+// wait for every load before it. Its product -0.0 changes no sum, a sum of -0.0 included.
+// t has to be the same in all lanes.
 template <int kB>
 struct Pairs {
     int32_t q[kB];
@@ -130,7 +131,7 @@ struct Pairs {
         for (int i = 0; i < kB; ++i) {
             if (q[i] >= num_rows) errbits |= kErrSlotRange;
             if (q[i] >= num_rows || j0 + i >= k) q[i] = -1;
-            if (q[i] < 0) w[i] = 0.0f;
+            if (q[i] < 0) w[i] = -0.0f;
         }
     }
 
@@ -159,7 +160,12 @@ __global__ __launch_bounds__(kUnpermuteThreads) void unpermute_kernel(
     const int lane = lane_id();
     const int v = c * kWave + lane;
     const u32x4 ad = load_word<kPolicyNt>(row_buffer(addend, t, V), v);
-    float acc[8] = {};
+    // under an addend the sum starts at -0.0, so that a token with no pair gets the addend's
+    // own bits; without one at +0.0, which is what such a token then gets
+    const float start = addend ? -0.0f : 0.0f;
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = start;
     int32_t errbits = 0;
     for (int j0 = 0; j0 < k; j0 += kB) {
         const Pairs<kB> pr(expert_slot, topk_w, t, j0, k, num_rows, errbits);

@@ -590,7 +590,9 @@ int ep_dispatch_permute_fp8(const uint8_t *x_fp8, const float *x_scales,
  *      addend       bf16 [T][H], say a shared expert's output                  (nullable)
  * Out: out          bf16 [T][H]; out[t] = bf16_rne( sum over j with q = expert_slot[t][j] >= 0
  *                   of topk_weights[t][j] * float(expert_out[q]), in fp32, plus
- *                   float(addend[t]) ); a token with no pair gets addend[t], or +0.0.
+ *                   float(addend[t]) ); a token with no pair gets addend[t], or +0.0. Zeros
+ *                   that add up to zero give +0.0, and -0.0 where there is an addend and
+ *                   all of them, addend included, are -0.0.
  *      Rows and weights of pairs that are not routed are not read into the sum. A row
  *      >= num_rows is skipped and sets EP_DEVERR_SLOT_RANGE. out may be addend's memory.
  * Sizes: H % 8 == 0; expert_out, addend and out 16-byte aligned.

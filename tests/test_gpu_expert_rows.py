@@ -553,3 +553,45 @@ def test_two_streams_at_once():
         P.assert_within(out, want, P.unpermute_bound(want, r0, wd, s, None), "out")
         _, want_w = P.unpermute_grad(P.f64(go), r, wd, s)
         P.assert_within(gw, want_w, P.dot_bound(P.f64(go), r0, s), "grad weights")
+
+
+@pytest.mark.parametrize("k", [1, 2, 3, 4, 8, 9, 20])
+@pytest.mark.parametrize("H", [8, 520, 7168])
+def test_an_addend_comes_back_bit_for_bit(H, k):
+    """A token with no pair (not routed, or its row out of range) gets addend[t] itself, its
+    negative zeros, subnormals and infinities too; and zeros of both signs under pairs: the
+    sum of negative zeros alone is a negative zero, any other sum of zeros a positive one."""
+    print(f"\ncase: addend bits H={H} k={k}", flush=True)
+    T = 12
+    g = gen(H + k)
+    values = torch.tensor([-0.0, 0.0, 1.0, -2.0**-133, 2.0**-130, float("inf"), float("-inf"), -3.5],
+                          device="cuda", dtype=BF16)
+    add = values[torch.randint(0, 8, (T, H), generator=g, device="cuda")]
+    add[0], add[1], add[6:] = -0.0, 0.0, -0.0
+    rows = torch.zeros((20, H), dtype=BF16, device="cuda")
+    rows[10:] = -0.0
+    slot = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    slot[5] = 20                       # out of range
+    slot[6, 0], slot[7, -1] = 10, 3    # one pair of -0.0, one of +0.0
+    slot[8], slot[9] = 11, 4           # all pairs of -0.0, all of +0.0
+    slot[10, 0], slot[11, 0] = 12, 5   # a weight below zero turns the sign
+    w = torch.rand((T, k), generator=g, device="cuda") + 0.1
+    w[10:] = -1.0
+    w[0] = float("nan")
+    out, fl = sentinel(T, H), flag()
+    ep.ep_combine_unpermute(rows, w, slot, out=out, addend=add, error_flag=fl)
+    assert int(fl) == ep.EP_DEVERR_SLOT_RANGE
+    bits = out.view(torch.int16)
+    assert torch.equal(bits[:6], add[:6].view(torch.int16))
+    for t, negative in ((6, True), (7, False), (8, True), (9, False), (10, False), (11, True)):
+        assert torch.all(bits[t] == (-0x8000 if negative else 0)), t
+    # every weight 1, and in the addend's own place
+    here = add.clone()
+    ep.ep_combine_unpermute(rows, None, slot, out=here, addend=here)
+    bits = here.view(torch.int16)
+    assert torch.equal(bits[:6], add[:6].view(torch.int16))
+    for t, negative in ((6, True), (7, False), (8, True), (9, False), (10, True), (11, False)):
+        assert torch.all(bits[t] == (-0x8000 if negative else 0)), t
+    # without an addend a sum of zeros is +0.0, as it is for a token with no pair
+    ep.ep_combine_unpermute(rows, w, slot, out=out)
+    assert torch.all(out.view(torch.int16) == 0)
