@@ -454,3 +454,61 @@ def test_grad_workspace_too_small_is_refused():
             ep.ep_rmsnorm_grad(x, x, w, grad_x=torch.empty_like(x),
                                grad_weight=torch.zeros(H, device="cuda"), workspace=ws)
         assert e.value.status == ep.EP_ERR_CAPACITY
+
+
+def repeats_of(base, times):
+    """[times * n][H]: the base's n rows over and over."""
+    return base.unsqueeze(0).expand(times, *base.shape).reshape(times * base.shape[0], -1).contiguous()
+
+
+def assert_repeats(got, base, times, what):
+    """Every repeat of the base's rows holds the base's bits."""
+    got = got.view(times, *base.shape)
+    for i in range(times):
+        assert torch.equal(got[i].view(torch.uint8), base.view(torch.uint8)), f"{what}: repeat {i} of {times}"
+
+
+@pytest.mark.parametrize("H", [8, 128, 512, 1024, 2048, 2176])
+def test_norm_in_two_launches_on_every_row(H):
+    """2^21 + 4096 rows, past what one launch takes, in each form of the kernel: all rows of all
+    outputs, the codes and scales of the second launch among them."""
+    n, times = 4096, 513
+    print(f"\ncase: rmsnorm in two launches H={H}", flush=True)
+    g = gen(H)
+    x, res, w = rand(g, n, H), rand(g, n, H, scale=3.0), weight_of(g, H, BF16)
+
+    def outputs(T):
+        o = dict(y=torch.full((T, H), 7.0, dtype=BF16, device="cuda"),
+                 residual_out=torch.full((T, H), 7.0, dtype=BF16, device="cuda"))
+        if H % 128 == 0:
+            o["y_fp8"] = torch.full((T, H), 0x55, dtype=torch.uint8, device="cuda")
+            o["y_scales"] = torch.full((T, H // 128), -1.0, device="cuda")
+        return o
+
+    base, many = outputs(n), outputs(n * times)
+    ep.ep_rmsnorm(x, w, residual=res, eps=EPS, **base)
+    check_norm(x, res, w, **base)
+    ep.ep_rmsnorm(repeats_of(x, times), w, residual=repeats_of(res, times), eps=EPS, **many)
+    for name in base:
+        assert_repeats(many[name], base[name], times, name)
+
+
+@pytest.mark.parametrize("H,n,times", [(8, 4096, 270), (64, 4096, 270), (264, 4096, 270),
+                                       (7168, 4096, 17), (40960, 512, 9)])
+@pytest.mark.parametrize("with_res", [False, True])
+def test_grad_without_the_weights_gradient_on_every_row(H, n, times, with_res):
+    """More rows than the blocks of one launch hold at once: blocks walk on to further rows.
+    (Rows past 16384 channels take a block each.)"""
+    print(f"\ncase: rmsnorm_grad without grad_weight T={n * times} H={H} res={with_res}", flush=True)
+    g = gen(H + 1)
+    dy, h, w = rand(g, n, H), rand(g, n, H, scale=4.0), weight_of(g, H, torch.float32)
+    dres = rand(g, n, H) if with_res else None
+    base = torch.full((n, H), 7.0, dtype=BF16, device="cuda")
+    many = torch.full((n * times, H), 7.0, dtype=BF16, device="cuda")
+    ep.ep_rmsnorm_grad(dy, h, w, grad_x=base, grad_residual_out=dres, eps=EPS)
+    d = (P.f64(dy), P.f64(dres) if with_res else None, P.f64(h), P.f64(w), EPS)
+    dx, _ = P.rmsnorm_grad(*d)
+    P.assert_within(base, dx, P.dx_bound(dx, *d), "grad_x")
+    ep.ep_rmsnorm_grad(repeats_of(dy, times), repeats_of(h, times), w, grad_x=many,
+                       grad_residual_out=repeats_of(dres, times) if with_res else None, eps=EPS)
+    assert_repeats(many, base, times, "grad_x")
