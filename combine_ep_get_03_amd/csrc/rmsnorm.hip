@@ -480,9 +480,10 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void rmsnorm_dw_sum_kernel(const 
 // the partial rows stay few. Measured at 7168 channels, two words per lane: 256 blocks of two
 // rows at a time 46.8 us at 4096 tokens and 138.4 us at 14000; 512 blocks of one row 47.2 and
 // 146.9 us (one word per lane: 256 blocks 52.6 and 157.7 us, 1024 blocks 64.5 and 168.2 us).
-// Batches of up to 256 rows take a row per block: 256 tokens 11.1 us against 12.4 us. What one
-// block holds at once needs no second launch: 8 tokens of 1024 channels 5.9 us from the host
-// and 4.9 in a graph, against 9.3 and 5.2; two rounds of one block 6.0 and 6.6 (16 tokens).
+// Batches of up to 256 rows take a row per block: 256 tokens 11.1 us against 12.4 us where the
+// two were compared, 9.5 us in the latest run. What one block holds at once needs no second
+// launch: 8 tokens of 1024 channels 5.9 us from the host and 4.9 in a graph, against 9.3 and
+// 5.2; two rounds of one block 6.0 and 6.6 (16 tokens).
 constexpr int64_t kGradBlocks = 256;
 // From this many bytes of h on, the rows' loads are non-temporal. Cached against
 // non-temporal: 17.6 against 18.2 us at 1024 tokens of 7168 channels (15 MB), 23.8 against
@@ -616,7 +617,10 @@ hipError_t launch_rmsnorm_grad(const void* grad_y, const void* grad_residual_out
     if (!s.W)
         return launch_wide_grad(dy, dres, hp, weight, weight_fp32, eps, T, H, dx, grad_weight,
                                 workspace, stream);
-    // without grad_w nothing ties a block to many rows
+    // Without grad_w nothing ties a block to many rows. Measured at 7168 channels against the
+    // form with grad_w: 5.4 against 9.5 us at 256 tokens, 12.2 against 17.5 at 1024, 22.8
+    // against 26.0 at 2048; but 51.9 against 46.2 at 4096 and 171.7 against 136.6 at 14000,
+    // where a block that holds a row once has no next row in flight while it reduces and writes.
     const int64_t grid =
         grad_weight ? s.blocks : std::min<int64_t>((T + s.G - 1) / s.G, int64_t{1} << 16);
     // a single block's partial row is the sum (it leaves in 128-bit words)

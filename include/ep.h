@@ -523,7 +523,9 @@ int ep_combine_recv(const void *stage, int num_nodes, int64_t max_tokens_per_ran
  *                   scale infinity, NaN codes for its infinities and codes 0 for the rest.
  *                   (nullable, both or none)
  *      At least one output must be asked for.
- * Sums and the norm are fp32: |s| up to about 1e18 (squares that pass fp32 give n = 0).
+ * Sums and the norm are fp32: |s| up to about 1e18 (squares that pass fp32 give n = 0). With
+ * an eps below 2^-126, rows whose mean square is below 2^-126 too lose precision, and a row
+ * whose squares are all 0 in fp32 (|s| up to 2^-75) is divided by sqrt(eps) alone.
  * residual_out may be x's or residual's memory and y may be the other's (the same start
  * address); any other overlap of outputs and inputs is undefined.
  * Sizes: 0 <= T <= INT32_MAX; H % 8 == 0, H % 128 == 0 with y_fp8 (else EP_ERR_ALIGN); rows 16-byte
