@@ -25,6 +25,7 @@ EP_MAX_RANKS, EP_MAX_EXPERTS, EP_EXPERT_SLOT_MAX_K = 1024, 8192, 16
 EP_LAYOUT_SCRATCH_BYTES = 4 << 20
 EP_COUNTS_MAX_RANKS = 64
 EP_LAYOUT_DISPATCH_MAX_TOKENS = 256
+EP_EXPERT_MAX_WIDTH = 1 << 20
 EP_HBM_SPREAD_CHUNK_BYTES = 4096
 
 _lib = None
@@ -85,6 +86,13 @@ def load() -> ctypes.CDLL:
     L.ep_combine_unpermute.argtypes = [P, i64, P, i64, i32, i32, P, P, P, P, P]
     L.ep_combine_unpermute_grad.argtypes = [P, P, i64, P, i64, i32, i32, P, P, P, P, P]
     L.ep_dispatch_permute_grad.argtypes = [P, P, i64, i64, i32, i32, P, P, P, P, P]
+    L.ep_expert_gate_up.argtypes = [P, P, P, i32, i64, i32, i32, P, P, P, P, P, P]
+    L.ep_expert_gate_up_fp8.argtypes = [P, P, P, P, P, i32, i64, i32, i32, P, P, P, P]
+    L.ep_expert_down.argtypes = [P, P, P, i32, i64, i32, i32, P, P, P]
+    L.ep_expert_down_fp8.argtypes = [P, P, P, P, P, i32, i64, i32, i32, P, P, P]
+    L.ep_expert_down_grad.argtypes = [P, P, P, i32, i64, i32, i32, P, P, P, P, P, P, P]
+    L.ep_expert_gate_up_grad.argtypes = [P, P, P, i32, i64, i32, i32, P, P, P]
+    L.ep_expert_weight_grad.argtypes = [P, P, P, i32, i64, i32, i32, P, i32, i32, P, P]
     L.ep_hbm_copy.argtypes = [P, P, sz, P]
     L.ep_hbm_fan.argtypes = [P, P, sz, i32, i32, P]
     L.ep_hbm_spread.argtypes = [P, P, sz, i32, i32, P]
@@ -94,7 +102,9 @@ def load() -> ctypes.CDLL:
               "ep_dispatch_recv", "ep_combine_send", "ep_combine_recv", "ep_hbm_copy",
               "ep_hbm_fan", "ep_hbm_spread", "ep_rmsnorm", "ep_rmsnorm_grad",
               "ep_dispatch_permute_fp8", "ep_combine_unpermute", "ep_combine_unpermute_grad",
-              "ep_dispatch_permute_grad"):
+              "ep_dispatch_permute_grad", "ep_expert_gate_up", "ep_expert_gate_up_fp8",
+              "ep_expert_down", "ep_expert_down_fp8", "ep_expert_down_grad",
+              "ep_expert_gate_up_grad", "ep_expert_weight_grad"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -840,6 +850,152 @@ def ep_dispatch_permute_grad(grad_perm_x, expert_slot, *, grad_x, grad_perm_weig
         _row_ptr(grad_x, _BF16, (T, H), "grad_x", cur),
         _row_ptr(grad_topk_weights, _F32, (T, k), "grad_topk_weights", cur, False),
         _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_dispatch_permute_grad")
+
+
+def _weights_3d(w, name: str):
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        if isinstance(w, torch.Tensor):
+            raise ValueError(f"{name}: expected 3 dimensions, got shape {tuple(w.shape)}")
+        _refuse(w, _BF16, None, name, True)
+    return w.shape
+
+
+def _even(n: int, name: str) -> int:
+    if n % 2:
+        raise ValueError(f"{name}: expected gate's and up's channels, got {n}")
+    return n // 2
+
+
+def ep_expert_gate_up(x, w_gate_up, expert_offset, *, act, gate_up=None, gate_up_fp8=None,
+                      gate_up_scales=None, error_flag=None, stream=None) -> None:
+    """act = silu(x Wg^T) * (x Wu^T) of each expert's rows. x: bf16 [rows][H]; w_gate_up: bf16
+    [E][2I][H], Wg's rows first; expert_offset: int32 [E + 1]; act: bf16 [rows][I]. For the
+    backward pass gate and up are kept as gate_up (bf16 [rows][2I]) or gate_up_fp8 (uint8 or
+    float8_e4m3fn [rows][2I]) with gate_up_scales (fp32 [rows][2I/128])."""
+    rows, H = _rows_2d(x, "x")
+    E, I2, _ = _weights_3d(w_gate_up, "w_gate_up")
+    I = _even(I2, "w_gate_up")
+    cur, st = _current(stream)
+    _check(load().ep_expert_gate_up(
+        _row_ptr(x, _BF16, (rows, H), "x", cur),
+        _row_ptr(w_gate_up, _BF16, (E, I2, H), "w_gate_up", cur),
+        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, H, I,
+        _row_ptr(act, _BF16, (rows, I), "act", cur),
+        _row_ptr(gate_up, _BF16, (rows, I2), "gate_up", cur, False),
+        _codes_ptr(gate_up_fp8, (rows, I2), "gate_up_fp8", cur, False),
+        _row_ptr(gate_up_scales, _F32, (rows, I2 // 128), "gate_up_scales", cur, False),
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_expert_gate_up")
+
+
+def ep_expert_gate_up_fp8(x_fp8, x_scales, w_fp8, w_scales, expert_offset, *, act_fp8, act_scales,
+                          error_flag=None, stream=None) -> None:
+    """ep_expert_gate_up in e4m3: x_fp8 [rows][H] with x_scales fp32 [rows][H/128], w_fp8
+    [E][2I][H] with w_scales fp32 [E][2I/128][H/128], act_fp8 [rows][I] with act_scales fp32
+    [rows][I/128]; codes as uint8 or float8_e4m3fn."""
+    rows, H = _rows_2d(x_fp8, "x_fp8")
+    E, I2, _ = _weights_3d(w_fp8, "w_fp8")
+    I = _even(I2, "w_fp8")
+    cur, st = _current(stream)
+    _check(load().ep_expert_gate_up_fp8(
+        _codes_ptr(x_fp8, (rows, H), "x_fp8", cur),
+        _row_ptr(x_scales, _F32, (rows, H // 128), "x_scales", cur),
+        _codes_ptr(w_fp8, (E, I2, H), "w_fp8", cur),
+        _row_ptr(w_scales, _F32, (E, I2 // 128, H // 128), "w_scales", cur),
+        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, H, I,
+        _codes_ptr(act_fp8, (rows, I), "act_fp8", cur),
+        _row_ptr(act_scales, _F32, (rows, I // 128), "act_scales", cur),
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_expert_gate_up_fp8")
+
+
+def ep_expert_down(act, w_down, expert_offset, *, expert_out, error_flag=None,
+                   stream=None) -> None:
+    """expert_out = act Wd^T of each expert's rows. act: bf16 [rows][I]; w_down: bf16 [E][H][I];
+    expert_offset: int32 [E + 1]; expert_out: bf16 [rows][H]."""
+    rows, I = _rows_2d(act, "act")
+    E, H, _ = _weights_3d(w_down, "w_down")
+    cur, st = _current(stream)
+    _check(load().ep_expert_down(
+        _row_ptr(act, _BF16, (rows, I), "act", cur),
+        _row_ptr(w_down, _BF16, (E, H, I), "w_down", cur),
+        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, H, I,
+        _row_ptr(expert_out, _BF16, (rows, H), "expert_out", cur),
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_expert_down")
+
+
+def ep_expert_down_fp8(act_fp8, act_scales, w_fp8, w_scales, expert_offset, *, expert_out,
+                       error_flag=None, stream=None) -> None:
+    """ep_expert_down in e4m3: act_fp8 [rows][I] with act_scales fp32 [rows][I/128], w_fp8
+    [E][H][I] with w_scales fp32 [E][H/128][I/128]; expert_out: bf16 [rows][H]."""
+    rows, I = _rows_2d(act_fp8, "act_fp8")
+    E, H, _ = _weights_3d(w_fp8, "w_fp8")
+    cur, st = _current(stream)
+    _check(load().ep_expert_down_fp8(
+        _codes_ptr(act_fp8, (rows, I), "act_fp8", cur),
+        _row_ptr(act_scales, _F32, (rows, I // 128), "act_scales", cur),
+        _codes_ptr(w_fp8, (E, H, I), "w_fp8", cur),
+        _row_ptr(w_scales, _F32, (E, H // 128, I // 128), "w_scales", cur),
+        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, H, I,
+        _row_ptr(expert_out, _BF16, (rows, H), "expert_out", cur),
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_expert_down_fp8")
+
+
+def ep_expert_down_grad(grad_expert_out, w_down, expert_offset, *, grad_gate_up, gate_up=None,
+                        gate_up_fp8=None, gate_up_scales=None, act=None, error_flag=None,
+                        stream=None) -> None:
+    """Back through the second product and the activation: grad_gate_up (bf16 [rows][2I]; may be
+    gate_up) from grad_expert_out (bf16 [rows][H]) and what the forward kept: gate_up, or
+    gate_up_fp8 and gate_up_scales. act (bf16 [rows][I]): the forward's output again."""
+    rows, H = _rows_2d(grad_expert_out, "grad_expert_out")
+    E, _, I = _weights_3d(w_down, "w_down")
+    cur, st = _current(stream)
+    if (gate_up is None) == (gate_up_fp8 is None):
+        raise ValueError("one of gate_up and gate_up_fp8 is required")
+    _check(load().ep_expert_down_grad(
+        _row_ptr(grad_expert_out, _BF16, (rows, H), "grad_expert_out", cur),
+        _row_ptr(w_down, _BF16, (E, H, I), "w_down", cur),
+        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, H, I,
+        _row_ptr(gate_up, _BF16, (rows, 2 * I), "gate_up", cur, False),
+        _codes_ptr(gate_up_fp8, (rows, 2 * I), "gate_up_fp8", cur, False),
+        _row_ptr(gate_up_scales, _F32, (rows, 2 * I // 128), "gate_up_scales", cur,
+                 gate_up_fp8 is not None),
+        _row_ptr(grad_gate_up, _BF16, (rows, 2 * I), "grad_gate_up", cur),
+        _row_ptr(act, _BF16, (rows, I), "act", cur, False),
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_expert_down_grad")
+
+
+def ep_expert_gate_up_grad(grad_gate_up, w_gate_up, expert_offset, *, grad_x, error_flag=None,
+                           stream=None) -> None:
+    """grad_x = grad_gate Wg + grad_up Wu of each expert's rows. grad_gate_up: bf16 [rows][2I];
+    w_gate_up: bf16 [E][2I][H]; grad_x: bf16 [rows][H]."""
+    rows, I2 = _rows_2d(grad_gate_up, "grad_gate_up")
+    I = _even(I2, "grad_gate_up")
+    E, _, H = _weights_3d(w_gate_up, "w_gate_up")
+    cur, st = _current(stream)
+    _check(load().ep_expert_gate_up_grad(
+        _row_ptr(grad_gate_up, _BF16, (rows, I2), "grad_gate_up", cur),
+        _row_ptr(w_gate_up, _BF16, (E, I2, H), "w_gate_up", cur),
+        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, H, I,
+        _row_ptr(grad_x, _BF16, (rows, H), "grad_x", cur),
+        _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_expert_gate_up_grad")
+
+
+def ep_expert_weight_grad(grad, input, expert_offset, *, grad_weight, accumulate: bool = False,
+                          error_flag=None, stream=None) -> None:
+    """grad_weight[e] = the sum over expert e's rows of grad's row times input's row (added to it
+    with accumulate). grad: bf16 [rows][M]; input: bf16 [rows][N]; grad_weight: bf16 or fp32
+    [E][M][N]. w_gate_up's is of grad_gate_up and x, w_down's of grad_expert_out and act."""
+    rows, M = _rows_2d(grad, "grad")
+    _, N = _rows_2d(input, "input")
+    E = _weights_3d(grad_weight, "grad_weight")[0]
+    cur, st = _current(stream)
+    dtype = _F32 if grad_weight.dtype is _F32 else _BF16
+    _check(load().ep_expert_weight_grad(
+        _row_ptr(grad, _BF16, (rows, M), "grad", cur),
+        _row_ptr(input, _BF16, (rows, N), "input", cur),
+        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, M, N,
+        _row_ptr(grad_weight, dtype, (E, M, N), "grad_weight", cur), int(dtype is _F32),
+        int(bool(accumulate)), _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st),
+        "ep_expert_weight_grad")
 
 
 def ep_hbm_copy(src, dst, nbytes: Optional[int] = None, stream=None) -> None:

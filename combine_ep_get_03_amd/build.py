@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libep.so")
 TENSOR_PTR = os.path.join(PKG, "_tensor_ptr.so")
 SOURCES = ["ep_abi.cpp", "layout.hip", "dispatch.hip", "restripe.hip", "combine.hip",
-           "hbm_copy.hip", "rmsnorm.hip", "expert_rows.hip"]
+           "hbm_copy.hip", "rmsnorm.hip", "expert_rows.hip", "expert_ffn.hip",
+           "expert_ffn_grad.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")

@@ -3,6 +3,7 @@
 // check fails, and no C++ exception leaves this file.
 #include "ep.h"
 
+#include <algorithm>
 #include <limits.h>
 #include <math.h>
 
@@ -70,6 +71,38 @@ int check_norm_sizes(int64_t T, int H, float eps) {
     if (static_cast<int64_t>(H) / 8 * 64 > INT32_MAX) return EP_ERR_ARG;
     if (T > static_cast<int64_t>(INT32_MAX)) return EP_ERR_ARG;
     return EP_OK;
+}
+
+// Sizes, offsets and flag shared by the experts' products of rows of width A against width B.
+int check_expert_products(const int32_t* offset, int E, int64_t rows, int A, int B, int multiple,
+                          const int32_t* error_flag) {
+    if (E < 1 || E > EP_MAX_EXPERTS || rows < 0 || rows > INT32_MAX) return EP_ERR_ARG;
+    if (A < 1 || B < 1 || A > 2 * EP_EXPERT_MAX_WIDTH || B > 2 * EP_EXPERT_MAX_WIDTH)
+        return EP_ERR_ARG;
+    if ((rows / 256 + 1) * (std::max(A, B) / 128 + 1) > INT32_MAX) return EP_ERR_ARG;
+    if (!offset) return EP_ERR_ARG;
+    if (A % multiple != 0 || B % multiple != 0) return EP_ERR_ALIGN;
+    if (!aligned(offset, 4) || !aligned(error_flag, 4)) return EP_ERR_ALIGN;
+    return EP_OK;
+}
+
+bool expert_widths_ok(int H, int I) {
+    return H >= 1 && I >= 1 && H <= EP_EXPERT_MAX_WIDTH && I <= EP_EXPERT_MAX_WIDTH;
+}
+
+ep::GemmArgs expert_args(const void* a, const void* b, const int32_t* offset, int E, int64_t rows,
+                         int N, int K, void* out, int32_t* error_flag) {
+    ep::GemmArgs g{};
+    g.a = a;
+    g.b = b;
+    g.offset = offset;
+    g.E = E;
+    g.num_rows = rows;
+    g.N = N;
+    g.K = K;
+    g.out = out;
+    g.error_flag = error_flag;
+    return g;
 }
 
 }  // namespace
@@ -693,6 +726,151 @@ int ep_dispatch_permute_grad(const void* grad_perm_x, const float* grad_perm_wei
     return hip_status(ep::launch_dispatch_permute_grad(
         grad_perm_x, grad_perm_weights, num_rows, expert_slot, T, H, k, grad_x, grad_topk_weights,
         error_flag, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_gate_up(const void* x, const void* w_gate_up, const int32_t* expert_offset,
+                      int num_experts, int64_t num_rows, int hidden, int inter, void* act,
+                      void* gate_up, uint8_t* gate_up_fp8, float* gate_up_scales,
+                      int32_t* error_flag, void* stream) {
+    const int H = hidden, I = inter;
+    if (!expert_widths_ok(H, I)) return EP_ERR_ARG;
+    const int st = check_expert_products(expert_offset, num_experts, num_rows, H, 2 * I, 8,
+                                         error_flag);
+    if (st != EP_OK) return st;
+    if (I % 8 != 0 || (gate_up_fp8 && I % 128 != 0)) return EP_ERR_ALIGN;
+    if ((gate_up_fp8 == nullptr) != (gate_up_scales == nullptr)) return EP_ERR_ARG;
+    if (num_rows > 0 && (!x || !w_gate_up || !act)) return EP_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(w_gate_up, 16) || !aligned(act, 16) || !aligned(gate_up, 16) ||
+        !aligned(gate_up_fp8, 16) || !aligned(gate_up_scales, 4))
+        return EP_ERR_ALIGN;
+    ep::GemmArgs g = expert_args(x, w_gate_up, expert_offset, num_experts, num_rows, I, H, act,
+                                 error_flag);
+    g.gate_up = gate_up;
+    g.codes = gate_up_fp8;
+    g.scales = gate_up_scales;
+    return hip_status(ep::launch_expert_gate_up(g, false, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_gate_up_fp8(const uint8_t* x_fp8, const float* x_scales, const uint8_t* w_fp8,
+                          const float* w_scales, const int32_t* expert_offset, int num_experts,
+                          int64_t num_rows, int hidden, int inter, uint8_t* act_fp8,
+                          float* act_scales, int32_t* error_flag, void* stream) {
+    const int H = hidden, I = inter;
+    if (!expert_widths_ok(H, I)) return EP_ERR_ARG;
+    const int st = check_expert_products(expert_offset, num_experts, num_rows, H, 2 * I, 128,
+                                         error_flag);
+    if (st != EP_OK) return st;
+    if (I % 128 != 0) return EP_ERR_ALIGN;
+    if (num_rows > 0 && (!x_fp8 || !x_scales || !w_fp8 || !w_scales || !act_fp8 || !act_scales))
+        return EP_ERR_ARG;
+    if (!aligned(x_fp8, 16) || !aligned(x_scales, 4) || !aligned(w_fp8, 16) ||
+        !aligned(w_scales, 4) || !aligned(act_fp8, 16) || !aligned(act_scales, 4))
+        return EP_ERR_ALIGN;
+    ep::GemmArgs g = expert_args(x_fp8, w_fp8, expert_offset, num_experts, num_rows, I, H, nullptr,
+                                 error_flag);
+    g.a_scales = x_scales;
+    g.b_scales = w_scales;
+    g.codes = act_fp8;
+    g.scales = act_scales;
+    return hip_status(ep::launch_expert_gate_up(g, true, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_down(const void* act, const void* w_down, const int32_t* expert_offset,
+                   int num_experts, int64_t num_rows, int hidden, int inter, void* expert_out,
+                   int32_t* error_flag, void* stream) {
+    const int H = hidden, I = inter;
+    if (!expert_widths_ok(H, I)) return EP_ERR_ARG;
+    const int st = check_expert_products(expert_offset, num_experts, num_rows, H, I, 8, error_flag);
+    if (st != EP_OK) return st;
+    if (num_rows > 0 && (!act || !w_down || !expert_out)) return EP_ERR_ARG;
+    if (!aligned(act, 16) || !aligned(w_down, 16) || !aligned(expert_out, 16)) return EP_ERR_ALIGN;
+    const ep::GemmArgs g = expert_args(act, w_down, expert_offset, num_experts, num_rows, H, I,
+                                       expert_out, error_flag);
+    return hip_status(ep::launch_expert_down(g, false, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_down_fp8(const uint8_t* act_fp8, const float* act_scales, const uint8_t* w_fp8,
+                       const float* w_scales, const int32_t* expert_offset, int num_experts,
+                       int64_t num_rows, int hidden, int inter, void* expert_out,
+                       int32_t* error_flag, void* stream) {
+    const int H = hidden, I = inter;
+    if (!expert_widths_ok(H, I)) return EP_ERR_ARG;
+    const int st = check_expert_products(expert_offset, num_experts, num_rows, H, I, 128,
+                                         error_flag);
+    if (st != EP_OK) return st;
+    if (num_rows > 0 && (!act_fp8 || !act_scales || !w_fp8 || !w_scales || !expert_out))
+        return EP_ERR_ARG;
+    if (!aligned(act_fp8, 16) || !aligned(act_scales, 4) || !aligned(w_fp8, 16) ||
+        !aligned(w_scales, 4) || !aligned(expert_out, 16))
+        return EP_ERR_ALIGN;
+    ep::GemmArgs g = expert_args(act_fp8, w_fp8, expert_offset, num_experts, num_rows, H, I,
+                                 expert_out, error_flag);
+    g.a_scales = act_scales;
+    g.b_scales = w_scales;
+    return hip_status(ep::launch_expert_down(g, true, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_down_grad(const void* grad_expert_out, const void* w_down,
+                        const int32_t* expert_offset, int num_experts, int64_t num_rows,
+                        int hidden, int inter, const void* gate_up, const uint8_t* gate_up_fp8,
+                        const float* gate_up_scales, void* grad_gate_up, void* act,
+                        int32_t* error_flag, void* stream) {
+    const int H = hidden, I = inter;
+    if (!expert_widths_ok(H, I)) return EP_ERR_ARG;
+    const int st = check_expert_products(expert_offset, num_experts, num_rows, H, 2 * I, 8,
+                                         error_flag);
+    if (st != EP_OK) return st;
+    if (I % 8 != 0 || (gate_up_fp8 && I % 128 != 0)) return EP_ERR_ALIGN;
+    if ((gate_up_fp8 == nullptr) != (gate_up_scales == nullptr)) return EP_ERR_ARG;
+    if (gate_up && gate_up_fp8) return EP_ERR_ARG;
+    if (num_rows > 0 && (!grad_expert_out || !w_down || !grad_gate_up || (!gate_up && !gate_up_fp8)))
+        return EP_ERR_ARG;
+    if (!aligned(grad_expert_out, 16) || !aligned(w_down, 16) || !aligned(gate_up, 16) ||
+        !aligned(gate_up_fp8, 16) || !aligned(gate_up_scales, 4) || !aligned(grad_gate_up, 16) ||
+        !aligned(act, 16))
+        return EP_ERR_ALIGN;
+    ep::GemmArgs g = expert_args(grad_expert_out, w_down, expert_offset, num_experts, num_rows, I,
+                                 H, grad_gate_up, error_flag);
+    g.gate_up = const_cast<void*>(gate_up);
+    g.codes = const_cast<uint8_t*>(gate_up_fp8);
+    g.scales = const_cast<float*>(gate_up_scales);
+    g.act = act;
+    return hip_status(ep::launch_expert_down_grad(g, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_gate_up_grad(const void* grad_gate_up, const void* w_gate_up,
+                           const int32_t* expert_offset, int num_experts, int64_t num_rows,
+                           int hidden, int inter, void* grad_x, int32_t* error_flag,
+                           void* stream) {
+    const int H = hidden, I = inter;
+    if (!expert_widths_ok(H, I)) return EP_ERR_ARG;
+    const int st = check_expert_products(expert_offset, num_experts, num_rows, H, 2 * I, 8,
+                                         error_flag);
+    if (st != EP_OK) return st;
+    if (I % 8 != 0) return EP_ERR_ALIGN;
+    if (num_rows > 0 && (!grad_gate_up || !w_gate_up || !grad_x)) return EP_ERR_ARG;
+    if (!aligned(grad_gate_up, 16) || !aligned(w_gate_up, 16) || !aligned(grad_x, 16))
+        return EP_ERR_ALIGN;
+    const ep::GemmArgs g = expert_args(grad_gate_up, w_gate_up, expert_offset, num_experts,
+                                       num_rows, H, 2 * I, grad_x, error_flag);
+    return hip_status(ep::launch_expert_gate_up_grad(g, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_weight_grad(const void* grad, const void* input, const int32_t* expert_offset,
+                          int num_experts, int64_t num_rows, int rows_out, int cols_out,
+                          void* grad_weight, int weight_is_fp32, int accumulate,
+                          int32_t* error_flag, void* stream) {
+    const int M = rows_out, N = cols_out;
+    const int st = check_expert_products(expert_offset, num_experts, num_rows, M, N, 8, error_flag);
+    if (st != EP_OK) return st;
+    if (!grad_weight || (num_rows > 0 && (!grad || !input))) return EP_ERR_ARG;
+    if (!aligned(grad, 16) || !aligned(input, 16) || !aligned(grad_weight, 16)) return EP_ERR_ALIGN;
+    ep::GemmArgs g = expert_args(grad, input, expert_offset, num_experts, num_rows, N, 0,
+                                 grad_weight, error_flag);
+    g.M = M;
+    g.out_fp32 = weight_is_fp32 != 0;
+    g.accumulate = accumulate != 0;
+    return hip_status(ep::launch_expert_weight_grad(g, static_cast<hipStream_t>(stream)));
 }
 
 int ep_hbm_copy(const void* src, void* dst, size_t bytes, void* stream) {

@@ -1,6 +1,6 @@
 // expert_ops.hpp -- device helpers and kernel launchers of the operators around the
-// expert-major rows (expert_rows.hip) and of the RMS norm in front of them (rmsnorm.hip).
-// Not part of the public ABI.
+// expert-major rows (expert_rows.hip), of the RMS norm in front of them (rmsnorm.hip) and of
+// the experts' own products (expert_ffn.hip, expert_ffn_grad.hip). Not part of the public ABI.
 #pragma once
 
 #include "ep_internal.hpp"
@@ -114,5 +114,32 @@ hipError_t launch_dispatch_permute_grad(const void* grad_rows, const float* grad
                                         int64_t num_rows, const int32_t* expert_slot, int64_t T,
                                         int H, int k, void* grad_x, float* grad_w,
                                         int32_t* error_flag, hipStream_t stream);
+
+// expert_ffn.hip, expert_ffn_grad.hip: the experts' own products. Rows of expert e are
+// offset[e] .. offset[e + 1] - 1 of every rows' array.
+struct GemmArgs {
+    const void* a;             // the m side
+    const void* b;             // the n side: weights, or a weight gradient's second rows' array
+    const float* a_scales;     // e4m3: [rows][K/128]
+    const float* b_scales;     // e4m3: [E][N/128][K/128]
+    const int32_t* offset;     // [E + 1] first row of each expert
+    int E;
+    int64_t num_rows;
+    int M;                     // weight gradient: channels of the m side; otherwise unused
+    int N;                     // channels of the n side (gate_up: of the gate alone)
+    int K;                     // inner size (weight gradient: unused, an expert's rows)
+    void* out;                 // act; expert_out; grad_gate_up; grad_x; grad_weight
+    void* gate_up;             // gate_up: bf16 out (nullable); down_grad: bf16 in (nullable)
+    uint8_t* codes;            // gate_up: e4m3 out (nullable); down_grad: e4m3 in (nullable)
+    float* scales;             // their scales
+    void* act;                 // down_grad: bf16 out (nullable)
+    int out_fp32, accumulate;  // weight gradient
+    int32_t* error_flag;
+};
+hipError_t launch_expert_gate_up(const GemmArgs& g, bool fp8, hipStream_t stream);
+hipError_t launch_expert_down(const GemmArgs& g, bool fp8, hipStream_t stream);
+hipError_t launch_expert_down_grad(const GemmArgs& g, hipStream_t stream);
+hipError_t launch_expert_gate_up_grad(const GemmArgs& g, hipStream_t stream);
+hipError_t launch_expert_weight_grad(const GemmArgs& g, hipStream_t stream);
 
 }  // namespace ep

@@ -30,7 +30,9 @@
  * and the operators around the expert-major rows, with their gradients: ep_rmsnorm (the
  * residual's addition, the norm and an e4m3 output), ep_dispatch_permute_fp8 and
  * ep_combine_unpermute; ep_rmsnorm_grad, ep_dispatch_permute_grad and
- * ep_combine_unpermute_grad.
+ * ep_combine_unpermute_grad; and the experts between them: ep_expert_gate_up and
+ * ep_expert_down in bf16 and e4m3, ep_expert_down_grad, ep_expert_gate_up_grad and
+ * ep_expert_weight_grad.
  *
  * Conventions for every entry point:
  *  - Every array argument is a DEVICE pointer owned by the caller; the library allocates
@@ -87,6 +89,7 @@ enum {
 #define EP_LAYOUT_SCRATCH_BYTES 4194304  /* device scratch of ep_get_layout_no_alloc (4 MiB) */
 #define EP_COUNTS_MAX_RANKS 64  /* largest num_ranks of ep_layout_counts / ep_dispatch_layout */
 #define EP_LAYOUT_DISPATCH_MAX_TOKENS 256  /* largest batch of ep_layout_dispatch */
+#define EP_EXPERT_MAX_WIDTH (1 << 20)  /* largest hidden or inter of the ep_expert_ calls */
 
 /* Static string for a status code; never NULL. */
 const char *ep_status_string(int status);
@@ -641,6 +644,102 @@ int ep_dispatch_permute_grad(const void *grad_perm_x, const float *grad_perm_wei
                              int64_t num_rows, int64_t num_tokens, int hidden, int num_topk,
                              const int32_t *expert_slot, void *grad_x, float *grad_topk_weights,
                              int32_t *error_flag, void *stream);
+
+/* The experts of a mixture-of-experts block, on rows sorted by expert (as ep_dispatch_permute
+ * and ep_dispatch_permute_fp8 write them): the gated feed-forward block
+ *   gate = x Wg^T, up = x Wu^T, act = silu(gate) * up, out = act Wd^T,  silu(g) = g / (1 + e^-g)
+ * and its gradients, one set of weights per expert. The pages stop at the rows a grouped
+ * product consumes ("[PR #634] Hybrid ep nixl restripe", "dispatch+permute"); these products
+ * are this library's own.
+ *
+ * Common to all of them:
+ *   num_rows       rows of every rows' array, used or not (the permute's capacity).
+ *   expert_offset  int32 [E+1] in device memory, from ep_get_layout: expert e's rows are
+ *                  expert_offset[e] .. expert_offset[e+1]-1. Rows before the first and behind
+ *                  the last expert's are neither read nor written. Rows >= num_rows are
+ *                  skipped and set EP_DEVERR_SLOT_RANGE; offsets that are negative or descend
+ *                  set it too, and nothing is computed.
+ *   hidden H, inter I: 1 .. EP_EXPERT_MAX_WIDTH, multiples of 8 (of 128 where e4m3 is read or
+ *                  written; else EP_ERR_ALIGN). 1 <= num_experts E <= EP_MAX_EXPERTS,
+ *                  0 <= num_rows <= INT32_MAX, and (num_rows / 256 + 1) * (max(H, 2 I) / 128 + 1)
+ *                  <= INT32_MAX.
+ *   Arrays are 16-byte aligned (scales, offsets and the flag 4-byte). Products are summed in
+ *   fp32, in an order fixed by the sizes and the expert's rows; every output is rounded once.
+ *   Outputs must not overlap inputs or each other, but where a call says so.
+ *   e4m3 rows have one fp32 scale per 128 channels, e4m3 weights one per 128 x 128 block; a
+ *   value is code * scale. e4m3 outputs are scaled as ep_rmsnorm's: per row and group of 128
+ *   channels a = max |value|, scale = max(a, 2^-100) / 448 (1.0 for zeros), the code rounded to
+ *   nearest even from fp32.
+ * Errors: EP_ERR_ARG, EP_ERR_ALIGN, EP_ERR_HIP.
+ *
+ * ep_expert_gate_up -- both projections, the activation and the product.
+ * In:  x          bf16 [num_rows][H]
+ *      w_gate_up  bf16 [E][2I][H]: Wg's rows, then Wu's
+ * Out: act        bf16 [num_rows][I], from the unrounded gate and up
+ *      gate_up    bf16 [num_rows][2I]: gate's channels, then up's, for the backward  (nullable)
+ *      gate_up_fp8 uint8 [num_rows][2I], gate_up_scales fp32 [num_rows][2I/128]: the same in
+ *                 e4m3, half the bytes (nullable, both or none; I % 128 == 0) */
+int ep_expert_gate_up(const void *x, const void *w_gate_up, const int32_t *expert_offset,
+                      int num_experts, int64_t num_rows, int hidden, int inter, void *act,
+                      void *gate_up, uint8_t *gate_up_fp8, float *gate_up_scales,
+                      int32_t *error_flag, void *stream);
+
+/* ep_expert_gate_up_fp8 -- the same in e4m3, for serving.
+ * In:  x_fp8 uint8 [num_rows][H], x_scales fp32 [num_rows][H/128] (as ep_dispatch_permute_fp8
+ *      writes them); w_fp8 uint8 [E][2I][H], w_scales fp32 [E][2I/128][H/128]
+ * Out: act_fp8 uint8 [num_rows][I], act_scales fp32 [num_rows][I/128] */
+int ep_expert_gate_up_fp8(const uint8_t *x_fp8, const float *x_scales, const uint8_t *w_fp8,
+                          const float *w_scales, const int32_t *expert_offset, int num_experts,
+                          int64_t num_rows, int hidden, int inter, uint8_t *act_fp8,
+                          float *act_scales, int32_t *error_flag, void *stream);
+
+/* ep_expert_down -- In: act bf16 [num_rows][I]; w_down bf16 [E][H][I].
+ * Out: expert_out bf16 [num_rows][H], as ep_combine_unpermute takes it. */
+int ep_expert_down(const void *act, const void *w_down, const int32_t *expert_offset,
+                   int num_experts, int64_t num_rows, int hidden, int inter, void *expert_out,
+                   int32_t *error_flag, void *stream);
+
+/* ep_expert_down_fp8 -- In: act_fp8 uint8 [num_rows][I], act_scales fp32 [num_rows][I/128];
+ *      w_fp8 uint8 [E][H][I], w_scales fp32 [E][H/128][I/128].
+ * Out: expert_out bf16 [num_rows][H]. */
+int ep_expert_down_fp8(const uint8_t *act_fp8, const float *act_scales, const uint8_t *w_fp8,
+                       const float *w_scales, const int32_t *expert_offset, int num_experts,
+                       int64_t num_rows, int hidden, int inter, void *expert_out,
+                       int32_t *error_flag, void *stream);
+
+/* ep_expert_down_grad -- back through the second product and the activation: with
+ * da = grad_expert_out Wd (fp32, not rounded) and s = 1 / (1 + e^-gate),
+ *   grad_gate = da up s (1 + gate (1 - s)),  grad_up = da gate s.
+ * In:  grad_expert_out bf16 [num_rows][H]; w_down bf16 [E][H][I]
+ *      gate_up bf16 [num_rows][2I], or gate_up_fp8 and gate_up_scales: as the forward kept
+ *      them (one form, the other NULL)
+ * Out: grad_gate_up bf16 [num_rows][2I]; may be gate_up's memory
+ *      act bf16 [num_rows][I], the forward's output again from the kept gate and up, for
+ *      w_down's gradient, so that a training step need not keep it (nullable) */
+int ep_expert_down_grad(const void *grad_expert_out, const void *w_down,
+                        const int32_t *expert_offset, int num_experts, int64_t num_rows,
+                        int hidden, int inter, const void *gate_up, const uint8_t *gate_up_fp8,
+                        const float *gate_up_scales, void *grad_gate_up, void *act,
+                        int32_t *error_flag, void *stream);
+
+/* ep_expert_gate_up_grad -- In: grad_gate_up bf16 [num_rows][2I]; w_gate_up bf16 [E][2I][H].
+ * Out: grad_x bf16 [num_rows][H], as ep_dispatch_permute_grad takes it. */
+int ep_expert_gate_up_grad(const void *grad_gate_up, const void *w_gate_up,
+                           const int32_t *expert_offset, int num_experts, int64_t num_rows,
+                           int hidden, int inter, void *grad_x, int32_t *error_flag,
+                           void *stream);
+
+/* ep_expert_weight_grad -- for every expert e the sum over its rows of grad's row times input's
+ * row: w_gate_up's gradient with grad = grad_gate_up (M = 2I) and input = x (N = H), w_down's
+ * with grad = grad_expert_out (M = H) and input = act (N = I).
+ * In:  grad bf16 [num_rows][M]; input bf16 [num_rows][N]
+ * Out: grad_weight [E][M][N], bf16, or fp32 with weight_is_fp32 != 0: overwritten (zeros for
+ *      an expert without rows), or with accumulate != 0 added to (in fp32, rounded once)
+ * Sizes: M (`rows_out`) and N (`cols_out`) as hidden and inter above. */
+int ep_expert_weight_grad(const void *grad, const void *input, const int32_t *expert_offset,
+                          int num_experts, int64_t num_rows, int rows_out, int cols_out,
+                          void *grad_weight, int weight_is_fp32, int accumulate,
+                          int32_t *error_flag, void *stream);
 
 /* ep_hbm_copy -- measurement helper, not a step of the path: a plain 128-bit copy of
  * `bytes` bytes (a multiple of 16; both pointers 16-byte aligned) used as the HBM

@@ -1,0 +1,115 @@
+"""Plain 64-bit forms of the experts' products and the bounds their kernels have to keep, for
+the tests. CPU float64 tensors in and out; rows of expert e are off[e] .. off[e + 1] - 1.
+
+Bounds. A product summed over K terms in fp32, in any order and with additions that may cut
+instead of rounding (a step, 2^-23, each), is off by at most K 2^-23 times the sum of the
+terms' magnitudes, to first order; products of two bf16 or two e4m3 numbers are exact in fp32.
+The e4m3 form scales each block of 128 terms (two roundings) and adds it (one more). The e4m3
+matrix instruction adds 128 products at once in a window below the largest of them: measured on
+MI355X its sum is off by up to 2^-13 of the magnitudes' sum, taken here as 2^-12. The fast
+exponential and reciprocal of the activation are within 2^-20 relative for |gate| up to 80
+(the exponent's argument is rounded: 80 * 2^-24 * log2(e) and the two functions' own 2^-22).
+"""
+import torch
+
+import plain_ops as P
+from plain_ops import BF16, TINY_BF16, U, f64
+
+GROUP = 128
+FAST = 2.0**-18  # sigmoid and the few products around it, relative, with room for |gate| to 80
+
+
+def experts(off):
+    return [(e, slice(int(off[e]), int(off[e + 1]))) for e in range(len(off) - 1)]
+
+
+def fp8_rows(codes, scales):
+    v = codes.cpu().view(torch.float8_e4m3fn).to(torch.float64)
+    return v * f64(scales).repeat_interleave(GROUP, dim=1)
+
+
+def fp8_weights(codes, scales):
+    v = codes.cpu().view(torch.float8_e4m3fn).to(torch.float64)
+    return v * f64(scales).repeat_interleave(GROUP, dim=1).repeat_interleave(GROUP, dim=2)
+
+
+def product_error(K, fp8=False):
+    """Relative to the sum of the terms' magnitudes."""
+    return 2.0**-12 + (K / 128 + 4) * 2.0**-23 if fp8 else (K + 2) * 2.0**-23
+
+
+def nt(a, w, off):
+    """(a_e w_e^T, the sums of the terms' magnitudes)."""
+    out = torch.zeros((a.shape[0], w.shape[1]), dtype=torch.float64)
+    mag = torch.zeros_like(out)
+    for e, r in experts(off):
+        out[r] = a[r] @ w[e].T
+        mag[r] = a[r].abs() @ w[e].abs().T
+    return out, mag
+
+
+def nn(a, w, off):
+    return nt(a, w.transpose(1, 2).contiguous(), off)
+
+
+def gate_up(x, w, off, fp8=False):
+    """(gate|up, its bound before rounding, act, act's bound before rounding)."""
+    gu, mag = nt(x, w, off)
+    err = product_error(x.shape[1], fp8) * mag
+    I = gu.shape[1] // 2
+    g, u, eg, eu = gu[:, :I], gu[:, I:], err[:, :I], err[:, I:]
+    s = torch.sigmoid(g)
+    act = g * s * u
+    # |d silu / dg| <= 1.1
+    bound = 1.1 * eg * (u.abs() + eu) + (g * s).abs() * eu + FAST * act.abs()
+    return gu, err, act, bound
+
+
+def rounded(value, err):
+    """The bound of a bf16 output whose fp32 value is within err."""
+    return err + BF16 * (value.abs() + err) + TINY_BF16
+
+
+def codes_bound(value, err, scale_want):
+    """Bound of code * scale: the value's own error, half a step of the code (of the scale where
+    it is below the smallest normal code), and the scale's error through the group's largest."""
+    step = scale_want.repeat_interleave(GROUP, dim=1)
+    return 2 * err + 2.0**-4 * (value.abs() + err) + 2.0**-10 * step * 1.01 + 2.0**-20 * value.abs()
+
+
+def scale_bound(value, err, scale_want):
+    top = err.view(err.shape[0], err.shape[1] // GROUP, GROUP).amax(dim=2)
+    return top / 448.0 + 4 * U * scale_want
+
+
+def down_grad(dout, w, gu, off):
+    """(grad of gate|up, its bound, act again, its bound)."""
+    da, mag = nn(dout, w, off)
+    err = product_error(dout.shape[1]) * mag
+    I = gu.shape[1] // 2
+    g, u = gu[:, :I], gu[:, I:]
+    s = torch.sigmoid(g)
+    fg = u * s * (1 + g * (1 - s))
+    fu = g * s
+    # 1 + g (1 - s) cancels for g < 0: its terms' magnitudes carry the rounding
+    mg = u.abs() * s * (1 + (g * (1 - s)).abs())
+    grad = torch.cat([da * fg, da * fu], dim=1)
+    bound = torch.cat([err * fg.abs() + FAST * (da.abs() + err) * mg,
+                       err * fu.abs() + FAST * (da.abs() + err) * fu.abs()], dim=1)
+    act = fu * u
+    return grad, rounded(grad, bound), act, rounded(act, FAST * act.abs())
+
+
+def weight_grad(grad, inp, off):
+    E = len(off) - 1
+    out = torch.zeros((E, grad.shape[1], inp.shape[1]), dtype=torch.float64)
+    mag = torch.zeros_like(out)
+    n = torch.zeros((E, 1, 1), dtype=torch.float64)
+    for e, r in experts(off):
+        out[e] = grad[r].T @ inp[r]
+        mag[e] = grad[r].abs().T @ inp[r].abs()
+        n[e] = r.stop - r.start
+    return out, (n + 2) * 2.0**-23 * mag
+
+
+assert_within = P.assert_within
