@@ -24,7 +24,9 @@ constexpr int kGemmThreads = 512;   // 8 waves, 2 along m and 4 along n
 constexpr int kGemmWaves = kGemmThreads / kWave;
 constexpr int kStepBytes = 128;     // bytes of k per row and step: 64 bf16 or 128 e4m3
 constexpr int kOperandBytes = 256 * kStepBytes;  // one operand of one step in LDS
+constexpr int kHalfBytes = kOperandBytes / 2;
 constexpr int kScaleBytes = 2048;   // one step's row scales in LDS (the second half unused)
+constexpr int kScaleSlots = 4;
 constexpr int kAmaxBytes = kTileM * 2 * 4 * 4;  // [row][gate, up][wave along n] magnitudes
 constexpr uint32_t kOutOfBuffer = 0x80000000u;  // an offset past every buffer made here
 
@@ -89,27 +91,54 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // ---------------------------------------------------------------- which tile is whose
-// The tiles of all experts in one order: expert after expert, and within one in bands of four
-// along m with n inside, so that the 32 blocks of one die share four parts of A and eight of
-// B in its L2. An expert of c rows has ceil(c / kTileM) tiles along m of about equal heights.
-// Every lane holds the number of such tiles before its chunk of experts; a tile is found by a
-// ballot and a walk through one chunk. Offsets are taken as non-negative and ascending, and
-// clamped to num_rows; where they are not, nothing is computed.
-constexpr int kBandM = 4;
+// The tiles of all experts in one order: expert after expert, and within one in bands of at most
+// kBandM tiles along m (of about equal numbers) with n outside, so that the 32 blocks of one die
+// take about six parts of A and five to eight of B between them and share both in its L2.
+// An expert of c rows has ceil(c / kTileM) tiles along m of about equal heights. Every lane
+// holds the number of such tiles before its chunk of experts; a tile is found by a ballot and a
+// walk through one chunk. Offsets are taken as non-negative and ascending, and clamped to
+// num_rows; where they are not, nothing is computed.
+// The blocks take tiles in rounds. Where the last round's tiles are at most half as many as the
+// blocks, each is cut along m in two (in four: a quarter), so that the round takes that much
+// less: `whole` tiles are not cut, `cut` pieces make one of the others.
+constexpr int kBandM = 8;
 
 struct Tile {
     int expert;
-    int m0, n0;    // first row (within the expert) or channel of the m side, and of the n side
-    int64_t row0;  // the expert's first row
-    int rows;      // the expert's rows
-    int height;    // valid rows (channels) of the m side in this tile
+    int m0, n0;  // first row (within the expert) or channel of the m side, and of the n side
+    int row0;    // the expert's first row
+    int rows;    // the expert's rows
+    int height;  // valid rows (channels) of the m side in this tile
+};
+
+// A block's next four tiles, in the lanes of one register: the loads run up to two tiles ahead of
+// the products, and looking a tile up takes more registers than the products leave.
+struct TileRing {
+    int lanes = 0;
+    __device__ __forceinline__ void put(int n, const Tile& t) {
+        const int at = (n & 3) * 8;
+        const int field[6] = {t.expert, t.m0, t.n0, t.row0, t.rows, t.height};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const int v = __builtin_amdgcn_readfirstlane(field[i]);
+            if (lane_id() == at + i) lanes = v;
+        }
+    }
+    __device__ __forceinline__ Tile get(int n) const {
+        const int at = (n & 3) * 8;
+        int field[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) field[i] = __builtin_amdgcn_readlane(lanes, at + i);
+        return Tile{field[0], field[1], field[2], field[3], field[4], field[5]};
+    }
 };
 
 struct TileMap {
     const int32_t* offset;
     int64_t num_rows;
     int chunk, E, nt, first;
-    int64_t total;
+    int64_t total, whole;  // of all pieces; of the tiles before the last round's
+    int cut;
     bool by_rows;  // m tiles cover an expert's rows; else M channels, mt of them per expert
     int M, mt;
 
@@ -146,22 +175,42 @@ struct TileMap {
         bad = wave_ballot(bad) != 0;
         over = wave_ballot(over) != 0;
         if (bad) total = 0;
+        const int blocks = gridDim.x;
+        const int rest = static_cast<int>(total % blocks);
+        cut = rest * 4 <= blocks ? 4 : rest * 2 <= blocks ? 2 : 1;
+        whole = total - rest;
+        total = whole + static_cast<int64_t>(rest) * cut;
         if ((bad || over) && blockIdx.x == 0 && threadIdx.x == 0)
             raise_error(g.error_flag, kErrSlotRange);
     }
 
     __device__ __forceinline__ void place(Tile& t, int in_expert, int mts, int n_tile) const {
-        const int band = in_expert / (kBandM * nt);
-        const int r = in_expert - band * kBandM * nt;
-        const int high = min(kBandM, mts - band * kBandM);
-        const int n = r / high;
+        const int bands = (mts + kBandM - 1) / kBandM;
+        const int high = (mts + bands - 1) / bands;
+        const int band = in_expert / (high * nt);
+        const int r = in_expert - band * high * nt;
+        const int here = min(high, mts - band * high);
+        const int n = r / here;
         t.n0 = n * n_tile;
-        t.m0 = band * kBandM + (r - n * high);  // the m tile's number, made a row by the caller
+        t.m0 = band * high + (r - n * here);  // the m tile's number, made a row by the caller
+    }
+
+    // The piece's rows (channels): of `height` from t.m0 on its share, in whole subtiles.
+    __device__ __forceinline__ void take(Tile& t, int piece, int pieces) const {
+        const int each = ((t.height + pieces - 1) / pieces + 15) & ~15;
+        t.m0 += piece * each;
+        t.height = max(0, min(each, t.height - piece * each));
     }
 
     __device__ __forceinline__ Tile find(int64_t index, int n_tile) const {
         Tile t;
-        int mts, in_expert;
+        int mts, in_expert, piece = 0, pieces = 1;
+        if (index >= whole) {
+            const int r = static_cast<int>(index - whole);
+            index = whole + r / cut;
+            piece = r % cut;
+            pieces = cut;
+        }
         if (by_rows) {
             const uint64_t le =
                 wave_ballot(static_cast<int64_t>(first) * nt <= index);
@@ -181,7 +230,7 @@ struct TileMap {
                 ++e;
             }
             t.expert = e;
-            t.row0 = a;
+            t.row0 = static_cast<int>(a);
             in_expert = static_cast<int>(index - static_cast<int64_t>(base) * nt);
             place(t, in_expert, mts, n_tile);
             const int each = ((t.rows + mts - 1) / mts + 15) & ~15;
@@ -191,55 +240,65 @@ struct TileMap {
             const int per = mt * nt;
             t.expert = static_cast<int>(index / per);
             in_expert = static_cast<int>(index - static_cast<int64_t>(t.expert) * per);
-            t.row0 = min<int64_t>(offset[t.expert], num_rows);
-            t.rows = static_cast<int>(min<int64_t>(offset[t.expert + 1], num_rows) - t.row0);
+            t.row0 = static_cast<int>(min<int64_t>(offset[t.expert], num_rows));
+            t.rows = static_cast<int>(min<int64_t>(offset[t.expert + 1], num_rows)) - t.row0;
             place(t, in_expert, mt, n_tile);
             t.m0 *= kTileM;
             t.height = min(kTileM, M - t.m0);
         }
+        take(t, piece, pieces);
         return t;
     }
 };
 
 // ---------------------------------------------------------------- one operand's loads
-// By rows: a step is 128 bytes of each of 256 rows, row after row in LDS, with a row's 16-byte
-// word c at place c ^ (row & 7): eight lanes of a fragment's read, on eight rows, then hit
-// eight different places. Each wave load writes eight rows. By columns: a step is 64 rows of k
-// of 256 channels (512 bytes), with the 32-byte pair of words p at place p ^ turn(k), so that
-// a transposing read's four rows (of each of two groups of lanes) lie in different banks.
+// An operand's step is two halves of 16 KB. By rows: 128 bytes of each of 128 rows, row after row
+// in LDS, with a row's 16-byte word c at place c ^ (row & 7): eight lanes of a fragment's read,
+// on eight rows, then hit eight different places. By columns: 64 rows of k of 128 channels (256
+// bytes each), with the 32-byte pair of words p at place p ^ turn(k), so that a transposing
+// read's four rows (of each of two groups of lanes) lie in different banks. Of the m side the
+// first half holds the subtiles that the first phase of a step reads (32 `split` rows of the
+// tile), the second half the rest.
 __device__ __forceinline__ int turn(int k) { return (k & 3) | ((k >> 1) & 4); }
 
 template <bool kByRows>
 struct OperandLoads {
-    static constexpr int kLoads = 4;  // per wave and step
-    uint32_t voff[kLoads];
+    uint32_t voff[4];  // of a wave's two loads of the first half, and of the second
 
-    // rows: valid rows from the first; width: valid bytes of a row of `stride`
-    __device__ __forceinline__ void init_rows(int wave, int lane, int rows, uint32_t stride) {
+    // rows: valid rows of the tile; the second half's first is row `split`
+    __device__ __forceinline__ void init_rows(int wave, int lane, int rows, int split,
+                                              uint32_t stride) {
 #pragma unroll
-        for (int t = 0; t < kLoads; ++t) {
-            const int row = (t * kGemmWaves + wave) * 8 + lane / 8;
-            voff[t] = row < rows ? row * stride + (((lane & 7) ^ (lane >> 3)) * 16) : kOutOfBuffer;
+        for (int t = 0; t < 4; ++t) {
+            const int r = ((t & 1) * kGemmWaves + wave) * 8 + lane / 8;
+            const int row = t < 2 ? r : r + split;
+            const bool in = row < rows && (t >= 2 || r < split);
+            voff[t] = in ? row * stride + (((lane & 7) ^ (lane >> 3)) * 16) : kOutOfBuffer;
         }
     }
     // columns: valid columns from col0
     __device__ __forceinline__ void init_columns(int wave, int lane, int col0, int columns,
-                                                 uint32_t stride) {
+                                                 int split, uint32_t stride) {
 #pragma unroll
-        for (int t = 0; t < kLoads; ++t) {
-            const int k = (t * kGemmWaves + wave) * 2 + lane / 32;
-            const int word = (lane & 31) ^ (2 * turn(k));
-            voff[t] = word * 8 < columns ? k * stride + (col0 + word * 8) * 2 : kOutOfBuffer;
+        for (int t = 0; t < 4; ++t) {
+            const int k = ((t & 1) * kGemmWaves + wave) * 4 + lane / 16;
+            const int c = ((lane & 15) ^ (2 * turn(k))) * 8;
+            const int col = t < 2 ? c : c + split;
+            const bool in = col < columns && (t >= 2 || c < split);
+            voff[t] = in ? k * stride + (col0 + col) * 2 : kOutOfBuffer;
         }
     }
     // by rows, last step: words past the row's end read zeros
     __device__ __forceinline__ void cut(int lane, int words) {
         if (((lane & 7) ^ (lane >> 3)) >= words) {
 #pragma unroll
-            for (int t = 0; t < kLoads; ++t) voff[t] = kOutOfBuffer;
+            for (int t = 0; t < 4; ++t) voff[t] = kOutOfBuffer;
         }
     }
 };
+
+// A tile of mt pairs of subtiles is computed in two phases of about equal length.
+__device__ __forceinline__ constexpr int first_phase(int mt) { return (mt + 1) / 2; }
 
 // ---------------------------------------------------------------- the kernel
 template <GemmOp kOp, bool kFp8>
@@ -252,22 +311,34 @@ struct GemmShape {
     static constexpr int kElem = kFp8 ? 1 : 2;
     static constexpr int kStepK = kStepBytes / kElem;
     static constexpr int kStages = 2;
-    static constexpr int kStageBytes = 2 * kOperandBytes + (kFp8 ? kScaleBytes : 0);
-    static constexpr int kLoads = 8 + (kFp8 ? 1 : 0);  // per wave and step
-    static constexpr bool kAmax = kGated;
-    static constexpr int kLdsBytes = kStages * kStageBytes + (kAmax ? kAmaxBytes : 0);
+    static constexpr int kStageBytes = 2 * kOperandBytes;  // the m side, then the n side
+    static constexpr int kLoads = 8 + (kFp8 ? 1 : 0);      // per wave and step
+    static constexpr int kScalesAt = kStages * kStageBytes;
+    static constexpr int kAmaxAt = kScalesAt + (kFp8 ? kScaleSlots * kScaleBytes : 0);
+    static constexpr int kLdsBytes = kAmaxAt + (kGated ? kAmaxBytes : 0);
     static_assert(kLdsBytes <= 160 * 1024, "LDS of one CU");
 };
+
+// A tile without rows to sum over (an expert's weight gradient) or to compute still takes one step,
+// of zeros.
+template <GemmOp kOp, bool kFp8>
+__device__ __forceinline__ int tile_steps(const GemmArgs& g, const Tile& t) {
+    using S = GemmShape<kOp, kFp8>;
+    const int k = t.height > 0 ? (S::kOverRows ? t.rows : g.K) : 0;
+    return max(1, (k + S::kStepK - 1) / S::kStepK);
+}
 
 // The stream of steps that a block loads: its tiles one after the other, the steps of each.
 template <GemmOp kOp, bool kFp8>
 struct Producer {
     using S = GemmShape<kOp, kFp8>;
     const GemmArgs& g;
-    const TileMap& map;
+    const uint32_t lds;
     int wave, lane;
-    int64_t index, stride;
-    int step, steps;
+    int tile, tiles;  // the block's present one, and how many it has
+    int step, steps;  // of the tile
+    int count;        // of all steps so far
+    bool live;
     Tile t;
     OperandLoads<S::kAByRows> a;
     OperandLoads<S::kBByRows> b;
@@ -275,45 +346,45 @@ struct Producer {
     const char *a_base = nullptr, *b_base = nullptr, *b_up = nullptr;
     uint32_t a_row, b_row;  // bytes between rows in memory
 
-    __device__ __forceinline__ Producer(const GemmArgs& g_, const TileMap& m, int64_t first,
-                                        int64_t by)
-        : g(g_), map(m), wave(__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)),
-          lane(lane_id()), index(first), stride(by), step(0), steps(0), t{} {
+    __device__ __forceinline__ Producer(const GemmArgs& g_, uint32_t lds_, int tiles_,
+                                        const TileRing& ring)
+        : g(g_), lds(lds_), wave(__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)),
+          lane(lane_id()), tile(0), tiles(tiles_), step(0), steps(0), count(0), live(false), t{} {
         a_row = static_cast<uint32_t>(S::kOverRows ? g.M : g.K) * S::kElem;
         b_row = static_cast<uint32_t>(S::kBByRows ? g.K : g.N) * S::kElem;
-        if (index < map.total) start();
+        if (tile < tiles) start(ring);
     }
 
-    __device__ __forceinline__ void start() {
-        t = map.find(index, S::kNTile);
+    __device__ __forceinline__ void start(const TileRing& ring) {
+        t = ring.get(tile);
         step = 0;
-        const int k = S::kOverRows ? t.rows : g.K;
-        steps = (k + S::kStepK - 1) / S::kStepK;
-        const char* rows_a = static_cast<const char*>(g.a) + t.row0 * a_row;
+        steps = tile_steps<kOp, kFp8>(g, t);
+        const int split = 32 * first_phase((t.height + 31) / 32);
+        const char* rows_a = static_cast<const char*>(g.a) + static_cast<int64_t>(t.row0) * a_row;
         if constexpr (S::kAByRows) {
             a_base = rows_a + static_cast<int64_t>(t.m0) * a_row;
-            a.init_rows(wave, lane, t.height, a_row);
+            a.init_rows(wave, lane, t.height, split, a_row);
         } else {
             a_base = rows_a;
-            a.init_columns(wave, lane, t.m0, t.height, a_row);
+            a.init_columns(wave, lane, t.m0, t.height, split, a_row);
         }
         const int nv = min(S::kNTile, g.N - t.n0);
         if constexpr (S::kOverRows) {
-            b_base = static_cast<const char*>(g.b) + t.row0 * b_row;
-            b.init_columns(wave, lane, t.n0, nv, b_row);
+            b_base = static_cast<const char*>(g.b) + static_cast<int64_t>(t.row0) * b_row;
+            b.init_columns(wave, lane, t.n0, nv, kTileN / 2, b_row);
         } else {
             const int64_t weights = static_cast<int64_t>(S::kGated ? 2 : 1) * g.N * g.K * S::kElem;
             b_base = static_cast<const char*>(g.b) + t.expert * weights;
             if constexpr (S::kBByRows) {
                 b_base += static_cast<int64_t>(t.n0) * b_row;
                 b_up = b_base + static_cast<int64_t>(g.N) * b_row;
-                b.init_rows(wave, lane, nv, b_row);
-                if constexpr (S::kGated) {  // tile rows 128..255 are the up projection's
+                b.init_rows(wave, lane, nv, kTileN / 2, b_row);
+                if constexpr (S::kGated) {  // the second half is the up projection's
 #pragma unroll
                     for (int i = 2; i < 4; ++i) b.voff[i] = b.voff[i - 2];
                 }
             } else {
-                b.init_columns(wave, lane, t.n0, nv, b_row);
+                b.init_columns(wave, lane, t.n0, nv, kTileN / 2, b_row);
             }
         }
         if constexpr (kFp8) {  // waves 0..3 take 64 rows' scales each
@@ -323,12 +394,33 @@ struct Producer {
         }
     }
 
-    __device__ __forceinline__ void issue(uint32_t lds) {
-        while (step == steps && index < map.total) {  // an expert without rows has no steps
-            index += stride;
-            if (index < map.total) start();
+    // The loads of the m side's half h of the present step.
+    __device__ __forceinline__ void issue_a(int h) {
+        const uint32_t dst = lds + (count & 1) * S::kStageBytes + h * kHalfBytes + wave * 1024;
+        const int k0 = step * S::kStepK;
+        i32x4 buf;
+        uint32_t along = 0;
+        if constexpr (S::kAByRows) {
+            buf = scalar_buffer(a_base, live ? static_cast<uint32_t>(t.height) * a_row : 0);
+            along = static_cast<uint32_t>(step) * kStepBytes;
+        } else {
+            const uint32_t n = live ? min(64, t.rows - k0) : 0;
+            buf = scalar_buffer(a_base + static_cast<int64_t>(k0) * a_row, n * a_row);
         }
-        const bool live = index < map.total;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            load_lds16(buf, dst + i * kGemmWaves * 1024, a.voff[2 * h + i], along);
+    }
+
+    // The next step's n side, the first half of its m side and its scales. With no step left the
+    // loads go on, of buffers of no bytes, so that the counts of loads in flight hold.
+    __device__ __forceinline__ void issue_first(const TileRing& ring) {
+        if (step == steps && tile < tiles) {
+            ++tile;
+            if (tile < tiles) start(ring);
+        }
+        live = tile < tiles;
+        if (!live) step = 0;
         const int k0 = step * S::kStepK;
         if constexpr (S::kAByRows || S::kBByRows) {
             if (live && k0 + S::kStepK > g.K) {  // only at a tile's last step
@@ -337,47 +429,37 @@ struct Producer {
                 if constexpr (S::kBByRows) b.cut(lane, words);
             }
         }
-        const uint32_t along = live ? static_cast<uint32_t>(step) * kStepBytes : 0u;
-        const uint32_t dst = lds + wave * 1024;
-        if constexpr (S::kAByRows) {
-            const auto buf = scalar_buffer(a_base, live ? static_cast<uint32_t>(t.height) * a_row : 0);
+        const uint32_t dst =
+            lds + (count & 1) * S::kStageBytes + kOperandBytes + wave * 1024;
+        if constexpr (S::kBByRows) {
+            const uint32_t along = static_cast<uint32_t>(step) * kStepBytes;
+            const uint32_t n = live ? static_cast<uint32_t>(min(S::kNTile, g.N - t.n0)) * b_row : 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                load_lds16(buf, dst + i * kGemmWaves * 1024, a.voff[i], along);
-        } else {
-            const uint32_t n = live ? min(64, t.rows - k0) : 0;
-            const auto buf = scalar_buffer(a_base + static_cast<int64_t>(k0) * a_row, n * a_row);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) load_lds16(buf, dst + i * kGemmWaves * 1024, a.voff[i], 0);
-        }
-        const uint32_t dst_b = dst + kOperandBytes;
-        if constexpr (S::kBByRows) {
-            const uint32_t n = live ? static_cast<uint32_t>(min(S::kNTile, g.N - t.n0)) * b_row : 0;
-            const auto buf = scalar_buffer(b_base, n);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (S::kGated) {
-                    const auto half = scalar_buffer(i < 2 ? b_base : b_up, n);
-                    load_lds16(half, dst_b + i * kGemmWaves * 1024, b.voff[i], along);
-                } else {
-                    load_lds16(buf, dst_b + i * kGemmWaves * 1024, b.voff[i], along);
-                }
-            }
+                load_lds16(scalar_buffer(S::kGated && i >= 2 ? b_up : b_base, n),
+                           dst + i * kGemmWaves * 1024, b.voff[i], along);
         } else {
             const uint32_t n = live ? min(64, (S::kOverRows ? t.rows : g.K) - k0) : 0;
             const auto buf = scalar_buffer(b_base + static_cast<int64_t>(k0) * b_row, n * b_row);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                load_lds16(buf, dst_b + i * kGemmWaves * 1024, b.voff[i], 0);
+                load_lds16(buf, dst + i * kGemmWaves * 1024, b.voff[i], 0);
         }
+        issue_a(0);
         if constexpr (kFp8) {
             const uint32_t row = static_cast<uint32_t>(g.K / 128) * 4u;
-            const auto buf = scalar_buffer(g.a_scales + (t.row0 + t.m0) * (g.K / 128),
-                                        live ? static_cast<uint32_t>(t.height) * row : 0);
-            load_lds4(buf, lds + 2 * kOperandBytes + wave * 256, scale_voff, live ? step * 4u : 0u);
+            const auto buf = scalar_buffer(g.a_scales + (static_cast<int64_t>(t.row0) + t.m0) * (g.K / 128),
+                                           live ? static_cast<uint32_t>(t.height) * row : 0);
+            load_lds4(buf, lds + S::kScalesAt + (count & 3) * kScaleBytes + wave * 256, scale_voff,
+                      static_cast<uint32_t>(step) * 4u);
         }
-        ++step;
-        if (!live) step = steps;
+    }
+
+    // The second half of the step's m side; on to the next step.
+    __device__ __forceinline__ void issue_second() {
+        issue_a(1);
+        ++count;
+        if (live) ++step;
     }
 };
 
@@ -406,76 +488,93 @@ __device__ __forceinline__ float group_amax(float a) {
     return a > 0.0f ? fmaxf(a, kSmallestAmax) : kE4m3Largest;
 }
 
-// A lane holds row (column) l % 16 of a fragment and the words of k that belong to l / 16.
-template <GemmOp kOp, bool kFp8, int kMT>
-__device__ __forceinline__ void gemm_step(f32x4 (&acc)[8][4], const char* lds_a, const char* lds_b,
-                                          const char* lds_s, int wm, int wn, int lane,
-                                          const float (&bs)[2]) {
-    using S = GemmShape<kOp, kFp8>;
-    const int row = lane & 15, quad = lane >> 4;
-    const int by_row = row * kStepBytes + ((quad ^ (row & 7)) * 16);
-    // by columns: lane's row of k within a group of 4, its 8 bytes within the pair
-    const int f = (row >> 2) | ((quad & 1) << 2);
-    const int by_col = (8 * quad + (row >> 2)) * 512 + (row & 3) * 8;
-    auto n_first = [&](int j) {
-        return S::kGated ? (j >> 1) * 128 + wn * 32 + (j & 1) * 16 : wn * 64 + j * 16;
-    };
-    auto read16 = [&](const char* base, bool rows, int first, int s) -> bf16x8 {
-        if (rows)
-            return *reinterpret_cast<const bf16x8*>(base + first * kStepBytes + (by_row ^ (s * 64)));
-        const char* p = base + by_col + s * 32 * 512 + (((first >> 4) ^ f) * 32);
+// Fragments of one wave: lane l holds row (column) l % 16 of a subtile and the words of k that
+// belong to l / 16: words l / 16 and 4 + l / 16 of the step's eight (any order of k will do as
+// long as both operands have it).
+union Fragment {
+    u32x4 word[2];
+    bf16x8 bf16[2];
+    i32x8 e4m3;
+};
+
+struct LanePlace {
+    int by_row;  // of the first word in a row subtile
+    int by_col;  // of the first 8 bytes in the column subtile of pair 0, turned
+
+    __device__ __forceinline__ explicit LanePlace(int lane) {
+        const int row = lane & 15, quad = lane >> 4;
+        by_row = row * kStepBytes + ((quad ^ (row & 7)) * 16);
+        const int f = (row >> 2) | ((quad & 1) << 2);  // turn(k) of the lane's rows of k
+        by_col = (8 * quad + (row >> 2)) * 256 + f * 32 + (row & 3) * 8;
+    }
+};
+
+// The subtile whose first row (column) within `half` is `first`.
+template <bool kByRows>
+__device__ __forceinline__ void read_fragment(Fragment& out, const char* half, int first,
+                                              const LanePlace& at) {
+    if constexpr (kByRows) {
+        const char* p = half + first * kStepBytes;
+        out.word[0] = *reinterpret_cast<const u32x4*>(p + at.by_row);
+        out.word[1] = *reinterpret_cast<const u32x4*>(p + (at.by_row ^ 64));
+    } else {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        union {
-            s16x4 h[2];
-            bf16x8 v;
-        } u;
-        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 512));
-        return u.v;
-    };
-    if constexpr (!kFp8) {
+        const char* p = half + (at.by_col ^ (first * 2));  // pair first / 16, of 32 bytes
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            bf16x8 b[4], a[kMT];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = read16(lds_b, S::kBByRows, n_first(j), s);
-#pragma unroll
-            for (int i = 0; i < kMT; ++i) a[i] = read16(lds_a, S::kAByRows, (2 * i + wm) * 16, s);
-#pragma unroll
-            for (int i = 0; i < kMT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
-        }
-    } else {
-        auto read32 = [&](const char* base, int first) -> i32x8 {
             union {
-                u32x4 h[2];
-                i32x8 v;
+                s16x4 h[2];
+                u32x4 w;
             } u;
-            u.h[0] = *reinterpret_cast<const u32x4*>(base + first * kStepBytes + by_row);
-            u.h[1] = *reinterpret_cast<const u32x4*>(base + first * kStepBytes + (by_row ^ 64));
-            return u.v;
-        };
-        i32x8 b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = read32(lds_b, n_first(j));
-#pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-            const i32x8 a = read32(lds_a, (2 * i + wm) * 16);
-            const float as = *reinterpret_cast<const float*>(lds_s + ((2 * i + wm) * 16 + row) * 4);
-            const float sc[2] = {as * bs[0], as * bs[1]};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    b[j], a, zero, 0, 0, 0, 0, 0, 0);
-                const float c = sc[S::kGated ? j >> 1 : 0];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], c, acc[i][j][r]);
-            }
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + s * 32 * 256));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + s * 32 * 256 + 4 * 256));
+            out.word[s] = u.w;
         }
+    }
+}
+
+template <GemmOp kOp, bool kFp8>
+__device__ __forceinline__ void read_n_side(Fragment (&b)[4], const char* operand, int wn,
+                                            const LanePlace& at) {
+    using S = GemmShape<kOp, kFp8>;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (S::kGated)  // gate's channels from the first half, up's from the second
+            read_fragment<S::kBByRows>(b[j], operand + (j >> 1) * kHalfBytes, wn * 32 + (j & 1) * 16,
+                                       at);
+        else
+            read_fragment<S::kBByRows>(b[j], operand + (wn >> 1) * kHalfBytes,
+                                       (wn & 1) * 64 + j * 16, at);
+    }
+}
+
+template <bool kFp8, bool kGated>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[4], const Fragment (&b)[4], const Fragment& a,
+                                         float as, const float (&bs)[2]) {
+    if constexpr (!kFp8) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].bf16[s], a.bf16[s], acc[j], 0,
+                                                                 0, 0);
+    } else {
+        const float sc[2] = {as * bs[0], as * bs[1]};
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            d[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j].e4m3, a.e4m3, zero, 0, 0, 0,
+                                                                    0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[j][r] = fmaf(d[j][r], sc[kGated ? j >> 1 : 0], acc[j][r]);
+        // the sums are made here: moved behind the wait that follows, they keep every product
+        // of the phase in registers, which then spill
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[j]));
     }
 }
 
@@ -485,7 +584,7 @@ template <GemmOp kOp, bool kFp8>
 __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32x4 (&acc)[8][4],
                                            char* lds_amax, int mt, int wm, int wn, int lane) {
     const int quad = lane >> 4;
-    const int64_t first_row = t.row0 + t.m0;
+    const int64_t first_row = static_cast<int64_t>(t.row0) + t.m0;
     if constexpr (kOp == GemmOp::kGateUp) {
         const int I = g.N;
         float(*amax)[2][4] = reinterpret_cast<float(*)[2][4]>(lds_amax);
@@ -656,35 +755,84 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
     }
 }
 
-// One tile's steps with kMT subtiles of 16 rows per wave. On entry the first step's loads are
-// on their way.
+// Ends a slot: this wave's LDS reads are in registers, and every wave gets here.
+__device__ __forceinline__ void end_slot() {
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// One tile's steps with kMT subtiles of 16 rows per wave. The block's two halves (waves 0..3 and
+// 4..7, one of each on every SIMD) take turns: while one multiplies, the other reads its next
+// fragments from LDS and issues loads, and a barrier ends each such slot. A step is four slots:
+//   waves 0..3   read 1   multiply 1   read 2       multiply 2
+//   waves 4..7   -        read 1       multiply 1   read 2       multiply 2
+// where reading 1 takes the n side and the first half of the m side and issues the second half
+// of the next step's m side; reading 2 takes the second half and issues the rest of the step
+// after the next into the places that reading 1 has left. Every load has six slots to arrive: of
+// a wave's loads all but the last kLoads have to be there at the end of every odd slot.
 template <GemmOp kOp, bool kFp8, int kMT>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& t, int steps,
-                                          Producer<kOp, kFp8>& p, f32x4 (&acc)[8][4], char* lds,
-                                          int& slot, int wm, int wn, int lane) {
+                                          Producer<kOp, kFp8>& p, f32x4 (&acc)[8][4],
+                                          const char* lds, int& count, const TileRing& ring, int wm,
+                                          int wn, const LanePlace& at, int lane) {
     using S = GemmShape<kOp, kFp8>;
+    constexpr int kP = first_phase(kMT);
     const float* bs_row = nullptr;
+    int64_t up_scales = 0;
+    float bs[2] = {1.0f, 1.0f};
     if constexpr (kFp8) {
         const int KB = g.K / 128;
         const int nb = S::kGated ? t.n0 / 128 : min((t.n0 + wn * 64) / 128, g.N / 128 - 1);
         bs_row = g.b_scales +
                  (static_cast<int64_t>(t.expert) * (S::kGated ? 2 : 1) * (g.N / 128) + nb) * KB;
+        up_scales = static_cast<int64_t>(g.N / 128) * KB;
     }
-    for (int step = 0; step < steps; ++step) {
-        wait_loads<0>();
-        lds_barrier();
-        char* now = lds + slot * S::kStageBytes;
-        slot ^= 1;
-        p.issue(lds_address(lds + slot * S::kStageBytes));
-        float bs[2] = {1.0f, 1.0f};
+    if (wm) end_slot();
+    for (int step = 0; step < steps; ++step, ++count) {
+        const char* stage = lds + (count & 1) * S::kStageBytes;
+        const char* scales = lds + S::kScalesAt + (count & 3) * kScaleBytes;
+        Fragment b[4], a[kP];
+        float as[kP];
+        read_n_side<kOp, kFp8>(b, stage + kOperandBytes, wn, at);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            read_fragment<S::kAByRows>(a[i], stage, (2 * i + wm) * 16, at);
+            if constexpr (kFp8)
+                as[i] = *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
+        }
         if constexpr (kFp8) {
             bs[0] = bs_row[step];
-            if constexpr (S::kGated)
-                bs[1] = bs_row[static_cast<int64_t>(g.N / 128) * (g.K / 128) + step];
+            if constexpr (S::kGated) bs[1] = bs_row[up_scales + step];
         }
-        gemm_step<kOp, kFp8, kMT>(acc, now, now + kOperandBytes, now + 2 * kOperandBytes, wm, wn,
-                                  lane, bs);
+        p.issue_second();
+        if (wm) wait_loads<S::kLoads>();
+        end_slot();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) multiply<kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
+        __builtin_amdgcn_s_setprio(0);
+        if (!wm) wait_loads<S::kLoads>();
+        end_slot();
+#pragma unroll
+        for (int i = kP; i < kMT; ++i) {
+            read_fragment<S::kAByRows>(a[i - kP], stage + kHalfBytes, (2 * (i - kP) + wm) * 16, at);
+            if constexpr (kFp8)
+                as[i - kP] =
+                    *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
+        }
+        p.issue_first(ring);
+        if (wm) wait_loads<S::kLoads>();
+        end_slot();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = kP; i < kMT; ++i)
+            multiply<kFp8, S::kGated>(acc[i], b, a[i - kP], as[i - kP], bs);
+        __builtin_amdgcn_s_setprio(0);
+        if (!wm) wait_loads<S::kLoads>();
+        end_slot();
     }
+    if (!wm) end_slot();
 }
 
 template <GemmOp kOp, bool kFp8>
@@ -694,6 +842,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave >> 2, wn = wave & 3;
+    const LanePlace at(lane);
     TileMap map;
     map.init(g, !S::kOverRows, S::kNTile);
     // block b runs on die b % 8: its tiles are neighbours of that die's other blocks' tiles
@@ -701,22 +850,36 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
     const int64_t first = gridDim.x % 8 == 0
                               ? static_cast<int64_t>(blockIdx.x % 8) * per_die + blockIdx.x / 8
                               : blockIdx.x;
-    Producer<kOp, kFp8> p(g, map, first, gridDim.x);
-    int slot = 0;
-    p.issue(lds_address(lds));
-    for (int64_t index = first; index < map.total; index += gridDim.x) {
-        const Tile t = map.find(index, S::kNTile);
-        const int steps = ((S::kOverRows ? t.rows : g.K) + S::kStepK - 1) / S::kStepK;
+    const int tiles =
+        first < map.total ? static_cast<int>((map.total - first + gridDim.x - 1) / gridDim.x) : 0;
+    TileRing ring;
+    auto look_up = [&](int n) {
+        if (n < tiles) ring.put(n, map.find(first + static_cast<int64_t>(n) * gridDim.x, S::kNTile));
+    };
+    look_up(0);
+    look_up(1);
+    look_up(2);
+    Producer<kOp, kFp8> p(g, lds_address(lds), tiles, ring);
+    int count = 0;
+    p.issue_first(ring);
+    p.issue_second();
+    p.issue_first(ring);
+    wait_loads<S::kLoads>();
+    end_slot();
+    for (int n = 0; n < tiles; ++n) {
+        look_up(n + 3);
+        const Tile t = ring.get(n);
+        const int steps = tile_steps<kOp, kFp8>(g, t);
         f32x4 acc[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const int mt = (t.height + 31) / 32;
-        switch (mt) {
-#define EP_GEMM_CASE(n)                                                                    \
-    case n:                                                                                \
-        gemm_tile<kOp, kFp8, n>(g, t, steps, p, acc, lds, slot, wm, wn, lane);             \
+        switch (max(mt, 1)) {  // a piece of a low tile may have got no row
+#define EP_GEMM_CASE(n)                                                                   \
+    case n:                                                                               \
+        gemm_tile<kOp, kFp8, n>(g, t, steps, p, acc, lds, count, ring, wm, wn, at, lane); \
         break;
             EP_GEMM_CASE(1)
             EP_GEMM_CASE(2)
@@ -728,9 +891,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
             EP_GEMM_CASE(8)
 #undef EP_GEMM_CASE
         }
-        gemm_store<kOp, kFp8>(g, t, acc, lds + S::kStages * S::kStageBytes, mt, wm, wn, lane);
+        gemm_store<kOp, kFp8>(g, t, acc, lds + S::kAmaxAt, mt, wm, wn, lane);
     }
-    wait_loads<0>();  // no load of the last step's outlives the block
+    wait_loads<0>();  // no load outlives the block
 }
 
 template <GemmOp kOp, bool kFp8>
