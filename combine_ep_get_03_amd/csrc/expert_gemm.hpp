@@ -27,6 +27,8 @@ constexpr int kOperandBytes = 256 * kStepBytes;  // one operand of one step in L
 constexpr int kHalfBytes = kOperandBytes / 2;
 constexpr int kScaleBytes = 2048;   // one step's row scales in LDS (the second half unused)
 constexpr int kScaleSlots = 4;
+constexpr int kTableExperts = 1024; // with at most so many experts, their offsets are kept in LDS
+constexpr int kTableBytes = (kTableExperts + 32) * 4;
 constexpr int kAmaxBytes = kTileM * 2 * 4 * 4;  // [row][gate, up][wave along n] magnitudes
 constexpr uint32_t kOutOfBuffer = 0x80000000u;  // an offset past every buffer made here
 
@@ -141,10 +143,21 @@ struct TileMap {
     int cut;
     bool by_rows;  // m tiles cover an expert's rows; else M channels, mt of them per expert
     int M, mt;
+    const int* table;  // the clamped offsets in LDS
 
     __device__ __forceinline__ int tiles(int c) const { return (c + kTileM - 1) / kTileM; }
 
-    __device__ __forceinline__ void init(const GemmArgs& g, bool rows, int n_tile) {
+    __device__ __forceinline__ int start(int e) const {
+        return E <= kTableExperts ? table[e]
+                                  : static_cast<int>(min<int64_t>(offset[e], num_rows));
+    }
+
+    // Ends with a barrier.
+    __device__ __forceinline__ void init(const GemmArgs& g, bool rows, int n_tile, int* lds_table) {
+        if (g.E <= kTableExperts)
+            for (int e = threadIdx.x; e <= g.E; e += kGemmThreads)
+                lds_table[e] = static_cast<int>(min<int64_t>(g.offset[e], g.num_rows));
+        table = lds_table;
         offset = g.offset;
         num_rows = g.num_rows;
         E = g.E;
@@ -182,6 +195,7 @@ struct TileMap {
         total = whole + static_cast<int64_t>(rest) * cut;
         if ((bad || over) && blockIdx.x == 0 && threadIdx.x == 0)
             raise_error(g.error_flag, kErrSlotRange);
+        lds_barrier();
     }
 
     __device__ __forceinline__ void place(Tile& t, int in_expert, int mts, int n_tile) const {
@@ -217,12 +231,12 @@ struct TileMap {
             const int lane = 63 - __builtin_clzll(le);
             int base = __builtin_amdgcn_readlane(first, lane);
             int e = lane * chunk;
-            int64_t a = min<int64_t>(offset[e], num_rows);
+            int a = start(e);
             for (;;) {
-                const int64_t b = min<int64_t>(offset[e + 1], num_rows);
-                mts = tiles(static_cast<int>(b - a));
+                const int b = start(e + 1);
+                mts = tiles(b - a);
                 if (index < static_cast<int64_t>(base + mts) * nt) {
-                    t.rows = static_cast<int>(b - a);
+                    t.rows = b - a;
                     break;
                 }
                 base += mts;
@@ -230,7 +244,7 @@ struct TileMap {
                 ++e;
             }
             t.expert = e;
-            t.row0 = static_cast<int>(a);
+            t.row0 = a;
             in_expert = static_cast<int>(index - static_cast<int64_t>(base) * nt);
             place(t, in_expert, mts, n_tile);
             const int each = ((t.rows + mts - 1) / mts + 15) & ~15;
@@ -240,8 +254,8 @@ struct TileMap {
             const int per = mt * nt;
             t.expert = static_cast<int>(index / per);
             in_expert = static_cast<int>(index - static_cast<int64_t>(t.expert) * per);
-            t.row0 = static_cast<int>(min<int64_t>(offset[t.expert], num_rows));
-            t.rows = static_cast<int>(min<int64_t>(offset[t.expert + 1], num_rows)) - t.row0;
+            t.row0 = start(t.expert);
+            t.rows = start(t.expert + 1) - t.row0;
             place(t, in_expert, mt, n_tile);
             t.m0 *= kTileM;
             t.height = min(kTileM, M - t.m0);
@@ -315,7 +329,8 @@ struct GemmShape {
     static constexpr int kLoads = 8 + (kFp8 ? 1 : 0);      // per wave and step
     static constexpr int kScalesAt = kStages * kStageBytes;
     static constexpr int kAmaxAt = kScalesAt + (kFp8 ? kScaleSlots * kScaleBytes : 0);
-    static constexpr int kLdsBytes = kAmaxAt + (kGated ? kAmaxBytes : 0);
+    static constexpr int kTableAt = kAmaxAt + (kGated ? kAmaxBytes : 0);
+    static constexpr int kLdsBytes = kTableAt + kTableBytes;
     static_assert(kLdsBytes <= 160 * 1024, "LDS of one CU");
 };
 
@@ -463,31 +478,6 @@ struct Producer {
     }
 };
 
-__device__ __forceinline__ float silu_sigmoid(float g) {
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
-}
-
-__device__ __forceinline__ u32x2 bf16_four(const float (&v)[4]) {
-    u32x2 w;
-    w[0] = bf16_pair(v[0], v[1]);
-    w[1] = bf16_pair(v[2], v[3]);
-    return w;
-}
-
-__device__ __forceinline__ uint32_t e4m3_four(const float (&v)[4], float inv) {
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-    return static_cast<uint32_t>(
-        __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true));
-}
-
-constexpr float kE4m3Largest = 448.0f;
-constexpr float kSmallestAmax = 0x1p-100f;
-
-// What a group whose largest magnitude is a is scaled to 448 by.
-__device__ __forceinline__ float group_amax(float a) {
-    return a > 0.0f ? fmaxf(a, kSmallestAmax) : kE4m3Largest;
-}
-
 // Fragments of one wave: lane l holds row (column) l % 16 of a subtile and the words of k that
 // belong to l / 16: words l / 16 and 4 + l / 16 of the step's eight (any order of k will do as
 // long as both operands have it).
@@ -578,181 +568,276 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[4], const Fragment (&b)[4]
     }
 }
 
-// What a tile's sums become in memory. Lane: row (2 i + wm) 16 + l % 16 of the tile, channels
-// 4 (l / 16) .. + 3 of each subtile j.
-template <GemmOp kOp, bool kFp8>
+// Two subtiles' sums of one row as eight consecutive channels per lane: lanes 0..31 take the
+// first subtile's 16 channels, lanes 32..63 the second's.
+__device__ __forceinline__ void eight_channels(const f32x4& a, const f32x4& b, float (&v)[8]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        // rows of 16 lanes: a = {a0 a1 b0 b1}, b = {a2 a3 b2 b3}, then {a0 a2 b0 b2}, {a1 a3 b1 b3}
+        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[r]),
+                                                        __float_as_uint(b[r]), false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+        v[r] = __uint_as_float(y[0]);
+        v[4 + r] = __uint_as_float(y[1]);
+    }
+}
+
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t buf, uint32_t at, u32x4 w) {
+    __builtin_amdgcn_raw_buffer_store_b128(w, buf, at, 0, 0);
+}
+
+__device__ __forceinline__ u32x2 e4m3_eight(const float (&v)[8], float inv) {
+    u32x2 w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int lo =
+            __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
+        w[h] = static_cast<uint32_t>(
+            __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, lo, true));
+    }
+    return w;
+}
+
+__device__ __forceinline__ void values_eight(u32x2 w, float scale, float (&v)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = static_cast<int>(w[h]);
+        v[4 * h] = __builtin_amdgcn_cvt_f32_fp8(c, 0) * scale;
+        v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(c, 1) * scale;
+        v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(c, 2) * scale;
+        v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(c, 3) * scale;
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float g) {
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+}
+
+constexpr float kE4m3Largest = 448.0f;
+constexpr float kSmallestAmax = 0x1p-100f;
+
+// What a group whose largest magnitude is a is scaled to 448 by.
+__device__ __forceinline__ float group_amax(float a) {
+    return a > 0.0f ? fmaxf(a, kSmallestAmax) : kE4m3Largest;
+}
+
+// What a tile's sums become in memory. Lane: row (2 i + wm) 16 + l % 16 of the tile, eight
+// channels of each pair of subtiles. The tile's rows of an array are a buffer, so that rows past
+// its height are dropped (or read as zeros) without a branch, and every tile of mt pairs of
+// subtiles makes the same number of stores.
+template <GemmOp kOp, bool kFp8, int kMT>
 __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32x4 (&acc)[8][4],
-                                           char* lds_amax, int mt, int wm, int wn, int lane) {
+                                           char* lds_amax, int wm, int wn, int lane) {
     const int quad = lane >> 4;
     const int64_t first_row = static_cast<int64_t>(t.row0) + t.m0;
+    const uint32_t height = t.height;
+    // the tile's rows of an array of `bytes` per row; none of it where the array is missing
+    auto rows_of = [&](const void* base, uint32_t bytes) {
+        const char* p = static_cast<const char*>(base) + (base ? first_row * bytes : 0);
+        return raw_buffer(p, base ? height * bytes : 0);
+    };
+    const int in_pair = (quad >> 1) * 16 + (quad & 1) * 8;
     if constexpr (kOp == GemmOp::kGateUp) {
         const int I = g.N;
         float(*amax)[2][4] = reinterpret_cast<float(*)[2][4]>(lds_amax);
         const bool quantise = g.codes != nullptr;
-        if (quantise) {
+        if constexpr (kFp8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i >= mt) continue;
-                float top[2] = {0.0f, 0.0f};
+            for (int i = 0; i < kMT; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        if constexpr (kFp8) {
-                            const float gate = acc[i][j][r];
-                            acc[i][j][r] = gate * silu_sigmoid(gate) * acc[i][j + 2][r];
-                            top[0] = fmaxf(top[0], fabsf(acc[i][j][r]));
-                        } else {
-                            top[0] = fmaxf(top[0], fabsf(acc[i][j][r]));
-                            top[1] = fmaxf(top[1], fabsf(acc[i][j + 2][r]));
-                        }
+                        const float gate = acc[i][j][r];
+                        acc[i][j][r] = gate * sigmoid(gate) * acc[i][j + 2][r];
                     }
+        }
+        if (quantise) {
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
 #pragma unroll
                 for (int h = 0; h < (kFp8 ? 1 : 2); ++h) {
-                    top[h] = fmaxf(top[h], __shfl_xor(top[h], 16));
-                    top[h] = fmaxf(top[h], __shfl_xor(top[h], 32));
-                    if (quad == 0) amax[(2 * i + wm) * 16 + (lane & 15)][h][wn] = top[h];
+                    float top = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        top = fmaxf(top, fmaxf(fabsf(acc[i][2 * h][r]), fabsf(acc[i][2 * h + 1][r])));
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    if (quad == 0) amax[(2 * i + wm) * 16 + (lane & 15)][h][wn] = top;
                 }
-            }
             lds_barrier();
         }
+        const int c = t.n0 + wn * 32 + in_pair;
+        const bool in = c < I;
+        const auto act_rows = rows_of(g.out, I * 2u);
+        const auto kept_rows = rows_of(g.gate_up, I * 4u);
+        const auto code_rows = rows_of(g.codes, I * (kFp8 ? 1u : 2u));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int m = (2 * i + wm) * 16 + (lane & 15);
-            if (i >= mt || m >= t.height) continue;
-            const int64_t row = first_row + m;
-            float inv[2], top[2];
+        for (int i = 0; i < kMT; ++i) {
+            const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
+            float gate[8], up[8];
+            eight_channels(acc[i][0], acc[i][1], gate);
+            if constexpr (!kFp8) eight_channels(acc[i][2], acc[i][3], up);
             if (quantise) {
+                float inv[2];
 #pragma unroll
                 for (int h = 0; h < (kFp8 ? 1 : 2); ++h) {
                     const float* p = amax[m][h];
-                    top[h] = group_amax(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])));
-                    inv[h] = kE4m3Largest / top[h];
+                    const float top = group_amax(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])));
+                    inv[h] = kE4m3Largest / top;
+                    if (wn == 0 && quad == 0 && m < height)
+                        g.scales[(first_row + m) * (I / (kFp8 ? 128 : 64)) + h * (I / 128) +
+                                 t.n0 / 128] = top / kE4m3Largest;
                 }
-                if (wn == 0 && quad == 0) {
-                    if constexpr (kFp8) {
-                        g.scales[row * (I / 128) + t.n0 / 128] = top[0] / kE4m3Largest;
-                    } else {
-                        float* s = g.scales + row * (I / 64) + t.n0 / 128;
-                        s[0] = top[0] / kE4m3Largest;
-                        s[I / 128] = top[1] / kE4m3Largest;
+                const uint32_t at = in ? m * (I * (kFp8 ? 1u : 2u)) + c : kOutOfBuffer;
+                __builtin_amdgcn_raw_buffer_store_b64(e4m3_eight(gate, inv[0]), code_rows, at, 0, 0);
+                if constexpr (!kFp8)
+                    __builtin_amdgcn_raw_buffer_store_b64(e4m3_eight(up, inv[1]), code_rows, at, I, 0);
+            }
+            if constexpr (!kFp8) {
+                if (g.gate_up) {
+                    const uint32_t at = in ? m * (I * 4u) + c * 2u : kOutOfBuffer;
+                    store16(kept_rows, at, narrow8(gate));
+                    store16(kept_rows, in ? at + I * 2u : at, narrow8(up));
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) gate[r] = gate[r] * sigmoid(gate[r]) * up[r];
+                store16(act_rows, in ? m * (I * 2u) + c * 2u : kOutOfBuffer, narrow8(gate));
+            }
+        }
+    } else if constexpr (kOp == GemmOp::kWeightGrad) {
+        const uint32_t row_bytes = g.N * (g.out_fp32 ? 4u : 2u);
+        const int64_t first = static_cast<int64_t>(t.expert) * g.M + t.m0;
+        const auto rows = raw_buffer(static_cast<char*>(g.out) + first * row_bytes, height * row_bytes);
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+            const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t c = t.n0 + wn * 64 + p * 32 + in_pair;
+                const bool in = c < static_cast<uint32_t>(g.N);
+                float v[8];
+                eight_channels(acc[i][2 * p], acc[i][2 * p + 1], v);
+                if (g.out_fp32) {
+                    const uint32_t at = in ? m * row_bytes + c * 4u : kOutOfBuffer;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f32x4 w = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+                        const uint32_t to = in ? at + 16 * h : at;
+                        if (g.accumulate)
+                            w += __builtin_bit_cast(
+                                f32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, to, 0, 0));
+                        store16(rows, to, __builtin_bit_cast(u32x4, w));
                     }
+                } else {
+                    const uint32_t at = in ? m * row_bytes + c * 2u : kOutOfBuffer;
+                    if (g.accumulate) {
+                        float w[8];
+                        widen8(__builtin_bit_cast(
+                                   u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, at, 0, 0)),
+                               w);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) v[r] += w[r];
+                    }
+                    store16(rows, at, narrow8(v));
                 }
             }
+        }
+    } else if constexpr (kOp == GemmOp::kDownGrad) {
+        const int I = g.N;
+        const auto kept = rows_of(g.gate_up, I * 4u);
+        const auto codes = rows_of(g.codes, I * 2u);
+        const auto scales = rows_of(g.scales, (I / 64) * 4u);
+        const auto grad = rows_of(g.out, I * 4u);
+        const auto act = rows_of(g.act, I * 2u);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = t.n0 + wn * 32 + j * 16 + quad * 4;
-                if (c >= I) continue;
-                float gate[4], up[4], act[4];
+        for (int i = 0; i < kMT; ++i) {
+            const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    gate[r] = acc[i][j][r];
-                    up[r] = acc[i][j + 2][r];
-                }
-                if constexpr (kFp8) {
-                    *reinterpret_cast<uint32_t*>(g.codes + row * I + c) = e4m3_four(gate, inv[0]);
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t c = t.n0 + wn * 64 + p * 32 + in_pair;
+                const bool in = c < static_cast<uint32_t>(I);
+                const uint32_t at = in ? m * (I * 4u) + c * 2u : kOutOfBuffer;
+                float da[8], gate[8], up[8];
+                eight_channels(acc[i][2 * p], acc[i][2 * p + 1], da);
+                if (g.gate_up) {
+                    widen8(__builtin_bit_cast(
+                               u32x4, __builtin_amdgcn_raw_buffer_load_b128(kept, at, 0, 0)),
+                           gate);
+                    widen8(__builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                         kept, in ? at + I * 2u : at, 0, 0)),
+                           up);
                 } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) act[r] = gate[r] * silu_sigmoid(gate[r]) * up[r];
-                    uint16_t* o = static_cast<uint16_t*>(g.out) + row * I + c;
-                    *reinterpret_cast<u32x2*>(o) = bf16_four(act);
-                    if (g.gate_up) {
-                        uint16_t* s = static_cast<uint16_t*>(g.gate_up) + row * 2 * I + c;
-                        *reinterpret_cast<u32x2*>(s) = bf16_four(gate);
-                        *reinterpret_cast<u32x2*>(s + I) = bf16_four(up);
-                    }
-                    if (quantise) {
-                        uint8_t* s = g.codes + row * 2 * I + c;
-                        *reinterpret_cast<uint32_t*>(s) = e4m3_four(gate, inv[0]);
-                        *reinterpret_cast<uint32_t*>(s + I) = e4m3_four(up, inv[1]);
-                    }
+                    const uint32_t from = in ? m * (I * 2u) + c : kOutOfBuffer;
+                    const uint32_t sc = in ? m * ((I / 64) * 4u) + c / 128 * 4u : kOutOfBuffer;
+                    const u32x2 a = __builtin_bit_cast(
+                        u32x2, __builtin_amdgcn_raw_buffer_load_b64(codes, from, 0, 0));
+                    const u32x2 b = __builtin_bit_cast(
+                        u32x2, __builtin_amdgcn_raw_buffer_load_b64(codes, in ? from + I : from, 0, 0));
+                    const float sg =
+                        __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(scales, sc, 0, 0));
+                    const float su = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                        scales, in ? sc + I / 128 * 4u : sc, 0, 0));
+                    values_eight(a, sg, gate);
+                    values_eight(b, su, up);
                 }
+                float dg[8], du[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float s = sigmoid(gate[r]);
+                    const float silu = gate[r] * s;
+                    du[r] = da[r] * silu;
+                    dg[r] = da[r] * up[r] * s * (1.0f + gate[r] * (1.0f - s));
+                    up[r] *= silu;
+                }
+                store16(grad, at, narrow8(dg));
+                store16(grad, in ? at + I * 2u : at, narrow8(du));
+                if (g.act) store16(act, in ? m * (I * 2u) + c * 2u : kOutOfBuffer, narrow8(up));
             }
         }
     } else {
+        const auto rows = rows_of(g.out, g.N * 2u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int m = (2 * i + wm) * 16 + (lane & 15);
-            if (i >= mt || m >= t.height) continue;
+        for (int i = 0; i < kMT; ++i) {
+            const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = t.n0 + wn * 64 + j * 16 + quad * 4;
-                if (c >= g.N) continue;
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r];
-                if constexpr (kOp == GemmOp::kWeightGrad) {
-                    const int64_t at =
-                        (static_cast<int64_t>(t.expert) * g.M + t.m0 + m) * g.N + c;
-                    if (g.out_fp32) {
-                        f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
-                        f32x4 w = {v[0], v[1], v[2], v[3]};
-                        if (g.accumulate) w += *o;
-                        *o = w;
-                    } else {
-                        u32x2* o = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + at);
-                        if (g.accumulate) {
-                            const u32x2 w = *o;
-                            v[0] += bf16_lo(w[0]);
-                            v[1] += bf16_hi(w[0]);
-                            v[2] += bf16_lo(w[1]);
-                            v[3] += bf16_hi(w[1]);
-                        }
-                        *o = bf16_four(v);
-                    }
-                } else if constexpr (kOp == GemmOp::kDownGrad) {
-                    const int I = g.N;
-                    const int64_t row = first_row + m;
-                    float gate[4], up[4];
-                    if (g.gate_up) {
-                        const uint16_t* s =
-                            static_cast<const uint16_t*>(g.gate_up) + row * 2 * I + c;
-                        const u32x2 a = *reinterpret_cast<const u32x2*>(s);
-                        const u32x2 b = *reinterpret_cast<const u32x2*>(s + I);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            gate[2 * q] = bf16_lo(a[q]);
-                            gate[2 * q + 1] = bf16_hi(a[q]);
-                            up[2 * q] = bf16_lo(b[q]);
-                            up[2 * q + 1] = bf16_hi(b[q]);
-                        }
-                    } else {
-                        const uint8_t* s = g.codes + row * 2 * I + c;
-                        const int a = *reinterpret_cast<const int*>(s);
-                        const int b = *reinterpret_cast<const int*>(s + I);
-                        const float* sc = g.scales + row * (I / 64) + c / 128;
-                        const float sg = sc[0], su = sc[I / 128];
-                        gate[0] = __builtin_amdgcn_cvt_f32_fp8(a, 0) * sg;
-                        gate[1] = __builtin_amdgcn_cvt_f32_fp8(a, 1) * sg;
-                        gate[2] = __builtin_amdgcn_cvt_f32_fp8(a, 2) * sg;
-                        gate[3] = __builtin_amdgcn_cvt_f32_fp8(a, 3) * sg;
-                        up[0] = __builtin_amdgcn_cvt_f32_fp8(b, 0) * su;
-                        up[1] = __builtin_amdgcn_cvt_f32_fp8(b, 1) * su;
-                        up[2] = __builtin_amdgcn_cvt_f32_fp8(b, 2) * su;
-                        up[3] = __builtin_amdgcn_cvt_f32_fp8(b, 3) * su;
-                    }
-                    float dg[4], du[4], act[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float sig = silu_sigmoid(gate[r]);
-                        const float silu = gate[r] * sig;
-                        du[r] = v[r] * silu;
-                        dg[r] = v[r] * up[r] * sig * (1.0f + gate[r] * (1.0f - sig));
-                        act[r] = silu * up[r];
-                    }
-                    uint16_t* o = static_cast<uint16_t*>(g.out) + row * 2 * I + c;
-                    *reinterpret_cast<u32x2*>(o) = bf16_four(dg);
-                    *reinterpret_cast<u32x2*>(o + I) = bf16_four(du);
-                    if (g.act)
-                        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.act) + row * I + c) =
-                            bf16_four(act);
-                } else {
-                    uint16_t* o = static_cast<uint16_t*>(g.out) + (first_row + m) * g.N + c;
-                    *reinterpret_cast<u32x2*>(o) = bf16_four(v);
-                }
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t c = t.n0 + wn * 64 + p * 32 + in_pair;
+                float v[8];
+                eight_channels(acc[i][2 * p], acc[i][2 * p + 1], v);
+                store16(rows,
+                        c < static_cast<uint32_t>(g.N) ? m * (g.N * 2u) + c * 2u : kOutOfBuffer,
+                        narrow8(v));
             }
         }
     }
+}
+
+// How many stores gemm_store is sure to make after its last load.
+template <GemmOp kOp, bool kFp8>
+__device__ __forceinline__ int stores_after(const GemmArgs& g, int mt) {
+    if constexpr (kOp == GemmOp::kGateUp)
+        return mt * (kFp8 ? 1 : 1 + (g.gate_up ? 2 : 0) + (g.codes ? 2 : 0));
+    else if constexpr (kOp == GemmOp::kWeightGrad)
+        return g.accumulate ? 0 : mt * (g.out_fp32 ? 4 : 2);
+    else if constexpr (kOp == GemmOp::kDownGrad)
+        return 0;
+    else
+        return mt * 2;
+}
+
+// All but the last kOutstanding loads have arrived, where at least `stores` stores were made
+// after the loads that are waited for.
+template <int kOutstanding>
+__device__ __forceinline__ void wait_loads_before(int stores) {
+    if (stores >= 32)
+        wait_loads<kOutstanding + 32>();
+    else if (stores >= 16)
+        wait_loads<kOutstanding + 16>();
+    else if (stores >= 8)
+        wait_loads<kOutstanding + 8>();
+    else
+        wait_loads<kOutstanding>();
 }
 
 // Ends a slot: this wave's LDS reads are in registers, and every wave gets here.
@@ -774,8 +859,9 @@ __device__ __forceinline__ void end_slot() {
 template <GemmOp kOp, bool kFp8, int kMT>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& t, int steps,
                                           Producer<kOp, kFp8>& p, f32x4 (&acc)[8][4],
-                                          const char* lds, int& count, const TileRing& ring, int wm,
-                                          int wn, const LanePlace& at, int lane) {
+                                          char* lds, int& count, int& stores,
+                                          const TileRing& ring, int wm, int wn,
+                                          const LanePlace& at, int lane) {
     using S = GemmShape<kOp, kFp8>;
     constexpr int kP = first_phase(kMT);
     const float* bs_row = nullptr;
@@ -806,13 +892,13 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& t, int 
             if constexpr (S::kGated) bs[1] = bs_row[up_scales + step];
         }
         p.issue_second();
-        if (wm) wait_loads<S::kLoads>();
+        if (wm) wait_loads_before<S::kLoads>(stores);
         end_slot();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < kP; ++i) multiply<kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
         __builtin_amdgcn_s_setprio(0);
-        if (!wm) wait_loads<S::kLoads>();
+        if (!wm) wait_loads_before<S::kLoads>(stores);
         end_slot();
 #pragma unroll
         for (int i = kP; i < kMT; ++i) {
@@ -822,17 +908,20 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& t, int 
                     *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
         }
         p.issue_first(ring);
-        if (wm) wait_loads<S::kLoads>();
+        if (wm) wait_loads_before<S::kLoads>(stores);
         end_slot();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = kP; i < kMT; ++i)
             multiply<kFp8, S::kGated>(acc[i], b, a[i - kP], as[i - kP], bs);
         __builtin_amdgcn_s_setprio(0);
-        if (!wm) wait_loads<S::kLoads>();
+        if (!wm) wait_loads_before<S::kLoads>(stores);
+        stores = 0;
         end_slot();
     }
     if (!wm) end_slot();
+    gemm_store<kOp, kFp8, kMT>(g, t, acc, lds + S::kAmaxAt, wm, wn, lane);
+    stores = stores_after<kOp, kFp8>(g, kMT);
 }
 
 template <GemmOp kOp, bool kFp8>
@@ -844,7 +933,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
     const int wm = wave >> 2, wn = wave & 3;
     const LanePlace at(lane);
     TileMap map;
-    map.init(g, !S::kOverRows, S::kNTile);
+    map.init(g, !S::kOverRows, S::kNTile, reinterpret_cast<int*>(lds + S::kTableAt));
     // block b runs on die b % 8: its tiles are neighbours of that die's other blocks' tiles
     const int per_die = gridDim.x / 8;
     const int64_t first = gridDim.x % 8 == 0
@@ -860,7 +949,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
     look_up(1);
     look_up(2);
     Producer<kOp, kFp8> p(g, lds_address(lds), tiles, ring);
-    int count = 0;
+    int count = 0, stores = 0;
     p.issue_first(ring);
     p.issue_second();
     p.issue_first(ring);
@@ -879,7 +968,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
         switch (max(mt, 1)) {  // a piece of a low tile may have got no row
 #define EP_GEMM_CASE(n)                                                                   \
     case n:                                                                               \
-        gemm_tile<kOp, kFp8, n>(g, t, steps, p, acc, lds, count, ring, wm, wn, at, lane); \
+        gemm_tile<kOp, kFp8, n>(g, t, steps, p, acc, lds, count, stores, ring, wm, wn, at, lane); \
         break;
             EP_GEMM_CASE(1)
             EP_GEMM_CASE(2)
@@ -891,7 +980,6 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
             EP_GEMM_CASE(8)
 #undef EP_GEMM_CASE
         }
-        gemm_store<kOp, kFp8>(g, t, acc, lds + S::kAmaxAt, mt, wm, wn, lane);
     }
     wait_loads<0>();  // no load outlives the block
 }
