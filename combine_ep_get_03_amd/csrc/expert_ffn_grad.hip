@@ -16,7 +16,11 @@ hipError_t launch_expert_gate_up_grad(const GemmArgs& g, hipStream_t stream) {
 }
 
 hipError_t launch_expert_weight_grad(const GemmArgs& g, hipStream_t stream) {
-    return launch_gemm<GemmOp::kWeightGrad, false>(g, stream);
+#ifdef EP_WG256
+    return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 256>>(g, stream);
+#else
+    return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 128>>(g, stream);
+#endif
 }
 
 }  // namespace ep

@@ -18,18 +18,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kTileM = 256;         // rows (m side) of a tile
-constexpr int kTileN = 256;         // channels (n side) of a tile
-constexpr int kGemmThreads = 512;   // 8 waves, 2 along m and 4 along n
-constexpr int kGemmWaves = kGemmThreads / kWave;
+constexpr int kBlocks = 256;        // one per CU
 constexpr int kStepBytes = 128;     // bytes of k per row and step: 64 bf16 or 128 e4m3
-constexpr int kOperandBytes = 256 * kStepBytes;  // one operand of one step in LDS
-constexpr int kHalfBytes = kOperandBytes / 2;
-constexpr int kScaleBytes = 2048;   // one step's row scales in LDS (the second half unused)
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 4;      // steps whose row scales are in LDS
 constexpr int kTableExperts = 1024; // with at most so many experts, their offsets are kept in LDS
 constexpr int kTableBytes = (kTableExperts + 32) * 4;
-constexpr int kAmaxBytes = kTileM * 2 * 4 * 4;  // [row][gate, up][wave along n] magnitudes
 constexpr uint32_t kOutOfBuffer = 0x80000000u;  // an offset past every buffer made here
 
 enum class GemmOp {
@@ -96,7 +89,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // The tiles of all experts in one order: expert after expert, and within one in bands of at most
 // kBandM tiles along m (of about equal numbers) with n outside, so that the 32 blocks of one die
 // take about six parts of A and five to eight of B between them and share both in its L2.
-// An expert of c rows has ceil(c / kTileM) tiles along m of about equal heights. Every lane
+// An expert of c rows has ceil(c / tile_m) tiles along m of about equal heights. Every lane
 // holds the number of such tiles before its chunk of experts; a tile is found by a ballot and a
 // walk through one chunk. Offsets are taken as non-negative and ascending, and clamped to
 // num_rows; where they are not, nothing is computed.
@@ -113,12 +106,13 @@ struct Tile {
     int height;  // valid rows (channels) of the m side in this tile
 };
 
-// A block's next four tiles, in the lanes of one register: the loads run up to two tiles ahead of
-// the products, and looking a tile up takes more registers than the products leave.
+// A block's next eight tiles, in the lanes of one register: the loads run up to kStages steps, of
+// as many tiles, ahead of the products, and looking a tile up takes more registers than the
+// products leave.
 struct TileRing {
     int lanes = 0;
     __device__ __forceinline__ void put(int n, const Tile& t) {
-        const int at = (n & 3) * 8;
+        const int at = (n & 7) * 8;
         const int field[6] = {t.expert, t.m0, t.n0, t.row0, t.rows, t.height};
 #pragma unroll
         for (int i = 0; i < 6; ++i) {
@@ -127,7 +121,7 @@ struct TileRing {
         }
     }
     __device__ __forceinline__ Tile get(int n) const {
-        const int at = (n & 3) * 8;
+        const int at = (n & 7) * 8;
         int field[6];
 #pragma unroll
         for (int i = 0; i < 6; ++i) field[i] = __builtin_amdgcn_readlane(lanes, at + i);
@@ -145,7 +139,9 @@ struct TileMap {
     int M, mt;
     const int* table;  // the clamped offsets in LDS
 
-    __device__ __forceinline__ int tiles(int c) const { return (c + kTileM - 1) / kTileM; }
+    int tile_m;
+
+    __device__ __forceinline__ int tiles(int c) const { return (c + tile_m - 1) / tile_m; }
 
     __device__ __forceinline__ int start(int e) const {
         return E <= kTableExperts ? table[e]
@@ -153,9 +149,11 @@ struct TileMap {
     }
 
     // Ends with a barrier.
-    __device__ __forceinline__ void init(const GemmArgs& g, bool rows, int n_tile, int* lds_table) {
+    __device__ __forceinline__ void init(const GemmArgs& g, bool rows, int m_tile, int n_tile,
+                                         int* lds_table) {
+        tile_m = m_tile;
         if (g.E <= kTableExperts)
-            for (int e = threadIdx.x; e <= g.E; e += kGemmThreads)
+            for (int e = threadIdx.x; e <= g.E; e += static_cast<int>(blockDim.x))
                 lds_table[e] = static_cast<int>(min<int64_t>(g.offset[e], g.num_rows));
         table = lds_table;
         offset = g.offset;
@@ -257,66 +255,25 @@ struct TileMap {
             t.row0 = start(t.expert);
             t.rows = start(t.expert + 1) - t.row0;
             place(t, in_expert, mt, n_tile);
-            t.m0 *= kTileM;
-            t.height = min(kTileM, M - t.m0);
+            t.m0 *= tile_m;
+            t.height = min(tile_m, M - t.m0);
         }
         take(t, piece, pieces);
         return t;
     }
 };
 
-// ---------------------------------------------------------------- one operand's loads
-// An operand's step is two halves of 16 KB. By rows: 128 bytes of each of 128 rows, row after row
-// in LDS, with a row's 16-byte word c at place c ^ (row & 7): eight lanes of a fragment's read,
-// on eight rows, then hit eight different places. By columns: 64 rows of k of 128 channels (256
-// bytes each), with the 32-byte pair of words p at place p ^ turn(k), so that a transposing
-// read's four rows (of each of two groups of lanes) lie in different banks. Of the m side the
-// first half holds the subtiles that the first phase of a step reads (32 `split` rows of the
-// tile), the second half the rest.
-__device__ __forceinline__ int turn(int k) { return (k & 3) | ((k >> 1) & 4); }
-
-template <bool kByRows>
-struct OperandLoads {
-    uint32_t voff[4];  // of a wave's two loads of the first half, and of the second
-
-    // rows: valid rows of the tile; the second half's first is row `split`
-    __device__ __forceinline__ void init_rows(int wave, int lane, int rows, int split,
-                                              uint32_t stride) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int r = ((t & 1) * kGemmWaves + wave) * 8 + lane / 8;
-            const int row = t < 2 ? r : r + split;
-            const bool in = row < rows && (t >= 2 || r < split);
-            voff[t] = in ? row * stride + (((lane & 7) ^ (lane >> 3)) * 16) : kOutOfBuffer;
-        }
-    }
-    // columns: valid columns from col0
-    __device__ __forceinline__ void init_columns(int wave, int lane, int col0, int columns,
-                                                 int split, uint32_t stride) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int k = ((t & 1) * kGemmWaves + wave) * 4 + lane / 16;
-            const int c = ((lane & 15) ^ (2 * turn(k))) * 8;
-            const int col = t < 2 ? c : c + split;
-            const bool in = col < columns && (t >= 2 || c < split);
-            voff[t] = in ? k * stride + (col0 + col) * 2 : kOutOfBuffer;
-        }
-    }
-    // by rows, last step: words past the row's end read zeros
-    __device__ __forceinline__ void cut(int lane, int words) {
-        if (((lane & 7) ^ (lane >> 3)) >= words) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) voff[t] = kOutOfBuffer;
-        }
-    }
-};
-
-// A tile of mt pairs of subtiles is computed in two phases of about equal length.
-__device__ __forceinline__ constexpr int first_phase(int mt) { return (mt + 1) / 2; }
-
-// ---------------------------------------------------------------- the kernel
-template <GemmOp kOp, bool kFp8>
+// ---------------------------------------------------------------- the kernels' shapes
+// Tiles of 256 x 256 for many rows per expert: the matrix cores are what is short, and two steps
+// in LDS are what fits beside them (gemm_kernel). Lower ones for fewer rows, where the time is
+// that of the weights' way from memory: as many steps as fit are in LDS, and waves of their own
+// do nothing but load (stream_kernel). A wave multiplies 64 channels with every second subtile of
+// 16 rows.
+template <GemmOp kOp_, bool kFp8_, int kTileM_, int kTileN_ = 256>
 struct GemmShape {
+    static constexpr GemmOp kOp = kOp_;
+    static constexpr bool kFp8 = kFp8_;
+    static constexpr int kTileM = kTileM_, kTileN = kTileN_;
     static constexpr bool kGated = kOp == GemmOp::kGateUp;
     static constexpr bool kAByRows = kOp != GemmOp::kWeightGrad;
     static constexpr bool kBByRows = kOp == GemmOp::kGateUp || kOp == GemmOp::kDown;
@@ -324,47 +281,123 @@ struct GemmShape {
     static constexpr int kNTile = kGated ? kTileN / 2 : kTileN;    // output channels of a tile
     static constexpr int kElem = kFp8 ? 1 : 2;
     static constexpr int kStepK = kStepBytes / kElem;
-    static constexpr int kStages = 2;
-    static constexpr int kStageBytes = 2 * kOperandBytes;  // the m side, then the n side
-    static constexpr int kLoads = 8 + (kFp8 ? 1 : 0);      // per wave and step
+    static constexpr int kMT = kTileM / 32;  // pairs of subtiles along m
+    static constexpr int kNWaves = kTileN / 64;
+    static constexpr int kWaves = 2 * kNWaves;              // waves that multiply
+    static constexpr int kLoaders = kTileM == 256 ? 0 : 4;  // waves that load
+    static constexpr int kThreads = (kWaves + kLoaders) * kWave;
+    static constexpr int kMBytes = kTileM * kStepBytes;
+    static constexpr int kStageBytes = kMBytes + kTileN * kStepBytes;  // the m side, the n side
+    static constexpr int kScaleBytes = (kTileM < 64 ? 64 : kTileM) * 4;
+    static constexpr int kAmaxBytes = kTileM * 2 * 4 * 4;  // [row][gate, up][wave along n]
+    static constexpr int kBesides = (kFp8 ? kScaleSlots * kScaleBytes : 0) +
+                                    (kGated ? kAmaxBytes : 0) + kTableBytes;
+    static constexpr int kFit = (160 * 1024 - kBesides) / kStageBytes;
+    static constexpr int kStages = kFit < 4 || !kFp8 ? (kFit < 8 ? kFit : 8) : 4;
     static constexpr int kScalesAt = kStages * kStageBytes;
     static constexpr int kAmaxAt = kScalesAt + (kFp8 ? kScaleSlots * kScaleBytes : 0);
     static constexpr int kTableAt = kAmaxAt + (kGated ? kAmaxBytes : 0);
     static constexpr int kLdsBytes = kTableAt + kTableBytes;
     static_assert(kLdsBytes <= 160 * 1024, "LDS of one CU");
+    static_assert(kStages >= 2 && (!kFp8 || kStages <= kScaleSlots), "a place for every step");
+    static_assert(kAByRows || kTileM >= 128, "an m side by columns has halves of 128");
+    static_assert(kBByRows || kTileN >= 128, "an n side by columns has halves of 128");
+    static_assert(kTileM < 256 || (kStages == 2 && kTileN == 256), "gemm_kernel");
 };
+
+// ---------------------------------------------------------------- one operand's loads
+// By rows: 128 bytes of each row of a step, row after row in LDS, with a row's 16-byte word c at
+// place c ^ (row & 7): eight lanes of a fragment's read, on eight rows, then hit eight different
+// places. By columns: halves of 64 rows of k of 128 channels (256 bytes each), with the 32-byte
+// pair of words p at place p ^ turn(k), so that a transposing read's four rows (of each of two
+// groups of lanes) lie in different banks. Of the m side the first half holds the subtiles that
+// the first phase of a step reads (32 `split` rows of the tile), the second half the rest.
+__device__ __forceinline__ int turn(int k) { return (k & 3) | ((k >> 1) & 4); }
+
+// A load of a wave is one unit of 1 KB: eight rows, or four rows of k of 128 columns. kUnits of them
+// are shared by kWaves waves.
+template <bool kByRows, int kUnits, int kWaves>
+struct OperandLoads {
+    static constexpr int kLoads = kUnits / kWaves;  // per wave
+    static_assert(kUnits % kWaves == 0, "the same number for every wave");
+    uint32_t voff[kLoads];
+
+    __device__ __forceinline__ static int unit(int t, int wave) { return t * kWaves + wave; }
+
+    // rows: valid rows of the tile, of which the first `split` are in the first 128 rows of LDS
+    // and the others behind them
+    __device__ __forceinline__ void init_rows(int wave, int lane, int rows, int split,
+                                              uint32_t stride) {
+#pragma unroll
+        for (int t = 0; t < kLoads; ++t) {
+            const int r = unit(t, wave) * 8 + lane / 8;
+            const bool second = r >= 128;
+            const int row = second ? r - 128 + split : r;
+            const bool in = row < rows && (second || r < split);
+            voff[t] = in ? row * stride + (((lane & 7) ^ (lane >> 3)) * 16) : kOutOfBuffer;
+        }
+    }
+    // columns: valid columns from col0, split alike
+    __device__ __forceinline__ void init_columns(int wave, int lane, int col0, int columns,
+                                                 int split, uint32_t stride) {
+#pragma unroll
+        for (int t = 0; t < kLoads; ++t) {
+            const bool second = unit(t, wave) >= 16;
+            const int k = (unit(t, wave) & 15) * 4 + lane / 16;
+            const int c = ((lane & 15) ^ (2 * turn(k))) * 8;
+            const int col = second ? c + split : c;
+            const bool in = col < columns && (second || c < split);
+            voff[t] = in ? k * stride + (col0 + col) * 2 : kOutOfBuffer;
+        }
+    }
+    // by rows, last step: words past the row's end read zeros
+    __device__ __forceinline__ void cut(int lane, int words) {
+        if (((lane & 7) ^ (lane >> 3)) >= words) {
+#pragma unroll
+            for (int t = 0; t < kLoads; ++t) voff[t] = kOutOfBuffer;
+        }
+    }
+};
+
+// How many of a tile's mt pairs of subtiles the first phase of a step takes.
+__device__ __forceinline__ constexpr int first_phase(int mt) { return (mt + 1) / 2; }
 
 // A tile without rows to sum over (an expert's weight gradient) or to compute still takes one step,
 // of zeros.
-template <GemmOp kOp, bool kFp8>
+template <class S>
 __device__ __forceinline__ int tile_steps(const GemmArgs& g, const Tile& t) {
-    using S = GemmShape<kOp, kFp8>;
     const int k = t.height > 0 ? (S::kOverRows ? t.rows : g.K) : 0;
     return max(1, (k + S::kStepK - 1) / S::kStepK);
 }
 
-// The stream of steps that a block loads: its tiles one after the other, the steps of each.
-template <GemmOp kOp, bool kFp8>
+// The stream of steps that a block loads: its tiles one after the other, the steps of each, by
+// kWaves waves.
+template <class S, int kWaves>
 struct Producer {
-    using S = GemmShape<kOp, kFp8>;
+    using ALoads = OperandLoads<S::kAByRows, S::kTileM / 8, kWaves>;
+    using BLoads = OperandLoads<S::kBByRows, S::kTileN / 8, kWaves>;
+    static constexpr int kLoads = ALoads::kLoads + BLoads::kLoads + (S::kFp8 ? 1 : 0);
+    static constexpr bool kTwoParts = S::kLoaders == 0;  // the m side is read in two halves
+
     const GemmArgs& g;
     const uint32_t lds;
     int wave, lane;
     int tile, tiles;  // the block's present one, and how many it has
     int step, steps;  // of the tile
-    int count;        // of all steps so far
+    int slot;         // the step's place in LDS
+    int scale_slot;   // its scales'
     bool live;
     Tile t;
-    OperandLoads<S::kAByRows> a;
-    OperandLoads<S::kBByRows> b;
+    ALoads a;
+    BLoads b;
     uint32_t scale_voff;
     const char *a_base = nullptr, *b_base = nullptr, *b_up = nullptr;
     uint32_t a_row, b_row;  // bytes between rows in memory
 
-    __device__ __forceinline__ Producer(const GemmArgs& g_, uint32_t lds_, int tiles_,
+    __device__ __forceinline__ Producer(const GemmArgs& g_, uint32_t lds_, int wave_, int tiles_,
                                         const TileRing& ring)
-        : g(g_), lds(lds_), wave(__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)),
-          lane(lane_id()), tile(0), tiles(tiles_), step(0), steps(0), count(0), live(false), t{} {
+        : g(g_), lds(lds_), wave(wave_), lane(lane_id()), tile(0), tiles(tiles_), step(0), steps(0),
+          slot(0), scale_slot(0), live(false), t{} {
         a_row = static_cast<uint32_t>(S::kOverRows ? g.M : g.K) * S::kElem;
         b_row = static_cast<uint32_t>(S::kBByRows ? g.K : g.N) * S::kElem;
         if (tile < tiles) start(ring);
@@ -373,8 +406,8 @@ struct Producer {
     __device__ __forceinline__ void start(const TileRing& ring) {
         t = ring.get(tile);
         step = 0;
-        steps = tile_steps<kOp, kFp8>(g, t);
-        const int split = 32 * first_phase((t.height + 31) / 32);
+        steps = tile_steps<S>(g, t);
+        const int split = kTwoParts ? 32 * first_phase((t.height + 31) / 32) : 128;
         const char* rows_a = static_cast<const char*>(g.a) + static_cast<int64_t>(t.row0) * a_row;
         if constexpr (S::kAByRows) {
             a_base = rows_a + static_cast<int64_t>(t.m0) * a_row;
@@ -386,32 +419,33 @@ struct Producer {
         const int nv = min(S::kNTile, g.N - t.n0);
         if constexpr (S::kOverRows) {
             b_base = static_cast<const char*>(g.b) + static_cast<int64_t>(t.row0) * b_row;
-            b.init_columns(wave, lane, t.n0, nv, kTileN / 2, b_row);
+            b.init_columns(wave, lane, t.n0, nv, 128, b_row);
         } else {
             const int64_t weights = static_cast<int64_t>(S::kGated ? 2 : 1) * g.N * g.K * S::kElem;
             b_base = static_cast<const char*>(g.b) + t.expert * weights;
             if constexpr (S::kBByRows) {
                 b_base += static_cast<int64_t>(t.n0) * b_row;
                 b_up = b_base + static_cast<int64_t>(g.N) * b_row;
-                b.init_rows(wave, lane, nv, kTileN / 2, b_row);
+                b.init_rows(wave, lane, nv, 128, b_row);
                 if constexpr (S::kGated) {  // the second half is the up projection's
+                    constexpr int kHalf = BLoads::kLoads / 2;
 #pragma unroll
-                    for (int i = 2; i < 4; ++i) b.voff[i] = b.voff[i - 2];
+                    for (int i = kHalf; i < 2 * kHalf; ++i) b.voff[i] = b.voff[i - kHalf];
                 }
             } else {
-                b.init_columns(wave, lane, t.n0, nv, kTileN / 2, b_row);
+                b.init_columns(wave, lane, t.n0, nv, 128, b_row);
             }
         }
-        if constexpr (kFp8) {  // waves 0..3 take 64 rows' scales each
-            const int row = wave * kWave + lane;
+        if constexpr (S::kFp8) {  // a wave takes 64 rows' scales, some waves the same ones
+            const int row = wave % (S::kScaleBytes / 256) * kWave + lane;
             scale_voff = row < t.height ? static_cast<uint32_t>(row) * (g.K / 128) * 4u
                                         : kOutOfBuffer;
         }
     }
 
-    // The loads of the m side's half h of the present step.
-    __device__ __forceinline__ void issue_a(int h) {
-        const uint32_t dst = lds + (count & 1) * S::kStageBytes + h * kHalfBytes + wave * 1024;
+    // The m side's loads from..to - 1 of the present step.
+    __device__ __forceinline__ void load_m(int from, int to) {
+        const uint32_t dst = lds + slot * S::kStageBytes;
         const int k0 = step * S::kStepK;
         i32x4 buf;
         uint32_t along = 0;
@@ -423,12 +457,14 @@ struct Producer {
             buf = scalar_buffer(a_base + static_cast<int64_t>(k0) * a_row, n * a_row);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            load_lds16(buf, dst + i * kGemmWaves * 1024, a.voff[2 * h + i], along);
+        for (int i = 0; i < ALoads::kLoads; ++i)
+            if (i >= from && i < to)
+                load_lds16(buf, dst + a.unit(i, wave) * 1024, a.voff[i], along);
     }
 
-    // The next step's n side, the first half of its m side and its scales. With no step left the
-    // loads go on, of buffers of no bytes, so that the counts of loads in flight hold.
+    // The next step's n side, the first half of its m side (all of it, where it is loaded in one
+    // part) and its scales. With no step left the loads go on, of buffers of no bytes, so that
+    // the counts of loads in flight hold.
     __device__ __forceinline__ void issue_first(const TileRing& ring) {
         if (step == steps && tile < tiles) {
             ++tile;
@@ -444,36 +480,47 @@ struct Producer {
                 if constexpr (S::kBByRows) b.cut(lane, words);
             }
         }
-        const uint32_t dst =
-            lds + (count & 1) * S::kStageBytes + kOperandBytes + wave * 1024;
+        const uint32_t dst = lds + slot * S::kStageBytes + S::kMBytes;
         if constexpr (S::kBByRows) {
             const uint32_t along = static_cast<uint32_t>(step) * kStepBytes;
             const uint32_t n = live ? static_cast<uint32_t>(min(S::kNTile, g.N - t.n0)) * b_row : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                load_lds16(scalar_buffer(S::kGated && i >= 2 ? b_up : b_base, n),
-                           dst + i * kGemmWaves * 1024, b.voff[i], along);
+            for (int i = 0; i < BLoads::kLoads; ++i)
+                load_lds16(scalar_buffer(S::kGated && i >= BLoads::kLoads / 2 ? b_up : b_base, n),
+                           dst + b.unit(i, wave) * 1024, b.voff[i], along);
         } else {
             const uint32_t n = live ? min(64, (S::kOverRows ? t.rows : g.K) - k0) : 0;
             const auto buf = scalar_buffer(b_base + static_cast<int64_t>(k0) * b_row, n * b_row);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                load_lds16(buf, dst + i * kGemmWaves * 1024, b.voff[i], 0);
+            for (int i = 0; i < BLoads::kLoads; ++i)
+                load_lds16(buf, dst + b.unit(i, wave) * 1024, b.voff[i], 0);
         }
-        issue_a(0);
-        if constexpr (kFp8) {
+        load_m(0, kTwoParts ? ALoads::kLoads / 2 : ALoads::kLoads);
+        if constexpr (S::kFp8) {
             const uint32_t row = static_cast<uint32_t>(g.K / 128) * 4u;
-            const auto buf = scalar_buffer(g.a_scales + (static_cast<int64_t>(t.row0) + t.m0) * (g.K / 128),
-                                           live ? static_cast<uint32_t>(t.height) * row : 0);
-            load_lds4(buf, lds + S::kScalesAt + (count & 3) * kScaleBytes + wave * 256, scale_voff,
-                      static_cast<uint32_t>(step) * 4u);
+            const auto buf =
+                scalar_buffer(g.a_scales + (static_cast<int64_t>(t.row0) + t.m0) * (g.K / 128),
+                              live ? static_cast<uint32_t>(t.height) * row : 0);
+            load_lds4(buf,
+                      lds + S::kScalesAt + scale_slot * S::kScaleBytes +
+                          wave % (S::kScaleBytes / 256) * 256,
+                      scale_voff, static_cast<uint32_t>(step) * 4u);
         }
+        if constexpr (!kTwoParts) next();
     }
 
     // The second half of the step's m side; on to the next step.
     __device__ __forceinline__ void issue_second() {
-        issue_a(1);
-        ++count;
+        load_m(ALoads::kLoads / 2, ALoads::kLoads);
+        next();
+    }
+
+    __device__ __forceinline__ void next() {
+        if constexpr (S::kStages == 2)
+            slot ^= 1;
+        else
+            slot = slot + 1 == S::kStages ? 0 : slot + 1;
+        scale_slot = (scale_slot + 1) & (kScaleSlots - 1);
         if (live) ++step;
     }
 };
@@ -523,18 +570,19 @@ __device__ __forceinline__ void read_fragment(Fragment& out, const char* half, i
     }
 }
 
-template <GemmOp kOp, bool kFp8>
+template <class S>
 __device__ __forceinline__ void read_n_side(Fragment (&b)[4], const char* operand, int wn,
                                             const LanePlace& at) {
-    using S = GemmShape<kOp, kFp8>;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if constexpr (S::kGated)  // gate's channels from the first half, up's from the second
-            read_fragment<S::kBByRows>(b[j], operand + (j >> 1) * kHalfBytes, wn * 32 + (j & 1) * 16,
-                                       at);
-        else
-            read_fragment<S::kBByRows>(b[j], operand + (wn >> 1) * kHalfBytes,
-                                       (wn & 1) * 64 + j * 16, at);
+            read_fragment<true>(b[j], operand,
+                                (j >> 1) * (S::kTileN / 2) + wn * 32 + (j & 1) * 16, at);
+        else if constexpr (S::kBByRows)
+            read_fragment<true>(b[j], operand, wn * 64 + j * 16, at);
+        else  // halves of 128 columns
+            read_fragment<false>(b[j], operand + (wn >> 1) * (128 * kStepBytes),
+                                 (wn & 1) * 64 + j * 16, at);
     }
 }
 
@@ -625,8 +673,8 @@ __device__ __forceinline__ float group_amax(float a) {
 // channels of each pair of subtiles. The tile's rows of an array are a buffer, so that rows past
 // its height are dropped (or read as zeros) without a branch, and every tile of mt pairs of
 // subtiles makes the same number of stores.
-template <GemmOp kOp, bool kFp8, int kMT>
-__device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32x4 (&acc)[8][4],
+template <class S, int kMT>
+__device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32x4 (&acc)[S::kMT][4],
                                            char* lds_amax, int wm, int wn, int lane) {
     const int quad = lane >> 4;
     const int64_t first_row = static_cast<int64_t>(t.row0) + t.m0;
@@ -637,11 +685,11 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
         return raw_buffer(p, base ? height * bytes : 0);
     };
     const int in_pair = (quad >> 1) * 16 + (quad & 1) * 8;
-    if constexpr (kOp == GemmOp::kGateUp) {
+    if constexpr (S::kOp == GemmOp::kGateUp) {
         const int I = g.N;
         float(*amax)[2][4] = reinterpret_cast<float(*)[2][4]>(lds_amax);
         const bool quantise = g.codes != nullptr;
-        if constexpr (kFp8) {
+        if constexpr (S::kFp8) {
 #pragma unroll
             for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -656,7 +704,7 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
 #pragma unroll
             for (int i = 0; i < kMT; ++i)
 #pragma unroll
-                for (int h = 0; h < (kFp8 ? 1 : 2); ++h) {
+                for (int h = 0; h < (S::kFp8 ? 1 : 2); ++h) {
                     float top = 0.0f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
@@ -671,30 +719,30 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
         const bool in = c < I;
         const auto act_rows = rows_of(g.out, I * 2u);
         const auto kept_rows = rows_of(g.gate_up, I * 4u);
-        const auto code_rows = rows_of(g.codes, I * (kFp8 ? 1u : 2u));
+        const auto code_rows = rows_of(g.codes, I * (S::kFp8 ? 1u : 2u));
 #pragma unroll
         for (int i = 0; i < kMT; ++i) {
             const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
             float gate[8], up[8];
             eight_channels(acc[i][0], acc[i][1], gate);
-            if constexpr (!kFp8) eight_channels(acc[i][2], acc[i][3], up);
+            if constexpr (!S::kFp8) eight_channels(acc[i][2], acc[i][3], up);
             if (quantise) {
                 float inv[2];
 #pragma unroll
-                for (int h = 0; h < (kFp8 ? 1 : 2); ++h) {
+                for (int h = 0; h < (S::kFp8 ? 1 : 2); ++h) {
                     const float* p = amax[m][h];
                     const float top = group_amax(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])));
                     inv[h] = kE4m3Largest / top;
                     if (wn == 0 && quad == 0 && m < height)
-                        g.scales[(first_row + m) * (I / (kFp8 ? 128 : 64)) + h * (I / 128) +
+                        g.scales[(first_row + m) * (I / (S::kFp8 ? 128 : 64)) + h * (I / 128) +
                                  t.n0 / 128] = top / kE4m3Largest;
                 }
-                const uint32_t at = in ? m * (I * (kFp8 ? 1u : 2u)) + c : kOutOfBuffer;
+                const uint32_t at = in ? m * (I * (S::kFp8 ? 1u : 2u)) + c : kOutOfBuffer;
                 __builtin_amdgcn_raw_buffer_store_b64(e4m3_eight(gate, inv[0]), code_rows, at, 0, 0);
-                if constexpr (!kFp8)
+                if constexpr (!S::kFp8)
                     __builtin_amdgcn_raw_buffer_store_b64(e4m3_eight(up, inv[1]), code_rows, at, I, 0);
             }
-            if constexpr (!kFp8) {
+            if constexpr (!S::kFp8) {
                 if (g.gate_up) {
                     const uint32_t at = in ? m * (I * 4u) + c * 2u : kOutOfBuffer;
                     store16(kept_rows, at, narrow8(gate));
@@ -705,7 +753,7 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
                 store16(act_rows, in ? m * (I * 2u) + c * 2u : kOutOfBuffer, narrow8(gate));
             }
         }
-    } else if constexpr (kOp == GemmOp::kWeightGrad) {
+    } else if constexpr (S::kOp == GemmOp::kWeightGrad) {
         const uint32_t row_bytes = g.N * (g.out_fp32 ? 4u : 2u);
         const int64_t first = static_cast<int64_t>(t.expert) * g.M + t.m0;
         const auto rows = raw_buffer(static_cast<char*>(g.out) + first * row_bytes, height * row_bytes);
@@ -743,7 +791,7 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
                 }
             }
         }
-    } else if constexpr (kOp == GemmOp::kDownGrad) {
+    } else if constexpr (S::kOp == GemmOp::kDownGrad) {
         const int I = g.N;
         const auto kept = rows_of(g.gate_up, I * 4u);
         const auto codes = rows_of(g.codes, I * 2u);
@@ -814,13 +862,13 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
 }
 
 // How many stores gemm_store is sure to make after its last load.
-template <GemmOp kOp, bool kFp8>
+template <class S>
 __device__ __forceinline__ int stores_after(const GemmArgs& g, int mt) {
-    if constexpr (kOp == GemmOp::kGateUp)
-        return mt * (kFp8 ? 1 : 1 + (g.gate_up ? 2 : 0) + (g.codes ? 2 : 0));
-    else if constexpr (kOp == GemmOp::kWeightGrad)
+    if constexpr (S::kOp == GemmOp::kGateUp)
+        return mt * (S::kFp8 ? 1 : 1 + (g.gate_up ? 2 : 0) + (g.codes ? 2 : 0));
+    else if constexpr (S::kOp == GemmOp::kWeightGrad)
         return g.accumulate ? 0 : mt * (g.out_fp32 ? 4 : 2);
-    else if constexpr (kOp == GemmOp::kDownGrad)
+    else if constexpr (S::kOp == GemmOp::kDownGrad)
         return 0;
     else
         return mt * 2;
@@ -847,6 +895,29 @@ __device__ __forceinline__ void end_slot() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// The products' scales of an e4m3 tile: one per step for the gate's (all) channels, one for the up
+// projection's.
+template <class S>
+struct WeightScales {
+    const float* row;
+    int64_t up;
+    __device__ __forceinline__ WeightScales(const GemmArgs& g, const Tile& t, int wn) {
+        if constexpr (S::kFp8) {
+            const int KB = g.K / 128;
+            const int nb = S::kGated ? t.n0 / 128 : min((t.n0 + wn * 64) / 128, g.N / 128 - 1);
+            row = g.b_scales +
+                  (static_cast<int64_t>(t.expert) * (S::kGated ? 2 : 1) * (g.N / 128) + nb) * KB;
+            up = static_cast<int64_t>(g.N / 128) * KB;
+        }
+    }
+    __device__ __forceinline__ void read(int step, float (&bs)[2]) const {
+        if constexpr (S::kFp8) {
+            bs[0] = row[step];
+            if constexpr (S::kGated) bs[1] = row[up + step];
+        }
+    }
+};
+
 // One tile's steps with kMT subtiles of 16 rows per wave. The block's two halves (waves 0..3 and
 // 4..7, one of each on every SIMD) take turns: while one multiplies, the other reads its next
 // fragments from LDS and issues loads, and a barrier ends each such slot. A step is four slots:
@@ -855,120 +926,128 @@ __device__ __forceinline__ void end_slot() {
 // where reading 1 takes the n side and the first half of the m side and issues the second half
 // of the next step's m side; reading 2 takes the second half and issues the rest of the step
 // after the next into the places that reading 1 has left. Every load has six slots to arrive: of
-// a wave's loads all but the last kLoads have to be there at the end of every odd slot.
-template <GemmOp kOp, bool kFp8, int kMT>
+// a wave's loads all but the last kLoads have to be there at the end of every odd slot. The
+// stores of the tile before lie between those loads in a tile's first step, and need not have
+// ended there.
+template <class S, int kMT>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& t, int steps,
-                                          Producer<kOp, kFp8>& p, f32x4 (&acc)[8][4],
+                                          Producer<S, S::kWaves>& p, f32x4 (&acc)[S::kMT][4],
                                           char* lds, int& count, int& stores,
                                           const TileRing& ring, int wm, int wn,
                                           const LanePlace& at, int lane) {
-    using S = GemmShape<kOp, kFp8>;
     constexpr int kP = first_phase(kMT);
-    const float* bs_row = nullptr;
-    int64_t up_scales = 0;
+    constexpr int kLoads = Producer<S, S::kWaves>::kLoads;
+    const WeightScales<S> weight_scales(g, t, wn);
     float bs[2] = {1.0f, 1.0f};
-    if constexpr (kFp8) {
-        const int KB = g.K / 128;
-        const int nb = S::kGated ? t.n0 / 128 : min((t.n0 + wn * 64) / 128, g.N / 128 - 1);
-        bs_row = g.b_scales +
-                 (static_cast<int64_t>(t.expert) * (S::kGated ? 2 : 1) * (g.N / 128) + nb) * KB;
-        up_scales = static_cast<int64_t>(g.N / 128) * KB;
-    }
     if (wm) end_slot();
     for (int step = 0; step < steps; ++step, ++count) {
         const char* stage = lds + (count & 1) * S::kStageBytes;
-        const char* scales = lds + S::kScalesAt + (count & 3) * kScaleBytes;
+        const char* scales = lds + S::kScalesAt + (count & 3) * S::kScaleBytes;
         Fragment b[4], a[kP];
         float as[kP];
-        read_n_side<kOp, kFp8>(b, stage + kOperandBytes, wn, at);
+        read_n_side<S>(b, stage + S::kMBytes, wn, at);
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
             read_fragment<S::kAByRows>(a[i], stage, (2 * i + wm) * 16, at);
-            if constexpr (kFp8)
+            if constexpr (S::kFp8)
                 as[i] = *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
         }
-        if constexpr (kFp8) {
-            bs[0] = bs_row[step];
-            if constexpr (S::kGated) bs[1] = bs_row[up_scales + step];
-        }
+        weight_scales.read(step, bs);
         p.issue_second();
-        if (wm) wait_loads_before<S::kLoads>(stores);
+        if (wm) wait_loads_before<kLoads>(stores);
         end_slot();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) multiply<kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
+        for (int i = 0; i < kP; ++i) multiply<S::kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
         __builtin_amdgcn_s_setprio(0);
-        if (!wm) wait_loads_before<S::kLoads>(stores);
+        if (!wm) wait_loads_before<kLoads>(stores);
         end_slot();
 #pragma unroll
         for (int i = kP; i < kMT; ++i) {
-            read_fragment<S::kAByRows>(a[i - kP], stage + kHalfBytes, (2 * (i - kP) + wm) * 16, at);
-            if constexpr (kFp8)
+            read_fragment<S::kAByRows>(a[i - kP], stage + S::kMBytes / 2, (2 * (i - kP) + wm) * 16,
+                                       at);
+            if constexpr (S::kFp8)
                 as[i - kP] =
                     *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
         }
         p.issue_first(ring);
-        if (wm) wait_loads_before<S::kLoads>(stores);
+        if (wm) wait_loads_before<kLoads>(stores);
         end_slot();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = kP; i < kMT; ++i)
-            multiply<kFp8, S::kGated>(acc[i], b, a[i - kP], as[i - kP], bs);
+            multiply<S::kFp8, S::kGated>(acc[i], b, a[i - kP], as[i - kP], bs);
         __builtin_amdgcn_s_setprio(0);
-        if (!wm) wait_loads_before<S::kLoads>(stores);
+        if (!wm) wait_loads_before<kLoads>(stores);
         stores = 0;
         end_slot();
     }
     if (!wm) end_slot();
-    gemm_store<kOp, kFp8, kMT>(g, t, acc, lds + S::kAmaxAt, wm, wn, lane);
-    stores = stores_after<kOp, kFp8>(g, kMT);
+    gemm_store<S, kMT>(g, t, acc, lds + S::kAmaxAt, wm, wn, lane);
+    stores = stores_after<S>(g, kMT);
 }
 
-template <GemmOp kOp, bool kFp8>
-__global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g) {
-    using S = GemmShape<kOp, kFp8>;
+// A block's tiles: every gridDim.x-th from its first. Block b runs on die b % 8: its tiles are
+// neighbours of that die's other blocks' tiles.
+struct BlockTiles {
+    TileMap map;
+    int64_t first;
+    int count;
+    TileRing ring;
+
+    template <class S>
+    __device__ __forceinline__ void init(const GemmArgs& g, char* lds) {
+        map.init(g, !S::kOverRows, S::kTileM, S::kNTile, reinterpret_cast<int*>(lds + S::kTableAt));
+        const int per_die = gridDim.x / 8;
+        first = gridDim.x % 8 == 0
+                    ? static_cast<int64_t>(blockIdx.x % 8) * per_die + blockIdx.x / 8
+                    : blockIdx.x;
+        count = first < map.total
+                    ? static_cast<int>((map.total - first + gridDim.x - 1) / gridDim.x)
+                    : 0;
+        for (int n = 0; n < S::kStages; ++n) look_up<S>(n);
+    }
+    template <class S>
+    __device__ __forceinline__ void look_up(int n) {
+        if (n < count)
+            ring.put(n, map.find(first + static_cast<int64_t>(n) * gridDim.x, S::kNTile));
+    }
+};
+
+template <class S>
+__device__ __forceinline__ void clear(f32x4 (&acc)[S::kMT][4]) {
+#pragma unroll
+    for (int i = 0; i < S::kMT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+template <class S>
+__global__ __launch_bounds__(S::kThreads, 1) void gemm_kernel(const GemmArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[S::kLdsBytes];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / S::kNWaves, wn = wave % S::kNWaves;
     const LanePlace at(lane);
-    TileMap map;
-    map.init(g, !S::kOverRows, S::kNTile, reinterpret_cast<int*>(lds + S::kTableAt));
-    // block b runs on die b % 8: its tiles are neighbours of that die's other blocks' tiles
-    const int per_die = gridDim.x / 8;
-    const int64_t first = gridDim.x % 8 == 0
-                              ? static_cast<int64_t>(blockIdx.x % 8) * per_die + blockIdx.x / 8
-                              : blockIdx.x;
-    const int tiles =
-        first < map.total ? static_cast<int>((map.total - first + gridDim.x - 1) / gridDim.x) : 0;
-    TileRing ring;
-    auto look_up = [&](int n) {
-        if (n < tiles) ring.put(n, map.find(first + static_cast<int64_t>(n) * gridDim.x, S::kNTile));
-    };
-    look_up(0);
-    look_up(1);
-    look_up(2);
-    Producer<kOp, kFp8> p(g, lds_address(lds), tiles, ring);
+    BlockTiles tiles;
+    tiles.init<S>(g, lds);
+    Producer<S, S::kWaves> p(g, lds_address(lds), wave, tiles.count, tiles.ring);
     int count = 0, stores = 0;
-    p.issue_first(ring);
+    p.issue_first(tiles.ring);
     p.issue_second();
-    p.issue_first(ring);
-    wait_loads<S::kLoads>();
+    p.issue_first(tiles.ring);
+    wait_loads<Producer<S, S::kWaves>::kLoads>();
     end_slot();
-    for (int n = 0; n < tiles; ++n) {
-        look_up(n + 3);
-        const Tile t = ring.get(n);
-        const int steps = tile_steps<kOp, kFp8>(g, t);
-        f32x4 acc[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int mt = (t.height + 31) / 32;
-        switch (max(mt, 1)) {  // a piece of a low tile may have got no row
-#define EP_GEMM_CASE(n)                                                                   \
-    case n:                                                                               \
-        gemm_tile<kOp, kFp8, n>(g, t, steps, p, acc, lds, count, stores, ring, wm, wn, at, lane); \
+    for (int n = 0; n < tiles.count; ++n) {
+        tiles.look_up<S>(n + S::kStages);
+        const Tile t = tiles.ring.get(n);
+        const int steps = tile_steps<S>(g, t);
+        f32x4 acc[S::kMT][4];
+        clear<S>(acc);
+        switch (max((t.height + 31) / 32, 1)) {  // a piece of a low tile may have got no row
+#define EP_GEMM_CASE(n)                                                                            \
+    case n:                                                                                        \
+        gemm_tile<S, n>(g, t, steps, p, acc, lds, count, stores, tiles.ring, wm, wn, at, lane);    \
         break;
             EP_GEMM_CASE(1)
             EP_GEMM_CASE(2)
@@ -984,17 +1063,132 @@ __global__ __launch_bounds__(kGemmThreads, 1) void gemm_kernel(const GemmArgs g)
     wait_loads<0>();  // no load outlives the block
 }
 
+// One tile's steps in the waves that multiply.
+template <class S, int kMT>
+__device__ __forceinline__ void stream_tile(const GemmArgs& g, const Tile& t, int steps,
+                                            f32x4 (&acc)[S::kMT][4], char* lds, int& slot,
+                                            int& scale_slot, int wm, int wn, const LanePlace& at,
+                                            int lane) {
+    const WeightScales<S> weight_scales(g, t, wn);
+    float bs[2] = {1.0f, 1.0f};
+    for (int step = 0; step < steps; ++step) {
+        weight_scales.read(step, bs);
+        lds_barrier();
+        const char* stage = lds + slot * S::kStageBytes;
+        const char* scales = lds + S::kScalesAt + scale_slot * S::kScaleBytes;
+        slot = slot + 1 == S::kStages ? 0 : slot + 1;
+        scale_slot = (scale_slot + 1) & (kScaleSlots - 1);
+        Fragment b[4], a[kMT];
+        float as[kMT];
+        read_n_side<S>(b, stage + S::kMBytes, wn, at);
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+            read_fragment<S::kAByRows>(a[i], stage, (2 * i + wm) * 16, at);
+            if constexpr (S::kFp8)
+                as[i] = *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) multiply<S::kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
+    }
+    gemm_store<S, kMT>(g, t, acc, lds + S::kAmaxAt, wm, wn, lane);
+}
+
+// Most waves multiply and four load: a load that memory holds up stops none of the products, and
+// the stores of a tile wait for no load. All meet once a step: then step k has arrived, step
+// k - 1 has been read, and the loaders go on to step k + kStages - 1 in its place.
+template <class S>
+__global__ __launch_bounds__(S::kThreads, 1) void stream_kernel(const GemmArgs g) {
+    __shared__ __attribute__((aligned(1024))) char lds[S::kLdsBytes];
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    BlockTiles tiles;
+    tiles.init<S>(g, lds);
+    if (wave >= S::kWaves) {
+        using P = Producer<S, S::kLoaders>;
+        P p(g, lds_address(lds), wave - S::kWaves, tiles.count, tiles.ring);
+        const bool meets_after = S::kGated && g.codes;  // for the magnitudes of the tile's groups
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) p.issue_first(tiles.ring);
+        for (int n = 0; n < tiles.count; ++n) {
+            tiles.look_up<S>(n + S::kStages);
+            const int steps = tile_steps<S>(g, tiles.ring.get(n));
+            for (int step = 0; step < steps; ++step) {
+                wait_loads<(S::kStages - 2) * P::kLoads>();
+                lds_barrier();
+                p.issue_first(tiles.ring);
+            }
+            if (meets_after) lds_barrier();
+        }
+        wait_loads<0>();  // no load outlives the block
+        return;
+    }
+    const int wm = wave / S::kNWaves, wn = wave % S::kNWaves;
+    const LanePlace at(lane);
+    int slot = 0, scale_slot = 0;
+    for (int n = 0; n < tiles.count; ++n) {
+        tiles.look_up<S>(n + S::kStages);
+        const Tile t = tiles.ring.get(n);
+        const int steps = tile_steps<S>(g, t);
+        f32x4 acc[S::kMT][4];
+        clear<S>(acc);
+        switch (max((t.height + 31) / 32, 1)) {
+#define EP_STREAM_CASE(n)                                                                        \
+    case n:                                                                                      \
+        if constexpr (n <= S::kMT)                                                               \
+            stream_tile<S, n>(g, t, steps, acc, lds, slot, scale_slot, wm, wn, at, lane);        \
+        break;
+            EP_STREAM_CASE(1)
+            EP_STREAM_CASE(2)
+            EP_STREAM_CASE(3)
+            EP_STREAM_CASE(4)
+#undef EP_STREAM_CASE
+        }
+    }
+}
+
+// Tiles of a call at most, as the host knows it.
+template <class S>
+int64_t most_tiles(const GemmArgs& g) {
+    const int64_t nt = (g.N + S::kNTile - 1) / S::kNTile;
+    if constexpr (S::kOverRows)
+        return static_cast<int64_t>(g.E) * ((g.M + S::kTileM - 1) / S::kTileM) * nt;
+    return (g.num_rows / S::kTileM + std::min<int64_t>(g.E, g.num_rows)) * nt;
+}
+
+template <class S>
+hipError_t launch_shape(const GemmArgs& g, hipStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(kBlocks, most_tiles<S>(g)));
+    if (blocks == 0) return hipSuccess;
+    if constexpr (S::kLoaders > 0)
+        stream_kernel<S><<<blocks, S::kThreads, 0, stream>>>(g);
+    else
+        gemm_kernel<S><<<blocks, S::kThreads, 0, stream>>>(g);
+    return hipGetLastError();
+}
+
+#ifndef EP_GEMM_LOW
+#define EP_GEMM_LOW 24
+#endif
+#ifndef EP_GEMM_MID
+#define EP_GEMM_MID 144
+#endif
+#ifndef EP_GEMM_FEW
+#define EP_GEMM_FEW kBlocks
+#endif
 template <GemmOp kOp, bool kFp8>
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream) {
-    using S = GemmShape<kOp, kFp8>;
-    constexpr int64_t kBlocks = 256;  // one per CU
-    const int64_t nt = (g.N + S::kNTile - 1) / S::kNTile;
-    const int64_t mt = S::kOverRows ? static_cast<int64_t>(g.E) * ((g.M + kTileM - 1) / kTileM)
-                                    : g.num_rows / kTileM + std::min<int64_t>(g.E, g.num_rows);
-    const int64_t blocks = std::min(kBlocks, mt * nt);
-    if (blocks == 0) return hipSuccess;
-    gemm_kernel<kOp, kFp8><<<static_cast<unsigned>(blocks), kGemmThreads, 0, stream>>>(g);
-    return hipGetLastError();
+    using Low = GemmShape<kOp, kFp8, 32>;
+    using Mid = GemmShape<kOp, kFp8, 128>;
+    const int64_t rows = g.num_rows / g.E;
+    if (rows <= EP_GEMM_LOW || most_tiles<Mid>(g) < EP_GEMM_FEW) {
+        if constexpr (!kFp8)
+            if (!(kOp == GemmOp::kGateUp && g.codes) && most_tiles<Low>(g) < EP_GEMM_FEW)
+                return launch_shape<GemmShape<kOp, kFp8, 32, 128>>(g, stream);
+        return launch_shape<Low>(g, stream);
+    }
+    if constexpr (!kFp8)
+        if (rows > EP_GEMM_MID) return launch_shape<GemmShape<kOp, kFp8, 256>>(g, stream);
+    return launch_shape<Mid>(g, stream);
 }
 
 }  // namespace ep
