@@ -5,6 +5,9 @@
 //   grad_W[e] = grad_rows^T input_rows over expert e's rows          ep_expert_weight_grad
 #include "expert_gemm.hpp"
 
+#ifndef EP_WG_ROWS
+#define EP_WG_ROWS 640
+#endif
 namespace ep {
 
 hipError_t launch_expert_down_grad(const GemmArgs& g, hipStream_t stream) {
@@ -16,11 +19,10 @@ hipError_t launch_expert_gate_up_grad(const GemmArgs& g, hipStream_t stream) {
 }
 
 hipError_t launch_expert_weight_grad(const GemmArgs& g, hipStream_t stream) {
-#ifdef EP_WG256
-    return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 256>>(g, stream);
-#else
+    // an expert's rows are the inner size here
+    if (g.num_rows / g.E > EP_WG_ROWS)
+        return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 256>>(g, stream);
     return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 128>>(g, stream);
-#endif
 }
 
 }  // namespace ep

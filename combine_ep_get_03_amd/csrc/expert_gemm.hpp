@@ -22,7 +22,8 @@ constexpr int kBlocks = 256;        // one per CU
 constexpr int kStepBytes = 128;     // bytes of k per row and step: 64 bf16 or 128 e4m3
 constexpr int kScaleSlots = 4;      // steps whose row scales are in LDS
 constexpr int kTableExperts = 1024; // with at most so many experts, their offsets are kept in LDS
-constexpr int kTableBytes = (kTableExperts + 32) * 4;
+constexpr int kRingBytes = 8 * 32;   // the next eight tiles
+constexpr int kTableBytes = (kTableExperts + 32) * 4 + kRingBytes;
 constexpr uint32_t kOutOfBuffer = 0x80000000u;  // an offset past every buffer made here
 
 enum class GemmOp {
@@ -630,8 +631,25 @@ __device__ __forceinline__ void eight_channels(const f32x4& a, const f32x4& b, f
     }
 }
 
+template <int kPolicy = 0>
 __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t buf, uint32_t at, u32x4 w) {
-    __builtin_amdgcn_raw_buffer_store_b128(w, buf, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(w, buf, at, 0, kPolicy);
+}
+
+// Lane l holds two 16-byte words of row l % 16 of a subtile: its quarter (l / 16) of the first and
+// of the second half of a 128-byte line. Exchanged between lanes eight apart, so that each of
+// two stores writes eight whole lines: a = the words of rows 0..7, b = those of rows 8..15, a
+// lane's being of row l % 8 (+ 8) and of half (l / 8) % 2.
+__device__ __forceinline__ void whole_lines(u32x4& a, u32x4& b, int lane) {
+    const bool low = (lane & 8) == 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t give = low ? b[i] : a[i];
+        const uint32_t got = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+            0, static_cast<int>(give), 0x128, 0xf, 0xf, true));  // rotated by 8 within 16 lanes
+        a[i] = low ? a[i] : got;
+        b[i] = low ? got : b[i];
+    }
 }
 
 __device__ __forceinline__ u32x2 e4m3_eight(const float (&v)[8], float inv) {
@@ -757,38 +775,64 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
         const uint32_t row_bytes = g.N * (g.out_fp32 ? 4u : 2u);
         const int64_t first = static_cast<int64_t>(t.expert) * g.M + t.m0;
         const auto rows = raw_buffer(static_cast<char*>(g.out) + first * row_bytes, height * row_bytes);
+        const int half = (lane >> 3) & 1;
+        constexpr int kPolicy = S::kLoaders > 0 ? kPolicyNt : 0;
 #pragma unroll
         for (int i = 0; i < kMT; ++i) {
-            const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
+            const uint32_t m = (2 * i + wm) * 16 + (lane & 7);
+            if (g.out_fp32) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const uint32_t c = t.n0 + wn * 64 + p * 32 + in_pair;
-                const bool in = c < static_cast<uint32_t>(g.N);
-                float v[8];
-                eight_channels(acc[i][2 * p], acc[i][2 * p + 1], v);
-                if (g.out_fp32) {
-                    const uint32_t at = in ? m * row_bytes + c * 4u : kOutOfBuffer;
+                for (int p = 0; p < 2; ++p) {
+                    const uint32_t c = t.n0 + wn * 64 + p * 32 + half * 16 + quad * 4;
+                    const bool in = c < static_cast<uint32_t>(g.N);
+                    u32x4 w[2] = {__builtin_bit_cast(u32x4, acc[i][2 * p]),
+                                  __builtin_bit_cast(u32x4, acc[i][2 * p + 1])};
+                    whole_lines(w[0], w[1], lane);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        f32x4 w = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-                        const uint32_t to = in ? at + 16 * h : at;
+                        const uint32_t at = in ? (m + 8 * h) * row_bytes + c * 4u : kOutOfBuffer;
                         if (g.accumulate)
-                            w += __builtin_bit_cast(
-                                f32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, to, 0, 0));
-                        store16(rows, to, __builtin_bit_cast(u32x4, w));
+                            w[h] = __builtin_bit_cast(
+                                u32x4, __builtin_bit_cast(f32x4, w[h]) +
+                                           __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                         rows, at, 0, 0)));
+                        store16<kPolicy>(rows, at, w[h]);
                     }
-                } else {
-                    const uint32_t at = in ? m * row_bytes + c * 2u : kOutOfBuffer;
-                    if (g.accumulate) {
-                        float w[8];
+                }
+            } else {
+                const uint32_t c = t.n0 + wn * 64 + half * 32 + in_pair;
+                const bool in = c < static_cast<uint32_t>(g.N);
+                u32x4 w[2];
+                if (g.accumulate) {
+                    // added in fp32, before the rounding: each pair's words where its sums are
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const uint32_t cp = t.n0 + wn * 64 + p * 32 + in_pair;
+                        const uint32_t at =
+                            cp < static_cast<uint32_t>(g.N)
+                                ? ((2 * i + wm) * 16 + (lane & 15)) * row_bytes + cp * 2u
+                                : kOutOfBuffer;
+                        float v[8], old[8];
+                        eight_channels(acc[i][2 * p], acc[i][2 * p + 1], v);
                         widen8(__builtin_bit_cast(
                                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, at, 0, 0)),
-                               w);
+                               old);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) v[r] += w[r];
+                        for (int r = 0; r < 8; ++r) v[r] += old[r];
+                        w[p] = narrow8(v);
                     }
-                    store16(rows, at, narrow8(v));
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        float v[8];
+                        eight_channels(acc[i][2 * p], acc[i][2 * p + 1], v);
+                        w[p] = narrow8(v);
+                    }
                 }
+                whole_lines(w[0], w[1], lane);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    store16<kPolicy>(rows, in ? (m + 8 * h) * row_bytes + c * 2u : kOutOfBuffer, w[h]);
             }
         }
     } else if constexpr (S::kOp == GemmOp::kDownGrad) {
@@ -801,6 +845,7 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
 #pragma unroll
         for (int i = 0; i < kMT; ++i) {
             const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
+            u32x4 dgate[2], dup[2], again[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const uint32_t c = t.n0 + wn * 64 + p * 32 + in_pair;
@@ -838,24 +883,42 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
                     dg[r] = da[r] * up[r] * s * (1.0f + gate[r] * (1.0f - s));
                     up[r] *= silu;
                 }
-                store16(grad, at, narrow8(dg));
-                store16(grad, in ? at + I * 2u : at, narrow8(du));
-                if (g.act) store16(act, in ? m * (I * 2u) + c * 2u : kOutOfBuffer, narrow8(up));
+                dgate[p] = narrow8(dg);
+                dup[p] = narrow8(du);
+                again[p] = narrow8(up);
+            }
+            whole_lines(dgate[0], dgate[1], lane);
+            whole_lines(dup[0], dup[1], lane);
+            whole_lines(again[0], again[1], lane);
+            const uint32_t c = t.n0 + wn * 64 + ((lane >> 3) & 1) * 32 + in_pair;
+            const bool in = c < static_cast<uint32_t>(I);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t row = (2 * i + wm) * 16 + (lane & 7) + 8 * h;
+                const uint32_t at = in ? row * (I * 4u) + c * 2u : kOutOfBuffer;
+                store16(grad, at, dgate[h]);
+                store16(grad, in ? at + I * 2u : at, dup[h]);
+                if (g.act) store16(act, in ? row * (I * 2u) + c * 2u : kOutOfBuffer, again[h]);
             }
         }
     } else {
         const auto rows = rows_of(g.out, g.N * 2u);
+        const uint32_t c = t.n0 + wn * 64 + ((lane >> 3) & 1) * 32 + in_pair;
+        const bool in = c < static_cast<uint32_t>(g.N);
 #pragma unroll
         for (int i = 0; i < kMT; ++i) {
-            const uint32_t m = (2 * i + wm) * 16 + (lane & 15);
+            u32x4 w[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const uint32_t c = t.n0 + wn * 64 + p * 32 + in_pair;
                 float v[8];
                 eight_channels(acc[i][2 * p], acc[i][2 * p + 1], v);
-                store16(rows,
-                        c < static_cast<uint32_t>(g.N) ? m * (g.N * 2u) + c * 2u : kOutOfBuffer,
-                        narrow8(v));
+                w[p] = narrow8(v);
+            }
+            whole_lines(w[0], w[1], lane);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t m = (2 * i + wm) * 16 + (lane & 7) + 8 * h;
+                store16(rows, in ? m * (g.N * 2u) + c * 2u : kOutOfBuffer, w[h]);
             }
         }
     }
@@ -1005,12 +1068,27 @@ struct BlockTiles {
         count = first < map.total
                     ? static_cast<int>((map.total - first + gridDim.x - 1) / gridDim.x)
                     : 0;
-        for (int n = 0; n < S::kStages; ++n) look_up<S>(n);
     }
     template <class S>
     __device__ __forceinline__ void look_up(int n) {
         if (n < count)
             ring.put(n, map.find(first + static_cast<int64_t>(n) * gridDim.x, S::kNTile));
+    }
+    // Tile n for the waves that do not look up themselves: they read it after a barrier.
+    template <class S>
+    __device__ __forceinline__ void publish(int n, char* lds) const {
+        const int at = (n & 7) * 8, lane = lane_id();
+        if (n < count && lane >= at && lane < at + 6)
+            reinterpret_cast<int*>(lds + S::kTableAt)[kTableExperts + 32 + lane] = ring.lanes;
+    }
+    template <class S>
+    __device__ __forceinline__ static Tile published(int n, const char* lds) {
+        const int* p = reinterpret_cast<const int*>(lds + S::kTableAt) + kTableExperts + 32 +
+                       (n & 7) * 8;
+        int field[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) field[i] = __builtin_amdgcn_readfirstlane(p[i]);
+        return Tile{field[0], field[1], field[2], field[3], field[4], field[5]};
     }
 };
 
@@ -1031,6 +1109,7 @@ __global__ __launch_bounds__(S::kThreads, 1) void gemm_kernel(const GemmArgs g) 
     const LanePlace at(lane);
     BlockTiles tiles;
     tiles.init<S>(g, lds);
+    for (int n = 0; n < S::kStages; ++n) tiles.look_up<S>(n);
     Producer<S, S::kWaves> p(g, lds_address(lds), wave, tiles.count, tiles.ring);
     int count = 0, stores = 0;
     p.issue_first(tiles.ring);
@@ -1105,17 +1184,25 @@ __global__ __launch_bounds__(S::kThreads, 1) void stream_kernel(const GemmArgs g
     tiles.init<S>(g, lds);
     if (wave >= S::kWaves) {
         using P = Producer<S, S::kLoaders>;
+        for (int n = 0; n < S::kStages; ++n) {
+            tiles.look_up<S>(n);
+            tiles.publish<S>(n, lds);
+        }
+        lds_barrier();
         P p(g, lds_address(lds), wave - S::kWaves, tiles.count, tiles.ring);
         const bool meets_after = S::kGated && g.codes;  // for the magnitudes of the tile's groups
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) p.issue_first(tiles.ring);
         for (int n = 0; n < tiles.count; ++n) {
-            tiles.look_up<S>(n + S::kStages);
             const int steps = tile_steps<S>(g, tiles.ring.get(n));
             for (int step = 0; step < steps; ++step) {
                 wait_loads<(S::kStages - 2) * P::kLoads>();
                 lds_barrier();
                 p.issue_first(tiles.ring);
+                if (step == 0) {
+                    tiles.look_up<S>(n + S::kStages);
+                    tiles.publish<S>(n + S::kStages, lds);
+                }
             }
             if (meets_after) lds_barrier();
         }
@@ -1125,9 +1212,9 @@ __global__ __launch_bounds__(S::kThreads, 1) void stream_kernel(const GemmArgs g
     const int wm = wave / S::kNWaves, wn = wave % S::kNWaves;
     const LanePlace at(lane);
     int slot = 0, scale_slot = 0;
+    lds_barrier();
     for (int n = 0; n < tiles.count; ++n) {
-        tiles.look_up<S>(n + S::kStages);
-        const Tile t = tiles.ring.get(n);
+        const Tile t = BlockTiles::published<S>(n, lds);
         const int steps = tile_steps<S>(g, t);
         f32x4 acc[S::kMT][4];
         clear<S>(acc);
