@@ -18,7 +18,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kBlocks = 256;        // one per CU
+constexpr int kBlocks = 256;        // one per CU; a power of two
 constexpr int kStepBytes = 128;     // bytes of k per row and step: 64 bf16 or 128 e4m3
 constexpr int kScaleSlots = 4;      // steps whose row scales are in LDS
 constexpr int kTableExperts = 1024; // with at most so many experts, their offsets are kept in LDS
@@ -149,13 +149,26 @@ struct TileMap {
                                   : static_cast<int>(min<int64_t>(offset[e], num_rows));
     }
 
-    // Ends with a barrier.
+    // Every wave has to come here.
     __device__ __forceinline__ void init(const GemmArgs& g, bool rows, int m_tile, int n_tile,
                                          int* lds_table) {
         tile_m = m_tile;
-        if (g.E <= kTableExperts)
-            for (int e = threadIdx.x; e <= g.E; e += static_cast<int>(blockDim.x))
-                lds_table[e] = static_cast<int>(min<int64_t>(g.offset[e], g.num_rows));
+        // one read of the offsets per block: the lanes' chunks are summed from LDS
+        int bad_pair = 0, past = 0;
+        for (int e = threadIdx.x; e <= g.E; e += static_cast<int>(blockDim.x)) {
+            const int here = g.offset[e];
+            const int before = e > 0 ? g.offset[e - 1] : 0;
+            bad_pair |= here < before;
+            past |= here > g.num_rows;
+            if (g.E <= kTableExperts)
+                lds_table[e] = static_cast<int>(min<int64_t>(here, g.num_rows));
+        }
+        if (threadIdx.x < 2) lds_table[kTableExperts + 2 + threadIdx.x] = 0;
+        lds_barrier();
+        if (bad_pair) lds_table[kTableExperts + 2] = 1;
+        if (past) lds_table[kTableExperts + 3] = 1;
+        lds_barrier();
+        const bool bad = lds_table[kTableExperts + 2] != 0, over = lds_table[kTableExperts + 3] != 0;
         table = lds_table;
         offset = g.offset;
         num_rows = g.num_rows;
@@ -167,15 +180,12 @@ struct TileMap {
         const int lane = lane_id();
         const int e0 = min(lane * chunk, E), e1 = min(e0 + chunk, E);
         int count = 0;
-        int64_t prev = offset[e0];
-        bool bad = prev < 0, over = false;
-        for (int e = e0; e < e1; ++e) {
-            const int64_t next = offset[e + 1];
-            bad |= next < prev;
-            over |= next > num_rows;
-            count += tiles(static_cast<int>(min(next, num_rows) - min(prev, num_rows)));
-            prev = next;
-        }
+        if (!bad)
+            for (int e = e0, prev = start(e0); e < e1; ++e) {
+                const int next = start(e + 1);
+                count += tiles(next - prev);
+                prev = next;
+            }
         int sum = count;
         for (int d = 1; d < kWave; d *= 2) {
             const int o = __shfl_up(sum, d);
@@ -184,17 +194,17 @@ struct TileMap {
         first = sum - count;
         mt = rows ? __builtin_amdgcn_readlane(sum, kWave - 1) : tiles(M);
         total = static_cast<int64_t>(mt) * nt * (rows ? 1 : E);
-        bad = wave_ballot(bad) != 0;
-        over = wave_ballot(over) != 0;
         if (bad) total = 0;
+        // a grid of fewer blocks than CUs has one for every tile
         const int blocks = gridDim.x;
-        const int rest = static_cast<int>(total % blocks);
+        const int rest = static_cast<int>(blocks == kBlocks ? total & (kBlocks - 1)
+                                          : total < blocks  ? total
+                                                            : 0);
         cut = rest * 4 <= blocks ? 4 : rest * 2 <= blocks ? 2 : 1;
         whole = total - rest;
         total = whole + static_cast<int64_t>(rest) * cut;
         if ((bad || over) && blockIdx.x == 0 && threadIdx.x == 0)
             raise_error(g.error_flag, kErrSlotRange);
-        lds_barrier();
     }
 
     __device__ __forceinline__ void place(Tile& t, int in_expert, int mts, int n_tile) const {
@@ -251,7 +261,8 @@ struct TileMap {
             t.height = min(each, t.rows - t.m0);
         } else {
             const int per = mt * nt;
-            t.expert = static_cast<int>(index / per);
+            t.expert = index <= INT32_MAX ? static_cast<int>(index) / per
+                                          : static_cast<int>(index / per);
             in_expert = static_cast<int>(index - static_cast<int64_t>(t.expert) * per);
             t.row0 = start(t.expert);
             t.rows = start(t.expert + 1) - t.row0;
@@ -1065,9 +1076,10 @@ struct BlockTiles {
         first = gridDim.x % 8 == 0
                     ? static_cast<int64_t>(blockIdx.x % 8) * per_die + blockIdx.x / 8
                     : blockIdx.x;
-        count = first < map.total
-                    ? static_cast<int>((map.total - first + gridDim.x - 1) / gridDim.x)
-                    : 0;
+        const int64_t left = map.total - first + gridDim.x - 1;
+        count = first >= map.total    ? 0
+                : gridDim.x == kBlocks ? static_cast<int>(left / kBlocks)
+                                       : static_cast<int>(left) / static_cast<int>(gridDim.x);
     }
     template <class S>
     __device__ __forceinline__ void look_up(int n) {
@@ -1268,9 +1280,10 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream) {
     using Mid = GemmShape<kOp, kFp8, 128>;
     const int64_t rows = g.num_rows / g.E;
     if (rows <= EP_GEMM_LOW || most_tiles<Mid>(g) < EP_GEMM_FEW) {
+        using Narrow = GemmShape<kOp, kFp8, 32, 128>;
         if constexpr (!kFp8)
-            if (!(kOp == GemmOp::kGateUp && g.codes) && most_tiles<Low>(g) < EP_GEMM_FEW)
-                return launch_shape<GemmShape<kOp, kFp8, 32, 128>>(g, stream);
+            if (!(kOp == GemmOp::kGateUp && g.codes) && most_tiles<Narrow>(g) <= EP_GEMM_FEW)
+                return launch_shape<Narrow>(g, stream);
         return launch_shape<Low>(g, stream);
     }
     if constexpr (!kFp8)
