@@ -5,9 +5,6 @@
 //   grad_W[e] = grad_rows^T input_rows over expert e's rows          ep_expert_weight_grad
 #include "expert_gemm.hpp"
 
-#ifndef EP_WG_ROWS
-#define EP_WG_ROWS 640
-#endif
 namespace ep {
 
 hipError_t launch_expert_down_grad(const GemmArgs& g, hipStream_t stream) {
@@ -19,8 +16,11 @@ hipError_t launch_expert_gate_up_grad(const GemmArgs& g, hipStream_t stream) {
 }
 
 hipError_t launch_expert_weight_grad(const GemmArgs& g, hipStream_t stream) {
-    // an expert's rows are the inner size here
-    if (g.num_rows / g.E > EP_WG_ROWS)
+    // The rows per expert are the inner size here: with few the time is that of the stores, which
+    // the lower tiles' waves do not wait for; with many it is the products' (of 4096 x 7168
+    // weights of 32 experts, fp32, lower against higher: 256 rows 1048 / 1053 us, 384 rows
+    // 1249 / 1209, 512 rows 1461 / 1379).
+    if (g.num_rows / g.E > 256)
         return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 256>>(g, stream);
     return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 128>>(g, stream);
 }

@@ -1265,29 +1265,33 @@ hipError_t launch_shape(const GemmArgs& g, hipStream_t stream) {
     return hipGetLastError();
 }
 
-#ifndef EP_GEMM_LOW
-#define EP_GEMM_LOW 24
-#endif
-#ifndef EP_GEMM_MID
-#define EP_GEMM_MID 144
-#endif
-#ifndef EP_GEMM_FEW
-#define EP_GEMM_FEW kBlocks
-#endif
+// Which tile, by the rows per expert that the host knows of (of 4096 x 7168 weights of 32 experts,
+// us on MI355X):
+//   32 against 128 rows     16 rows  e4m3 158 / 165    32 rows  e4m3 178 / 168, bf16 333 / 310
+//   128 against 256 rows    64 rows  bf16 314 / 324    128 rows bf16 395 / 346, 1024 rows 1720 / 1540
+// e4m3 keeps the 128 rows: their products take half the time, and the loads are what is short at
+// either height (2164 against 2310 for 131072 rows of 2048 x 7168). A call with fewer tiles
+// of 128 rows than CUs takes the low ones, and narrow ones where those are at most one per CU
+// too (one token over eight experts 81 against 96 narrow and wide; 257 tokens of 1024 over 16
+// experts 17.1 against 19.8 low and not).
+constexpr int64_t kLowRows = 20, kMidRows = 96;
+
 template <GemmOp kOp, bool kFp8>
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream) {
     using Low = GemmShape<kOp, kFp8, 32>;
     using Mid = GemmShape<kOp, kFp8, 128>;
     const int64_t rows = g.num_rows / g.E;
-    if (rows <= EP_GEMM_LOW || most_tiles<Mid>(g) < EP_GEMM_FEW) {
-        using Narrow = GemmShape<kOp, kFp8, 32, 128>;
-        if constexpr (!kFp8)
-            if (!(kOp == GemmOp::kGateUp && g.codes) && most_tiles<Narrow>(g) <= EP_GEMM_FEW)
+    if (rows <= kLowRows || most_tiles<Mid>(g) < kBlocks) {
+        // a narrow tile has half a group of the gate's 128 channels, so it writes no codes
+        if constexpr (!kFp8) {
+            using Narrow = GemmShape<kOp, kFp8, 32, 128>;
+            if (!(kOp == GemmOp::kGateUp && g.codes) && most_tiles<Narrow>(g) <= kBlocks)
                 return launch_shape<Narrow>(g, stream);
+        }
         return launch_shape<Low>(g, stream);
     }
     if constexpr (!kFp8)
-        if (rows > EP_GEMM_MID) return launch_shape<GemmShape<kOp, kFp8, 256>>(g, stream);
+        if (rows > kMidRows) return launch_shape<GemmShape<kOp, kFp8, 256>>(g, stream);
     return launch_shape<Mid>(g, stream);
 }
 
