@@ -79,7 +79,8 @@ int check_expert_products(const int32_t* offset, int E, int64_t rows, int A, int
     if (E < 1 || E > EP_MAX_EXPERTS || rows < 0 || rows > INT32_MAX) return EP_ERR_ARG;
     if (A < 1 || B < 1 || A > 2 * EP_EXPERT_MAX_WIDTH || B > 2 * EP_EXPERT_MAX_WIDTH)
         return EP_ERR_ARG;
-    if ((rows / 256 + 1) * (std::max(A, B) / 128 + 1) > INT32_MAX) return EP_ERR_ARG;
+    // an expert's tiles, of the lowest kind, are numbered in 32 bits
+    if ((rows / 32 + 1) * (std::max(A, B) / 128 + 1) > INT32_MAX) return EP_ERR_ARG;
     if (!offset) return EP_ERR_ARG;
     if (A % multiple != 0 || B % multiple != 0) return EP_ERR_ALIGN;
     if (!aligned(offset, 4) || !aligned(error_flag, 4)) return EP_ERR_ALIGN;

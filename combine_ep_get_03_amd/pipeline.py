@@ -9,7 +9,8 @@ outputs:
 - one call per step: ep_get_layout, ep_dispatch, ep_restripe_prob, ep_combine.
 `step()` takes the one-call layout + dispatch or the counts path where they apply. Also the two-phase ("hook") form of
 dispatch and combine, whose send phase returns a callable that enqueues the receive phase
-later, and ExpertPath, the expert-major block with the norm in front of it and its gradients.
+later, and ExpertPath, the expert-major block with the norm in front of it, the experts
+themselves and all their gradients.
 
 Device buffers are allocated once per shape (torch, memory plumbing only); the step
 functions enqueue their calls and return without synchronising.
@@ -246,15 +247,24 @@ class ExpertPath:
         dispatch(topk_idx)               ep_get_layout with expert slots, then
                                          ep_dispatch_permute, or with fp8=True
                                          ep_dispatch_permute_fp8, of the norm's output
-        ... the caller's experts on rows expert_offset[e] .. expert_offset[e + 1] - 1 of
-            perm_x (perm_x_fp8 and perm_scales with fp8=True) ...
+        experts(w_gate_up, w_down)       with inter=I: ep_expert_gate_up and ep_expert_down, or
+                                         with fp8=True their e4m3 forms: expert_out. Or the
+                                         caller's own on rows expert_offset[e] ..
+                                         expert_offset[e + 1] - 1 of perm_x (perm_x_fp8 and
+                                         perm_scales with fp8=True)
         combine(expert_out, topk_weights, addend)   ep_combine_unpermute: out
 
     and with training=True, in reverse,
 
         combine_grad(grad_out, expert_out, topk_weights)  grad_expert_out, grad_topk_weights
+        experts_grad(w_gate_up, w_down, ...)              grad_perm_x, the weights' gradients
         dispatch_grad(grad_perm_x, addend=...)            grad_y
         norm_grad(weight, grad_residual_out)              grad_x, grad_weight
+
+    What experts() keeps of gate and up for experts_grad() is bf16, or with checkpoint="fp8" e4m3
+    in half the bytes, of which experts_grad() makes act again as well: paths of several layers
+    may then share one act (p.act = q.act). The experts' gradients need bf16 rows: inter and
+    training=True do not go with fp8=True.
 
     The gate weights are applied once, by combine(), so their gradient is combine_grad()'s.
     y feeds more than the dispatch: the router that the gate weights come from, and a shared
@@ -268,9 +278,17 @@ class ExpertPath:
     refuses. Rows of perm_x behind the last routed pair are left as they were."""
 
     def __init__(self, T: int, H: int, E: int, k: int, *, R: int = 1, N: int = 1,
-                 eps: float = 1e-6, fp8: bool = False, training: bool = False, device="cuda"):
+                 eps: float = 1e-6, fp8: bool = False, training: bool = False, device="cuda",
+                 inter: Optional[int] = None, checkpoint: str = "bf16"):
+        if checkpoint not in ("bf16", "fp8"):
+            raise ValueError(f"checkpoint: expected 'bf16' or 'fp8', got {checkpoint!r}")
+        if inter is not None and fp8 and training:
+            raise ValueError("the experts' gradients need bf16 rows: inter and training=True do not "
+                             "go with fp8=True")
+        if inter is not None and (fp8 or (training and checkpoint == "fp8")) and inter % 128:
+            raise ValueError(f"inter: expected a multiple of 128 for e4m3, got {inter}")
         self.T, self.H, self.E, self.k, self.R, self.N, self.eps = T, H, E, k, R, N, eps
-        self.fp8, self.training = fp8, training
+        self.fp8, self.training, self.inter, self.checkpoint = fp8, training, inter, checkpoint
         bf16 = dict(dtype=torch.bfloat16, device=device)
         f32 = dict(dtype=torch.float32, device=device)
         u8 = dict(dtype=torch.uint8, device=device)
@@ -297,6 +315,23 @@ class ExpertPath:
             self.grad_weight = torch.empty(H, **f32)
             ws = max(16, B.ep_rmsnorm_grad_workspace_bytes(T, H))
             self.norm_workspace = torch.empty(ws, **u8)
+        self.gate_up = self.gate_up_fp8 = self.gate_up_scales = None
+        self._kept = False  # experts() has kept gate and up
+        if inter is not None:
+            self.expert_out = torch.empty((cap, H), **bf16)
+            if fp8:
+                self.act_fp8 = torch.empty((cap, inter), **u8)
+                self.act_scales = torch.empty((cap, inter // 128), **f32)
+            else:
+                self.act = torch.empty((cap, inter), **bf16)
+            if training and checkpoint == "fp8":
+                self.gate_up_fp8 = torch.empty((cap, 2 * inter), **u8)
+                self.gate_up_scales = torch.empty((cap, 2 * inter // 128), **f32)
+            elif training:
+                self.gate_up = torch.empty((cap, 2 * inter), **bf16)
+            if training:
+                self.grad_gate_up = torch.empty((cap, 2 * inter), **bf16)
+                self.grad_perm_x = torch.empty((cap, H), **bf16)
 
     @property
     def error_flag(self) -> torch.Tensor:
@@ -339,6 +374,34 @@ class ExpertPath:
                                   stream=stream)
             self._wrote(self.perm_x, "dispatch")
 
+    def _needs_inter(self) -> None:
+        if self.inter is None:
+            raise ValueError("the experts need an ExpertPath built with inter")
+
+    def experts(self, w_gate_up, w_down, stream=None) -> None:
+        """expert_out of dispatch()'s rows. w_gate_up: bf16 [E][2 inter][H], w_down: bf16
+        [E][H][inter]; with fp8=True each a pair of e4m3 codes of that shape and fp32 scales per
+        128 x 128."""
+        self._needs_inter()
+        off, err = self.expert_offset, self.error_flag
+        if self.fp8:
+            B.ep_expert_gate_up_fp8(self.perm_x_fp8, self.perm_scales, *w_gate_up, off,
+                                    act_fp8=self.act_fp8, act_scales=self.act_scales,
+                                    error_flag=err, stream=stream)
+            B.ep_expert_down_fp8(self.act_fp8, self.act_scales, *w_down, off,
+                                 expert_out=self.expert_out, error_flag=err, stream=stream)
+        else:
+            B.ep_expert_gate_up(self.perm_x, w_gate_up, off, act=self.act, gate_up=self.gate_up,
+                                gate_up_fp8=self.gate_up_fp8, gate_up_scales=self.gate_up_scales,
+                                error_flag=err, stream=stream)
+            self._wrote(self.act, "experts")
+            if self.gate_up is not None:
+                self._wrote(self.gate_up, "experts")
+            B.ep_expert_down(self.act, w_down, off, expert_out=self.expert_out, error_flag=err,
+                             stream=stream)
+        self._kept = self.training
+        self._wrote(self.expert_out, "experts")
+
     def combine(self, expert_out, topk_weights, addend=None, stream=None) -> None:
         B.ep_combine_unpermute(expert_out, topk_weights, self.layout_buf.expert_slot,
                                out=self.out, addend=addend, error_flag=self.error_flag,
@@ -357,6 +420,35 @@ class ExpertPath:
                                     grad_topk_weights=self.grad_topk_weights,
                                     error_flag=self.error_flag, stream=stream)
         self._wrote(self.grad_expert_out, "combine_grad")
+
+    def experts_grad(self, w_gate_up, w_down, *, grad_w_gate_up=None, grad_w_down=None,
+                     accumulate: bool = False, stream=None) -> None:
+        """grad_perm_x from combine_grad()'s grad_expert_out and what experts() kept of the same
+        batch, and, where given, the weights' gradients (bf16 or fp32, shaped as the weights):
+        overwritten, or with accumulate added to."""
+        self._needs_training()
+        self._needs_inter()
+        if not self._kept:
+            raise ValueError("experts_grad needs experts() first")
+        off, err = self.expert_offset, self.error_flag
+        again = self.checkpoint == "fp8"
+        B.ep_expert_down_grad(self.grad_expert_out, w_down, off, grad_gate_up=self.grad_gate_up,
+                              gate_up=self.gate_up, gate_up_fp8=self.gate_up_fp8,
+                              gate_up_scales=self.gate_up_scales, act=self.act if again else None,
+                              error_flag=err, stream=stream)
+        if grad_w_down is not None:
+            B.ep_expert_weight_grad(self.grad_expert_out, self.act, off, grad_weight=grad_w_down,
+                                    accumulate=accumulate, error_flag=err, stream=stream)
+        if grad_w_gate_up is not None:
+            B.ep_expert_weight_grad(self.grad_gate_up, self.perm_x, off,
+                                    grad_weight=grad_w_gate_up, accumulate=accumulate,
+                                    error_flag=err, stream=stream)
+        B.ep_expert_gate_up_grad(self.grad_gate_up, w_gate_up, off, grad_x=self.grad_perm_x,
+                                 error_flag=err, stream=stream)
+        self._wrote(self.grad_gate_up, "experts_grad")
+        self._wrote(self.grad_perm_x, "experts_grad")
+        if again:
+            self._wrote(self.act, "experts_grad")
 
     def dispatch_grad(self, grad_perm_x, stream=None, *, addend=None) -> None:
         """grad_y = the sum of each token's routed rows of grad_perm_x, + addend (bf16 [T][H]:

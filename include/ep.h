@@ -661,7 +661,7 @@ int ep_dispatch_permute_grad(const void *grad_perm_x, const float *grad_perm_wei
  *                  set it too, and nothing is computed.
  *   hidden H, inter I: 1 .. EP_EXPERT_MAX_WIDTH, multiples of 8 (of 128 where e4m3 is read or
  *                  written; else EP_ERR_ALIGN). 1 <= num_experts E <= EP_MAX_EXPERTS,
- *                  0 <= num_rows <= INT32_MAX, and (num_rows / 256 + 1) * (max(H, 2 I) / 128 + 1)
+ *                  0 <= num_rows <= INT32_MAX, and (num_rows / 32 + 1) * (max(H, 2 I) / 128 + 1)
  *                  <= INT32_MAX.
  *   Arrays are 16-byte aligned (scales, offsets and the flag 4-byte). Products are summed in
  *   fp32, in an order fixed by the sizes and the expert's rows; every output is rounded once.
