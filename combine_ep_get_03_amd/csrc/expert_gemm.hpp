@@ -14,6 +14,7 @@
 namespace ep {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -290,6 +291,7 @@ struct GemmShape {
     static constexpr bool kAByRows = kOp != GemmOp::kWeightGrad;
     static constexpr bool kBByRows = kOp == GemmOp::kGateUp || kOp == GemmOp::kDown;
     static constexpr bool kOverRows = kOp == GemmOp::kWeightGrad;  // k runs over the rows
+    static constexpr bool kWidened = kFp8 && kGated;               // multiplied as bf16
     static constexpr int kNTile = kGated ? kTileN / 2 : kTileN;    // output channels of a tile
     static constexpr int kElem = kFp8 ? 1 : 2;
     static constexpr int kStepK = kStepBytes / kElem;
@@ -582,16 +584,20 @@ __device__ __forceinline__ void read_fragment(Fragment& out, const char* half, i
     }
 }
 
+// The first tile row of a wave's subtile j of the n side: with two projections the gate's
+// channels come from the first half, the up projection's from the second.
+template <class S>
+__device__ __forceinline__ int n_first(int j, int wn) {
+    return S::kGated ? (j >> 1) * (S::kTileN / 2) + wn * 32 + (j & 1) * 16 : wn * 64 + j * 16;
+}
+
 template <class S>
 __device__ __forceinline__ void read_n_side(Fragment (&b)[4], const char* operand, int wn,
                                             const LanePlace& at) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if constexpr (S::kGated)  // gate's channels from the first half, up's from the second
-            read_fragment<true>(b[j], operand,
-                                (j >> 1) * (S::kTileN / 2) + wn * 32 + (j & 1) * 16, at);
-        else if constexpr (S::kBByRows)
-            read_fragment<true>(b[j], operand, wn * 64 + j * 16, at);
+        if constexpr (S::kBByRows)
+            read_fragment<true>(b[j], operand, n_first<S>(j, wn), at);
         else  // halves of 128 columns
             read_fragment<false>(b[j], operand + (wn >> 1) * (128 * kStepBytes),
                                  (wn & 1) * 64 + j * 16, at);
@@ -1154,6 +1160,70 @@ __global__ __launch_bounds__(S::kThreads, 1) void gemm_kernel(const GemmArgs g) 
     wait_loads<0>();  // no load outlives the block
 }
 
+// Sixteen e4m3 codes as bf16, which holds every one of them.
+__device__ __forceinline__ void widen_codes(const u32x4& w, bf16x8 (&v)[2]) {
+    union {
+        bf16x2 pair[8];
+        bf16x8 eight[2];
+    } u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        u.pair[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false);
+        u.pair[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true);
+    }
+    v[0] = u.eight[0];
+    v[1] = u.eight[1];
+}
+
+// A step of e4m3 rows with the products summed in fp32 throughout: the codes are widened to bf16
+// for the bf16 matrix instruction. The e4m3 one keeps about 17 bits below the largest of the
+// products it adds (measured: its sums of 128 are off by 1.5e-5 of their size, the others by 1e-8),
+// which a bf16 output does not show, but the fp32 scales of act do. It takes twice the matrix
+// time and half as many conversions as products of the e4m3 one per lane; where the weights' way
+// from memory is what is waited for that costs little. Tiles of four pairs of subtiles take a
+// step in two parts, each scaled and added, to stay within the registers.
+template <class S, int kMT>
+__device__ __forceinline__ void widened_step(f32x4 (&acc)[S::kMT][4], const char* stage,
+                                             const float* as, const float (&bs)[2], int wm, int wn,
+                                             const LanePlace& at) {
+    constexpr int kParts = kMT > 3 ? 2 : 1, kWords = 2 / kParts;
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+        bf16x8 a[kMT][2 * kWords];
+        auto read = [&](const char* base, int first, bf16x8* v) {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                const int place = at.by_row ^ ((part + w) * 64);
+                bf16x8 two[2];
+                widen_codes(*reinterpret_cast<const u32x4*>(base + first * kStepBytes + place), two);
+                v[2 * w] = two[0];
+                v[2 * w + 1] = two[1];
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) read(stage, (2 * i + wm) * 16, a[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bf16x8 b[2 * kWords];
+            read(stage + S::kMBytes, n_first<S>(j, wn), b);
+            f32x4 d[kMT];
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < 2 * kWords; ++s)
+#pragma unroll
+                for (int i = 0; i < kMT; ++i)
+                    d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s], a[i][s], d[i], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) {
+                const float scale = as[i] * bs[S::kGated ? j >> 1 : 0];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[i][r], scale, acc[i][j][r]);
+            }
+        }
+    }
+}
+
 // One tile's steps in the waves that multiply.
 template <class S, int kMT>
 __device__ __forceinline__ void stream_tile(const GemmArgs& g, const Tile& t, int steps,
@@ -1169,15 +1239,21 @@ __device__ __forceinline__ void stream_tile(const GemmArgs& g, const Tile& t, in
         const char* scales = lds + S::kScalesAt + scale_slot * S::kScaleBytes;
         slot = slot + 1 == S::kStages ? 0 : slot + 1;
         scale_slot = (scale_slot + 1) & (kScaleSlots - 1);
-        Fragment b[4], a[kMT];
         float as[kMT];
-        read_n_side<S>(b, stage + S::kMBytes, wn, at);
+        if constexpr (S::kFp8) {
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-            read_fragment<S::kAByRows>(a[i], stage, (2 * i + wm) * 16, at);
-            if constexpr (S::kFp8)
+            for (int i = 0; i < kMT; ++i)
                 as[i] = *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
         }
+        if constexpr (S::kWidened) {
+            widened_step<S, kMT>(acc, stage, as, bs, wm, wn, at);
+            continue;
+        }
+        Fragment b[4], a[kMT];
+        read_n_side<S>(b, stage + S::kMBytes, wn, at);
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+            read_fragment<S::kAByRows>(a[i], stage, (2 * i + wm) * 16, at);
 #pragma unroll
         for (int i = 0; i < kMT; ++i) multiply<S::kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
     }

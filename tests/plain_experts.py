@@ -4,9 +4,10 @@ the tests. CPU float64 tensors in and out; rows of expert e are off[e] .. off[e 
 Bounds. A product summed over K terms in fp32, in any order and with additions that may cut
 instead of rounding (a step, 2^-23, each), is off by at most K 2^-23 times the sum of the
 terms' magnitudes, to first order; products of two bf16 or two e4m3 numbers are exact in fp32.
-The e4m3 form scales each block of 128 terms (two roundings) and adds it (one more). The e4m3
-matrix instruction adds 128 products at once in a window below the largest of them: measured on
-MI355X its sum is off by up to 2^-13 of the magnitudes' sum, taken here as 2^-12. The fast
+The e4m3 forms scale each block of 128 terms, or half of one (two roundings), and add it (one
+more). ep_expert_gate_up_fp8 multiplies in bf16, so that is all there; ep_expert_down_fp8 with the
+e4m3 matrix instruction, which adds 128 products at once in a window below the largest of them:
+measured on MI355X its sum is off by up to 2^-13 of the magnitudes' sum, taken here as 2^-12. The fast
 exponential and reciprocal of the activation are within 2^-20 relative for |gate| up to 80
 (the exponent's argument is rounded: 80 * 2^-24 * log2(e) and the two functions' own 2^-22).
 """
@@ -34,7 +35,7 @@ def fp8_weights(codes, scales):
 
 
 def product_error(K, fp8=False):
-    """Relative to the sum of the terms' magnitudes."""
+    """Relative to the sum of the terms' magnitudes. fp8: the e4m3 matrix instruction."""
     return 2.0**-12 + (K / 128 + 4) * 2.0**-23 if fp8 else (K + 2) * 2.0**-23
 
 
@@ -55,7 +56,9 @@ def nn(a, w, off):
 def gate_up(x, w, off, fp8=False):
     """(gate|up, its bound before rounding, act, act's bound before rounding)."""
     gu, mag = nt(x, w, off)
-    err = product_error(x.shape[1], fp8) * mag
+    err = product_error(x.shape[1]) * mag
+    if fp8:
+        err = err + (x.shape[1] / 64 + 4) * 2.0**-23 * mag
     I = gu.shape[1] // 2
     g, u, eg, eu = gu[:, :I], gu[:, I:], err[:, :I], err[:, I:]
     s = torch.sigmoid(g)
