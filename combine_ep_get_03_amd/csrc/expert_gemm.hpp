@@ -131,6 +131,12 @@ struct TileRing {
     }
 };
 
+// The number of expert e's first piece where its rows begin at `offset`: at least as many
+// numbers lie between two experts' as the first one's rows have pieces.
+__device__ __forceinline__ int first_piece(int offset, int e, int piece_rows) {
+    return offset / piece_rows + e;
+}
+
 struct TileMap {
     const int32_t* offset;
     int64_t num_rows;
@@ -143,11 +149,30 @@ struct TileMap {
 
     int tile_m;
 
-    __device__ __forceinline__ int tiles(int c) const { return (c + tile_m - 1) / tile_m; }
+    // unsigned: c may be as large as INT32_MAX
+    __device__ __forceinline__ int tiles(int c) const {
+        return static_cast<int>((static_cast<uint32_t>(c) + tile_m - 1) / tile_m);
+    }
 
     __device__ __forceinline__ int start(int e) const {
         return E <= kTableExperts ? table[e]
                                   : static_cast<int>(min<int64_t>(offset[e], num_rows));
+    }
+
+    // Pieces of experts in the experts' place: of expert e those from number first_piece() on,
+    // its rows cut every piece_rows, and empty ones up to the next expert's first. The offsets
+    // are sound: number `pieces` - 1 is the largest.
+    __device__ __forceinline__ void piece_offsets(const GemmArgs& g, int* lds_table) const {
+        for (int e = threadIdx.x; e <= g.E; e += static_cast<int>(blockDim.x)) {
+            const int a = static_cast<int>(min<int64_t>(g.offset[e], g.num_rows));
+            const int b = e < g.E ? static_cast<int>(min<int64_t>(g.offset[e + 1], g.num_rows)) : a;
+            const int from = first_piece(a, e, g.piece_rows);
+            const int to = e < g.E ? first_piece(b, e + 1, g.piece_rows) : g.pieces + 1;
+            for (int s = e > 0 ? from : 0; s < to; ++s)
+                lds_table[s] = s < from ? a
+                                        : static_cast<int>(min<int64_t>(
+                                              a + static_cast<int64_t>(s - from) * g.piece_rows, b));
+        }
     }
 
     // Every wave has to come here.
@@ -174,6 +199,11 @@ struct TileMap {
         offset = g.offset;
         num_rows = g.num_rows;
         E = g.E;
+        if (!rows && g.piece_rows > 0) {
+            E = g.pieces;
+            if (!bad) piece_offsets(g, lds_table);
+            lds_barrier();
+        }
         by_rows = rows;
         M = g.M;
         nt = (g.N + n_tile - 1) / n_tile;
@@ -257,7 +287,8 @@ struct TileMap {
             t.row0 = a;
             in_expert = static_cast<int>(index - static_cast<int64_t>(base) * nt);
             place(t, in_expert, mts, n_tile);
-            const int each = ((t.rows + mts - 1) / mts + 15) & ~15;
+            const int each =
+                static_cast<int>((static_cast<uint32_t>(t.rows) + mts - 1) / mts + 15) & ~15;
             t.m0 *= each;
             t.height = min(each, t.rows - t.m0);
         } else {
@@ -307,16 +338,17 @@ struct GemmShape {
     static constexpr int kBesides = (kFp8 ? kScaleSlots * kScaleBytes : 0) +
                                     (kGated ? kAmaxBytes : 0) + kTableBytes;
     static constexpr int kFit = (160 * 1024 - kBesides) / kStageBytes;
-    static constexpr int kStages = kFit < 4 || !kFp8 ? (kFit < 8 ? kFit : 8) : 4;
+    static constexpr int kMost = kFp8 ? kScaleSlots : 8;  // the scales' places, the tile ring's
+    static constexpr int kStages = kFit < kMost ? kFit : kMost;
     static constexpr int kScalesAt = kStages * kStageBytes;
     static constexpr int kAmaxAt = kScalesAt + (kFp8 ? kScaleSlots * kScaleBytes : 0);
     static constexpr int kTableAt = kAmaxAt + (kGated ? kAmaxBytes : 0);
     static constexpr int kLdsBytes = kTableAt + kTableBytes;
     static_assert(kLdsBytes <= 160 * 1024, "LDS of one CU");
-    static_assert(kStages >= 2 && (!kFp8 || kStages <= kScaleSlots), "a place for every step");
+    static_assert(kStages >= 2, "one step arrives while another is multiplied");
     static_assert(kAByRows || kTileM >= 128, "an m side by columns has halves of 128");
     static_assert(kBByRows || kTileN >= 128, "an n side by columns has halves of 128");
-    static_assert(kTileM < 256 || (kStages == 2 && kTileN == 256), "gemm_kernel");
+    static_assert(kTileM < 256 || (kStages == 2 && kTileN == 256 && !kFp8), "gemm_kernel");
 };
 
 // ---------------------------------------------------------------- one operand's loads
@@ -380,8 +412,8 @@ __device__ __forceinline__ constexpr int first_phase(int mt) { return (mt + 1) /
 // of zeros.
 template <class S>
 __device__ __forceinline__ int tile_steps(const GemmArgs& g, const Tile& t) {
-    const int k = t.height > 0 ? (S::kOverRows ? t.rows : g.K) : 0;
-    return max(1, (k + S::kStepK - 1) / S::kStepK);
+    const uint32_t k = t.height > 0 ? (S::kOverRows ? t.rows : g.K) : 0;
+    return max(1, static_cast<int>((k + S::kStepK - 1) / S::kStepK));
 }
 
 // The stream of steps that a block loads: its tiles one after the other, the steps of each, by
@@ -604,34 +636,36 @@ __device__ __forceinline__ void read_n_side(Fragment (&b)[4], const char* operan
     }
 }
 
-template <bool kFp8, bool kGated>
-__device__ __forceinline__ void multiply(f32x4 (&acc)[4], const Fragment (&b)[4], const Fragment& a,
-                                         float as, const float (&bs)[2]) {
-    if constexpr (!kFp8) {
+__device__ __forceinline__ void multiply(f32x4 (&acc)[4], const Fragment (&b)[4],
+                                         const Fragment& a) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].bf16[s], a.bf16[s], acc[j], 0,
-                                                                 0, 0);
-    } else {
-        const float sc[2] = {as * bs[0], as * bs[1]};
-        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-        f32x4 d[4];
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            d[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j].e4m3, a.e4m3, zero, 0, 0, 0,
-                                                                    0, 0, 0);
+            acc[j] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].bf16[s], a.bf16[s], acc[j], 0, 0, 0);
+}
+
+// 128 channels of e4m3 under one scale. The instruction keeps about 17 bits below the largest of
+// the products that it adds (measured: sums of 128 are off by 1.5e-5 of their size). That is a
+// 250th of half a step of the bf16 that the result is rounded to; act's fp32 scales, which would
+// show it, come from widened_step.
+__device__ __forceinline__ void multiply_e4m3(f32x4 (&acc)[4], const Fragment (&b)[4],
+                                              const Fragment& a, float scale) {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 d[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j)
+        d[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j].e4m3, a.e4m3, zero, 0, 0, 0,
+                                                                0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                acc[j][r] = fmaf(d[j][r], sc[kGated ? j >> 1 : 0], acc[j][r]);
-        // the sums are made here: moved behind the wait that follows, they keep every product
-        // of the phase in registers, which then spill
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[j]));
-    }
+        for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(d[j][r], scale, acc[j][r]);
+    // the sums are made here: moved behind the wait that follows, they keep every product of the
+    // step in registers, which then spill
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[j]));
 }
 
 // Two subtiles' sums of one row as eight consecutive channels per lane: lanes 0..31 take the
@@ -1017,46 +1051,33 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& t, int 
                                           const LanePlace& at, int lane) {
     constexpr int kP = first_phase(kMT);
     constexpr int kLoads = Producer<S, S::kWaves>::kLoads;
-    const WeightScales<S> weight_scales(g, t, wn);
-    float bs[2] = {1.0f, 1.0f};
     if (wm) end_slot();
     for (int step = 0; step < steps; ++step, ++count) {
         const char* stage = lds + (count & 1) * S::kStageBytes;
-        const char* scales = lds + S::kScalesAt + (count & 3) * S::kScaleBytes;
         Fragment b[4], a[kP];
-        float as[kP];
         read_n_side<S>(b, stage + S::kMBytes, wn, at);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
+        for (int i = 0; i < kP; ++i)
             read_fragment<S::kAByRows>(a[i], stage, (2 * i + wm) * 16, at);
-            if constexpr (S::kFp8)
-                as[i] = *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
-        }
-        weight_scales.read(step, bs);
         p.issue_second();
         if (wm) wait_loads_before<kLoads>(stores);
         end_slot();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) multiply<S::kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
+        for (int i = 0; i < kP; ++i) multiply(acc[i], b, a[i]);
         __builtin_amdgcn_s_setprio(0);
         if (!wm) wait_loads_before<kLoads>(stores);
         end_slot();
 #pragma unroll
-        for (int i = kP; i < kMT; ++i) {
+        for (int i = kP; i < kMT; ++i)
             read_fragment<S::kAByRows>(a[i - kP], stage + S::kMBytes / 2, (2 * (i - kP) + wm) * 16,
                                        at);
-            if constexpr (S::kFp8)
-                as[i - kP] =
-                    *reinterpret_cast<const float*>(scales + ((2 * i + wm) * 16 + (lane & 15)) * 4);
-        }
         p.issue_first(ring);
         if (wm) wait_loads_before<kLoads>(stores);
         end_slot();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = kP; i < kMT; ++i)
-            multiply<S::kFp8, S::kGated>(acc[i], b, a[i - kP], as[i - kP], bs);
+        for (int i = kP; i < kMT; ++i) multiply(acc[i], b, a[i - kP]);
         __builtin_amdgcn_s_setprio(0);
         if (!wm) wait_loads_before<kLoads>(stores);
         stores = 0;
@@ -1176,11 +1197,12 @@ __device__ __forceinline__ void widen_codes(const u32x4& w, bf16x8 (&v)[2]) {
 }
 
 // A step of e4m3 rows with the products summed in fp32 throughout: the codes are widened to bf16
-// for the bf16 matrix instruction. The e4m3 one keeps about 17 bits below the largest of the
-// products it adds (measured: its sums of 128 are off by 1.5e-5 of their size, the others by 1e-8),
-// which a bf16 output does not show, but the fp32 scales of act do. It takes twice the matrix
-// time and half as many conversions as products of the e4m3 one per lane; where the weights' way
-// from memory is what is waited for that costs little. Tiles of four pairs of subtiles take a
+// for the bf16 matrix instruction. The e4m3 one's sums of 128 are off by 1.5e-5 of their size,
+// these by 1e-8, and the fp32 scales of act show it. It takes twice the matrix time and the
+// conversions on top (weights of 4096 x 7168: 16 rows of each of 32 experts 160 us against 158,
+// 128 rows of each of 256 experts 2690 against 1800). Every wave converts what it reads, in
+// registers; fewer waves with more channels each, conversions between the products, and
+// conversions through fp32 and a byte permute gained nothing. Tiles of four pairs of subtiles take a
 // step in two parts, each scaled and added, to stay within the registers.
 template <class S, int kMT>
 __device__ __forceinline__ void widened_step(f32x4 (&acc)[S::kMT][4], const char* stage,
@@ -1255,7 +1277,12 @@ __device__ __forceinline__ void stream_tile(const GemmArgs& g, const Tile& t, in
         for (int i = 0; i < kMT; ++i)
             read_fragment<S::kAByRows>(a[i], stage, (2 * i + wm) * 16, at);
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) multiply<S::kFp8, S::kGated>(acc[i], b, a[i], as[i], bs);
+        for (int i = 0; i < kMT; ++i) {
+            if constexpr (S::kFp8)
+                multiply_e4m3(acc[i], b, a[i], as[i] * bs[0]);
+            else
+                multiply(acc[i], b, a[i]);
+        }
     }
     gemm_store<S, kMT>(g, t, acc, lds + S::kAmaxAt, wm, wn, lane);
 }
@@ -1326,7 +1353,8 @@ template <class S>
 int64_t most_tiles(const GemmArgs& g) {
     const int64_t nt = (g.N + S::kNTile - 1) / S::kNTile;
     if constexpr (S::kOverRows)
-        return static_cast<int64_t>(g.E) * ((g.M + S::kTileM - 1) / S::kTileM) * nt;
+        return static_cast<int64_t>(g.piece_rows > 0 ? g.pieces : g.E) *
+               ((g.M + S::kTileM - 1) / S::kTileM) * nt;
     return (g.num_rows / S::kTileM + std::min<int64_t>(g.E, g.num_rows)) * nt;
 }
 

@@ -134,6 +134,7 @@ struct GemmArgs {
     float* scales;             // their scales
     void* act;                 // down_grad: bf16 out (nullable)
     int out_fp32, accumulate;  // weight gradient
+    int piece_rows, pieces;    // weight gradient: an expert's rows in pieces of so many; 0: whole
     int32_t* error_flag;
 };
 hipError_t launch_expert_gate_up(const GemmArgs& g, bool fp8, hipStream_t stream);
@@ -141,5 +142,9 @@ hipError_t launch_expert_down(const GemmArgs& g, bool fp8, hipStream_t stream);
 hipError_t launch_expert_down_grad(const GemmArgs& g, hipStream_t stream);
 hipError_t launch_expert_gate_up_grad(const GemmArgs& g, hipStream_t stream);
 hipError_t launch_expert_weight_grad(const GemmArgs& g, hipStream_t stream);
+// 0 where the rows stay whole, and the call above serves
+size_t expert_weight_grad_workspace_bytes(int E, int64_t rows, int M, int N);
+hipError_t launch_expert_weight_grad_split(const GemmArgs& g, float* workspace,
+                                           hipStream_t stream);
 
 }  // namespace ep

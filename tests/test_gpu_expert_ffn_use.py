@@ -471,3 +471,25 @@ def test_an_empty_batch_through_the_experts():
     gg, gd = torch.ones((4, 256, 256), device="cuda"), torch.ones((4, 256, 128), device="cuda")
     train(p, d, gg, gd)
     assert not bool(gg.any()) and not bool(gd.any()) and int(p.error_flag) == 0
+
+
+def test_as_many_rows_as_32_bits_number():
+    """One expert of INT32_MAX rows of eight channels (34 GB): the first and the last ones."""
+    n, H, I, some = 2**31 - 1, 8, 8, 1000
+    print(f"\ncase: {n} rows of {H}", flush=True)
+    g = gen(29)
+    off = torch.tensor([0, n], dtype=I32, device="cuda")
+    x = torch.zeros((n, H), dtype=BF16, device="cuda")
+    for r in (slice(0, some), slice(n - some, n)):
+        x[r] = torch.randn((some, H), generator=g, device="cuda").to(BF16)
+    w, wd = weights(g, 1, 2 * I, H), weights(g, 1, H, I)
+    act, fl = torch.empty((n, I), dtype=BF16, device="cuda"), flag()
+    ep.ep_expert_gate_up(x, w, off, act=act, error_flag=fl)
+    for r in (slice(0, some), slice(n - some, n)):
+        _, _, wact, err = X.gate_up(P.f64(x[r]), P.f64(w), [0, some])
+        X.assert_within(act[r], wact, X.rounded(wact, err), "act")
+    ep.ep_expert_down(act, wd, off, expert_out=x, error_flag=fl)
+    for r in (slice(0, some), slice(n - some, n)):
+        want, mag = X.nt(P.f64(act[r]), P.f64(wd), [0, some])
+        X.assert_within(x[r], want, X.rounded(want, X.product_error(I) * mag), "expert_out")
+    assert fl.item() == 0
