@@ -16,7 +16,7 @@ from ._binding import (EP_DEVERR_RECV_OVERFLOW, EP_DEVERR_SLOT_RANGE, EP_DEVERR_
                        ep_dispatch_permute_fp8, ep_dispatch_permute_grad, ep_expert_down,
                        ep_expert_down_fp8, ep_expert_down_grad, ep_expert_gate_up,
                        ep_expert_gate_up_fp8, ep_expert_gate_up_grad, ep_expert_weight_grad,
-                       ep_rmsnorm,
+                       ep_expert_weight_grad_workspace_bytes, ep_rmsnorm,
                        ep_rmsnorm_grad, ep_rmsnorm_grad_workspace_bytes,
                        ep_combine_send, ep_dispatch, ep_dispatch_fp8, ep_dispatch_permute,
                        ep_dispatch_layout, ep_dispatch_permute_layout, ep_dispatch_preprocess, ep_dispatch_recv,
@@ -34,6 +34,7 @@ __all__ = [
     "ep_combine_unpermute_grad",
     "ep_expert_gate_up", "ep_expert_gate_up_fp8", "ep_expert_down", "ep_expert_down_fp8",
     "ep_expert_down_grad", "ep_expert_gate_up_grad", "ep_expert_weight_grad",
+    "ep_expert_weight_grad_workspace_bytes",
     "ep_get_layout", "ep_get_layout_no_alloc", "ep_dispatch_preprocess", "ep_layout_counts",
     "ep_layout_counts_workspace_bytes", "ep_dispatch_layout", "ep_dispatch_permute_layout",
     "ep_layout_dispatch",

@@ -93,6 +93,9 @@ def load() -> ctypes.CDLL:
     L.ep_expert_down_grad.argtypes = [P, P, P, i32, i64, i32, i32, P, P, P, P, P, P, P]
     L.ep_expert_gate_up_grad.argtypes = [P, P, P, i32, i64, i32, i32, P, P, P]
     L.ep_expert_weight_grad.argtypes = [P, P, P, i32, i64, i32, i32, P, i32, i32, P, P]
+    L.ep_expert_weight_grad_split.argtypes = [P, P, P, i32, i64, i32, i32, P, i32, i32, P, P, sz, P]
+    L.ep_expert_weight_grad_workspace_bytes.argtypes = [i32, i64, i32, i32]
+    L.ep_expert_weight_grad_workspace_bytes.restype = sz
     L.ep_hbm_copy.argtypes = [P, P, sz, P]
     L.ep_hbm_fan.argtypes = [P, P, sz, i32, i32, P]
     L.ep_hbm_spread.argtypes = [P, P, sz, i32, i32, P]
@@ -104,7 +107,7 @@ def load() -> ctypes.CDLL:
               "ep_dispatch_permute_fp8", "ep_combine_unpermute", "ep_combine_unpermute_grad",
               "ep_dispatch_permute_grad", "ep_expert_gate_up", "ep_expert_gate_up_fp8",
               "ep_expert_down", "ep_expert_down_fp8", "ep_expert_down_grad",
-              "ep_expert_gate_up_grad", "ep_expert_weight_grad"):
+              "ep_expert_gate_up_grad", "ep_expert_weight_grad", "ep_expert_weight_grad_split"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -159,6 +162,13 @@ def _stream(stream) -> ctypes.c_void_p:
             raise ValueError(f"stream is on {stream.device}, but the current device is cuda:{cur}")
         stream = stream.cuda_stream
     return ctypes.c_void_p(int(stream))
+
+
+def _torch_stream(stream):
+    """The torch stream of a call's `stream` argument; None for the current one."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
 def _check(status: int, where: str) -> None:
@@ -979,23 +989,41 @@ def ep_expert_gate_up_grad(grad_gate_up, w_gate_up, expert_offset, *, grad_x, er
         _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st), "ep_expert_gate_up_grad")
 
 
+def ep_expert_weight_grad_workspace_bytes(num_experts: int, num_rows: int, rows_out: int,
+                                          cols_out: int) -> int:
+    return int(load().ep_expert_weight_grad_workspace_bytes(num_experts, num_rows, rows_out,
+                                                            cols_out))
+
+
 def ep_expert_weight_grad(grad, input, expert_offset, *, grad_weight, accumulate: bool = False,
-                          error_flag=None, stream=None) -> None:
+                          workspace=None, error_flag=None, stream=None) -> None:
     """grad_weight[e] = the sum over expert e's rows of grad's row times input's row (added to it
     with accumulate). grad: bf16 [rows][M]; input: bf16 [rows][N]; grad_weight: bf16 or fp32
-    [E][M][N]. w_gate_up's is of grad_gate_up and x, w_down's of grad_expert_out and act."""
+    [E][M][N]. w_gate_up's is of grad_gate_up and x, w_down's of grad_expert_out and act.
+    workspace: uint8 of ep_expert_weight_grad_workspace_bytes(E, rows, M, N); where that is not 0
+    and none is given, one is allocated for the call, on its stream."""
     rows, M = _rows_2d(grad, "grad")
     _, N = _rows_2d(input, "input")
     E = _weights_3d(grad_weight, "grad_weight")[0]
     cur, st = _current(stream)
     dtype = _F32 if grad_weight.dtype is _F32 else _BF16
-    _check(load().ep_expert_weight_grad(
-        _row_ptr(grad, _BF16, (rows, M), "grad", cur),
-        _row_ptr(input, _BF16, (rows, N), "input", cur),
-        _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, M, N,
-        _row_ptr(grad_weight, dtype, (E, M, N), "grad_weight", cur), int(dtype is _F32),
-        int(bool(accumulate)), _row_ptr(error_flag, _I32, None, "error_flag", cur, False), st),
-        "ep_expert_weight_grad")
+    args = (_row_ptr(grad, _BF16, (rows, M), "grad", cur),
+            _row_ptr(input, _BF16, (rows, N), "input", cur),
+            _row_ptr(expert_offset, _I32, (E + 1,), "expert_offset", cur), E, rows, M, N,
+            _row_ptr(grad_weight, dtype, (E, M, N), "grad_weight", cur), int(dtype is _F32),
+            int(bool(accumulate)), _row_ptr(error_flag, _I32, None, "error_flag", cur, False))
+    lib = load()
+    if workspace is None:
+        need = lib.ep_expert_weight_grad_workspace_bytes(E, rows, M, N)
+        if need:
+            # of the stream's own memory, so that what is allocated next waits for the call
+            with torch.cuda.stream(_torch_stream(stream)):
+                workspace = torch.empty(need, dtype=_U8, device=grad.device)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws = _row_ptr(workspace, _U8, getattr(workspace, "shape", None), "workspace", cur)
+        ws_bytes = workspace.numel()
+    _check(lib.ep_expert_weight_grad_split(*args, ws, ws_bytes, st), "ep_expert_weight_grad")
 
 
 def ep_hbm_copy(src, dst, nbytes: Optional[int] = None, stream=None) -> None:

@@ -106,6 +106,20 @@ ep::GemmArgs expert_args(const void* a, const void* b, const int32_t* offset, in
     return g;
 }
 
+int weight_grad_args(const void* grad, const void* input, const int32_t* offset, int E,
+                     int64_t rows, int M, int N, void* grad_weight, int weight_is_fp32,
+                     int accumulate, int32_t* error_flag, ep::GemmArgs& g) {
+    const int st = check_expert_products(offset, E, rows, M, N, 8, error_flag);
+    if (st != EP_OK) return st;
+    if (!grad_weight || (rows > 0 && (!grad || !input))) return EP_ERR_ARG;
+    if (!aligned(grad, 16) || !aligned(input, 16) || !aligned(grad_weight, 16)) return EP_ERR_ALIGN;
+    g = expert_args(grad, input, offset, E, rows, N, 0, grad_weight, error_flag);
+    g.M = M;
+    g.out_fp32 = weight_is_fp32 != 0;
+    g.accumulate = accumulate != 0;
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -861,17 +875,38 @@ int ep_expert_weight_grad(const void* grad, const void* input, const int32_t* ex
                           int num_experts, int64_t num_rows, int rows_out, int cols_out,
                           void* grad_weight, int weight_is_fp32, int accumulate,
                           int32_t* error_flag, void* stream) {
-    const int M = rows_out, N = cols_out;
-    const int st = check_expert_products(expert_offset, num_experts, num_rows, M, N, 8, error_flag);
+    ep::GemmArgs g;
+    const int st = weight_grad_args(grad, input, expert_offset, num_experts, num_rows, rows_out,
+                                    cols_out, grad_weight, weight_is_fp32, accumulate, error_flag, g);
     if (st != EP_OK) return st;
-    if (!grad_weight || (num_rows > 0 && (!grad || !input))) return EP_ERR_ARG;
-    if (!aligned(grad, 16) || !aligned(input, 16) || !aligned(grad_weight, 16)) return EP_ERR_ALIGN;
-    ep::GemmArgs g = expert_args(grad, input, expert_offset, num_experts, num_rows, N, 0,
-                                 grad_weight, error_flag);
-    g.M = M;
-    g.out_fp32 = weight_is_fp32 != 0;
-    g.accumulate = accumulate != 0;
     return hip_status(ep::launch_expert_weight_grad(g, static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_expert_weight_grad_workspace_bytes(int num_experts, int64_t num_rows, int rows_out,
+                                             int cols_out) {
+    // an offset array that is never read stands for the one that the sizes' check asks for
+    static const int32_t offset = 0;
+    if (check_expert_products(&offset, num_experts, num_rows, rows_out, cols_out, 8, nullptr) !=
+        EP_OK)
+        return 0;
+    return ep::expert_weight_grad_workspace_bytes(num_experts, num_rows, rows_out, cols_out);
+}
+
+int ep_expert_weight_grad_split(const void* grad, const void* input, const int32_t* expert_offset,
+                                int num_experts, int64_t num_rows, int rows_out, int cols_out,
+                                void* grad_weight, int weight_is_fp32, int accumulate,
+                                int32_t* error_flag, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    ep::GemmArgs g;
+    const int st = weight_grad_args(grad, input, expert_offset, num_experts, num_rows, rows_out,
+                                    cols_out, grad_weight, weight_is_fp32, accumulate, error_flag, g);
+    if (st != EP_OK) return st;
+    if (!aligned(workspace, 16)) return EP_ERR_ALIGN;
+    const size_t need =
+        ep::expert_weight_grad_workspace_bytes(num_experts, num_rows, rows_out, cols_out);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return EP_ERR_CAPACITY;
+    return hip_status(ep::launch_expert_weight_grad_split(g, static_cast<float*>(workspace),
+                                                          static_cast<hipStream_t>(stream)));
 }
 
 int ep_hbm_copy(const void* src, void* dst, size_t bytes, void* stream) {

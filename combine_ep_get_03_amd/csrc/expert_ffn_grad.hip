@@ -5,6 +5,8 @@
 //   grad_W[e] = grad_rows^T input_rows over expert e's rows          ep_expert_weight_grad
 #include "expert_gemm.hpp"
 
+#include <algorithm>
+
 namespace ep {
 
 hipError_t launch_expert_down_grad(const GemmArgs& g, hipStream_t stream) {
@@ -23,6 +25,134 @@ hipError_t launch_expert_weight_grad(const GemmArgs& g, hipStream_t stream) {
     if (g.num_rows / g.E > 256)
         return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 256>>(g, stream);
     return launch_shape<GemmShape<GemmOp::kWeightGrad, false, 128>>(g, stream);
+}
+
+// ---------------------------------------------------------------- long sums, few tiles
+// A block sums an expert's rows for one tile of the weight, so a weight of few tiles leaves most
+// CUs idle for as long as its rows take. There the rows are cut into pieces of equal length, so
+// many that their tiles fill the chip once; every piece's sums go to the workspace in fp32 (at
+// most 64 MB), and a second launch adds each expert's in order. Measured (us on MI355X, whole /
+// in pieces of the lower tiles / of the higher ones):
+//   1 weight of 112 x 112       512 rows 14 / 13 / 14    16384 rows 256 / 20 / 21
+//   1 of 2048 x 1024 (64 low)   512 rows 23 / 25 / 30     4096 rows 93 / 35 / 43
+//   32 of 192 x 496 (128 low)   512 rows 20 / 24 / 27     1024 rows 29 / 31 / 33    4096 rows 81 / 65 / 60
+//   1 of 2048 x 2048 (128 low)  512 rows 25 / 29 / 35     1024 rows 35 / 36 / 36   16384 rows 335 / 230 / 156
+namespace {
+
+template <int kTileM>
+using WeightShape = GemmShape<GemmOp::kWeightGrad, false, kTileM>;
+
+constexpr int64_t kLeastPiece = 256;  // four steps; 128 rows are slower from 8192 rows on (18 against 16 us)
+constexpr int64_t kManyTiles = 64;    // of the lower ones
+constexpr int kManyPieces = 32;
+
+struct Pieces {
+    int rows = 0, count = 0;
+    bool high = false;
+};
+
+template <int kTileM>
+int64_t weight_tiles(int E, int M, int N) {
+    constexpr int kTileN = WeightShape<kTileM>::kNTile;
+    return static_cast<int64_t>(E) * ((M + kTileM - 1) / kTileM) * ((N + kTileN - 1) / kTileN);
+}
+
+Pieces pieces_of(int E, int64_t rows, int M, int N) {
+    Pieces p;
+    int64_t tiles = weight_tiles<128>(E, M, N);
+    if (tiles > kBlocks / 2 || rows / E < std::max<int64_t>(512, 8 * tiles)) return p;
+    p.high = tiles > kManyTiles;
+    if (p.high) tiles = weight_tiles<256>(E, M, N);
+    const int64_t left = kBlocks - tiles;  // every expert may have one piece begun
+    const int64_t each = std::max(kLeastPiece, (rows * (tiles / E) + left - 1) / left);
+    p.rows = static_cast<int>(std::min<int64_t>((each + 63) / 64 * 64, INT32_MAX / 64 * 64));
+    p.count = static_cast<int>(rows / p.rows) + E;
+    return p;
+}
+
+// Adds the pieces of a word of four channels per lane, eight loads in flight: all of them in one
+// wave, or (kWaves = 4) every fourth in each of a block's four and then their sums, which many
+// pieces are worth (64 of 112 x 112 19.5 against 26 us; 2 of 2048 x 2048 140 against 126).
+template <int kWaves>
+__global__ __launch_bounds__(256) void weight_pieces_kernel(const GemmArgs g,
+                                                            const f32x4* __restrict__ partial) {
+    constexpr int kWords = 256 / kWaves;
+    __shared__ f32x4 sums[kWaves][kWords];
+    bool bad = false;
+    for (int e = threadIdx.x; e <= g.E; e += 256)
+        bad |= g.offset[e] < (e > 0 ? g.offset[e - 1] : 0);
+    if (__syncthreads_or(bad)) return;
+    const int word = threadIdx.x % kWords, wave = threadIdx.x / kWords;
+    const int64_t per = static_cast<int64_t>(g.M) * g.N / 4;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kWords + word;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (at < per * g.E) {
+        const int e = static_cast<int>(at / per);
+        auto first = [&](int i) {
+            return first_piece(static_cast<int>(min<int64_t>(g.offset[i], g.num_rows)), i,
+                               g.piece_rows);
+        };
+        const int from = first(e) + wave, to = first(e + 1);
+        const int64_t next = kWaves * per;
+        const f32x4* p = partial + from * per + (at - e * per);
+        int left = to > from ? (to - from + kWaves - 1) / kWaves : 0;
+        for (; left >= 8; left -= 8, p += 8 * next) {
+            f32x4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = p[i * next];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += v[i];
+        }
+        for (; left > 0; --left, p += next) sum += *p;
+    }
+    if constexpr (kWaves > 1) {
+        sums[wave][word] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) sum += sums[w][word];
+    }
+    if (wave > 0 || at >= per * g.E) return;
+    if (g.out_fp32) {
+        f32x4* out = static_cast<f32x4*>(g.out) + at;
+        if (g.accumulate) sum += *out;
+        *out = sum;
+    } else {
+        u32x2* out = static_cast<u32x2*>(g.out) + at;
+        if (g.accumulate) {
+            const u32x2 old = *out;
+            sum += f32x4{bf16_lo(old[0]), bf16_hi(old[0]), bf16_lo(old[1]), bf16_hi(old[1])};
+        }
+        *out = u32x2{bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+    }
+}
+
+}  // namespace
+
+size_t expert_weight_grad_workspace_bytes(int E, int64_t rows, int M, int N) {
+    return static_cast<size_t>(pieces_of(E, rows, M, N).count) * M * N * sizeof(float);
+}
+
+hipError_t launch_expert_weight_grad_split(const GemmArgs& g, float* workspace,
+                                           hipStream_t stream) {
+    const Pieces p = pieces_of(g.E, g.num_rows, g.M, g.N);
+    if (p.count == 0) return launch_expert_weight_grad(g, stream);
+    GemmArgs part = g;
+    part.piece_rows = p.rows;
+    part.pieces = p.count;
+    GemmArgs join = part;
+    part.out = workspace;
+    part.out_fp32 = 1;
+    part.accumulate = 0;
+    const hipError_t st = p.high ? launch_shape<WeightShape<256>>(part, stream)
+                                 : launch_shape<WeightShape<128>>(part, stream);
+    if (st != hipSuccess) return st;
+    const int64_t words = static_cast<int64_t>(g.E) * g.M * g.N / 4;
+    const f32x4* sums = reinterpret_cast<const f32x4*>(workspace);
+    if (p.count / g.E >= kManyPieces)
+        weight_pieces_kernel<4><<<static_cast<unsigned>((words + 63) / 64), 256, 0, stream>>>(join, sums);
+    else
+        weight_pieces_kernel<1><<<static_cast<unsigned>((words + 255) / 256), 256, 0, stream>>>(join, sums);
+    return hipGetLastError();
 }
 
 }  // namespace ep

@@ -331,6 +331,9 @@ class ExpertPath:
                 self.gate_up = torch.empty((cap, 2 * inter), **bf16)
             if training:
                 self.grad_gate_up = torch.empty((cap, 2 * inter), **bf16)
+                ws = max(B.ep_expert_weight_grad_workspace_bytes(E, cap, 2 * inter, H),
+                         B.ep_expert_weight_grad_workspace_bytes(E, cap, H, inter))
+                self.weight_workspace = torch.empty(ws, **u8)
                 self.grad_perm_x = torch.empty((cap, H), **bf16)
 
     @property
@@ -438,11 +441,12 @@ class ExpertPath:
                               error_flag=err, stream=stream)
         if grad_w_down is not None:
             B.ep_expert_weight_grad(self.grad_expert_out, self.act, off, grad_weight=grad_w_down,
-                                    accumulate=accumulate, error_flag=err, stream=stream)
+                                    accumulate=accumulate, workspace=self.weight_workspace,
+                                    error_flag=err, stream=stream)
         if grad_w_gate_up is not None:
             B.ep_expert_weight_grad(self.grad_gate_up, self.perm_x, off,
                                     grad_weight=grad_w_gate_up, accumulate=accumulate,
-                                    error_flag=err, stream=stream)
+                                    workspace=self.weight_workspace, error_flag=err, stream=stream)
         B.ep_expert_gate_up_grad(self.grad_gate_up, w_gate_up, off, grad_x=self.grad_perm_x,
                                  error_flag=err, stream=stream)
         self._wrote(self.grad_gate_up, "experts_grad")

@@ -741,6 +741,23 @@ int ep_expert_weight_grad(const void *grad, const void *input, const int32_t *ex
                           void *grad_weight, int weight_is_fp32, int accumulate,
                           int32_t *error_flag, void *stream);
 
+/* Bytes of workspace ep_expert_weight_grad_split needs: 0 for weights large enough, or rows few
+ * enough, that it does what ep_expert_weight_grad does (and for sizes that it refuses), at most
+ * 64 MiB. */
+size_t ep_expert_weight_grad_workspace_bytes(int num_experts, int64_t num_rows, int rows_out,
+                                             int cols_out);
+
+/* ep_expert_weight_grad_split -- ep_expert_weight_grad, the same arguments, checks and outputs,
+ * where a small weight is summed over many rows: the rows are cut into pieces that are summed side
+ * by side in fp32 and then added in order, so its roundings in fp32 are others.
+ * Workspace: at least ep_expert_weight_grad_workspace_bytes of the same sizes, 16-byte aligned,
+ *   contents on entry irrelevant, clobbered (EP_ERR_CAPACITY if smaller); NULL where that is 0. */
+int ep_expert_weight_grad_split(const void *grad, const void *input, const int32_t *expert_offset,
+                                int num_experts, int64_t num_rows, int rows_out, int cols_out,
+                                void *grad_weight, int weight_is_fp32, int accumulate,
+                                int32_t *error_flag, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
 /* ep_hbm_copy -- measurement helper, not a step of the path: a plain 128-bit copy of
  * `bytes` bytes (a multiple of 16; both pointers 16-byte aligned) used as the HBM
  * copy-bandwidth yardstick and as the known-size reference for hardware byte counters.

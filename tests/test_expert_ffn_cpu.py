@@ -291,3 +291,29 @@ def test_bounds_reject_a_planted_mistake():
     X.assert_within(value, gu, X.codes_bound(gu, err, scale), "codes")
     with pytest.raises(AssertionError):
         X.assert_within(value * 1.08, gu, X.codes_bound(gu, err, scale), "codes")
+
+
+def split(lib, E=1, n=4096, M=256, N=128, out=A16, ws=A16, ws_bytes=None):
+    need = ep.ep_expert_weight_grad_workspace_bytes(E, n, M, N)
+    return lib.ep_expert_weight_grad_split(A16, A16, A16, E, n, M, N, out, 1, 0, None, ws,
+                                           need if ws_bytes is None else ws_bytes, None)
+
+
+def test_workspace_of_a_weight_gradient_in_pieces(lib):
+    size = ep.ep_expert_weight_grad_workspace_bytes
+    assert size(1, 4096, 256, 128) > 0
+    # many tiles, few rows, no rows, sizes that are refused
+    for E, n, M, N in ((32, 32768, 4096, 7168), (1, 511, 256, 128), (1, 0, 8, 8), (0, 4096, 8, 8),
+                       (1, 4096, 12, 8), (1, -1, 8, 8), (1, 2**31, 8, 8), (1, 4096, 2**22, 8)):
+        assert size(E, n, M, N) == 0, (E, n, M, N)
+    for E in (1, 3, 64, 128):
+        for n in (600, 4097, 10**6, 2**31 - 1):
+            for M, N in ((8, 8), (136, 264), (1032, 1000), (2048, 2048)):
+                one = M * N * 4  # whole pieces, one per expert at least
+                assert size(E, n, M, N) % one == 0 and size(E, n, M, N) <= 64 << 20
+                assert size(E, n, M, N) == 0 or size(E, n, M, N) >= E * one
+    assert split(lib, ws=None) == ep.EP_ERR_CAPACITY
+    assert split(lib, ws_bytes=size(1, 4096, 256, 128) - 1) == ep.EP_ERR_CAPACITY
+    assert split(lib, ws=A8) == ep.EP_ERR_ALIGN
+    assert split(lib, out=None) == ep.EP_ERR_ARG
+    assert split(lib, n=-1) == ep.EP_ERR_ARG
