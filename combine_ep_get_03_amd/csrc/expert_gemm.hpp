@@ -1139,6 +1139,13 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[S::kMT][4]) {
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
+// One block per CU, two steps of 64 KB in LDS: per step of k an output takes 1/128 of an element from
+// the L2, where a tile of 128 x 256 takes 1/85 and comes to that way's limit (about 23 TB/s). 32768
+// rows of 4096 x 7168 weights of 32 experts take 1500 to 1630 us (1180 to 1280 TFLOP/s) at the 1.55
+// GHz that the clock falls to, the matrix cores busy for .65 of the cycles; a plain library product of
+// that size 1278 us at 1.62 GHz, busy for .88. Between products the block waits for its epilogue:
+// down's gradient, with six arrays in it, takes 940 to 970 us, 780 of them products at that rate;
+// the weights' 2080 to 2250 us with 3.8 GB of fp32 stores, which take 606 us alone.
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 1) void gemm_kernel(const GemmArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[S::kLdsBytes];
@@ -1289,7 +1296,11 @@ __device__ __forceinline__ void stream_tile(const GemmArgs& g, const Tile& t, in
 
 // Most waves multiply and four load: a load that memory holds up stops none of the products, and
 // the stores of a tile wait for no load. All meet once a step: then step k has arrived, step
-// k - 1 has been read, and the loaders go on to step k + kStages - 1 in its place.
+// k - 1 has been read, and the loaders go on to step k + kStages - 1 in its place. What bounds it
+// is the weights' way from memory: 5.3 to 6.2 of the 6.2 TB/s that a copy reaches from 512 rows of
+// 256 experts down to one token of eight (1213, 435, 81 us); with more rows the e4m3 products
+// (131072 rows of 2048 x 7168 2120 to 2250 us) and the widened ones (32768 rows of 4096 x 7168
+// 2600 to 2690 us) are. A call of a few us waits for 16 to 112 steps of about .3 us.
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 1) void stream_kernel(const GemmArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[S::kLdsBytes];
@@ -1369,15 +1380,17 @@ hipError_t launch_shape(const GemmArgs& g, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Which tile, by the rows per expert that the host knows of (of 4096 x 7168 weights of 32 experts,
-// us on MI355X):
-//   32 against 128 rows     16 rows  e4m3 158 / 165    32 rows  e4m3 178 / 168, bf16 333 / 310
-//   128 against 256 rows    64 rows  bf16 314 / 324    128 rows bf16 395 / 346, 1024 rows 1720 / 1540
-// e4m3 keeps the 128 rows: their products take half the time, and the loads are what is short at
-// either height (2164 against 2310 for 131072 rows of 2048 x 7168). A call with fewer tiles
-// of 128 rows than CUs takes the low ones, and narrow ones where those are at most one per CU
-// too (one token over eight experts 81 against 96 narrow and wide; 257 tokens of 1024 over 16
-// experts 17.1 against 19.8 low and not).
+// Which tile, by the rows per expert that the host knows of (us on MI355X):
+//   32 against 128 rows (weights of 4096 x 7168, 7168 x 2048 and 4096 x 1408): 17 skewed rows of
+//     each of 128 experts, down's gradient 284 / 305; 16 rows of 256, e4m3 down 641 / 622; up to
+//     20 rows within 1% otherwise; 32 rows of 32 experts, e4m3 186 / 163, bf16 338 / 314
+//   128 against 256 rows (bf16, 4096 x 7168 weights of 32 experts): 64 rows 314 / 324, 128 rows
+//     395 / 346, 1024 rows 1720 / 1540
+// e4m3 keeps the 128 rows: the e4m3 instruction's products take half the time and the loads are
+// what is short at either height (131072 rows of 2048 x 7168 2164 against 2310); widened to bf16
+// they leave no registers for more. A call with fewer tiles of 128 rows than CUs takes the low
+// ones, and narrow ones where those are at most one per CU too (one token over eight experts 81
+// against 96 narrow and wide; 257 tokens of 1024 over 16 experts 17.1 against 19.8 low and not).
 constexpr int64_t kLowRows = 20, kMidRows = 96;
 
 template <GemmOp kOp, bool kFp8>
