@@ -52,24 +52,26 @@ __device__ __forceinline__ i32x4 scalar_buffer(const void* base, uint32_t bytes)
 // Each lane's 16 (4) bytes at base + voff + soff go to LDS at lds + 16 (4) * lane. Lanes past
 // the buffer's end write zeros. Inline so that the compiler does not order its LDS reads after
 // these writes: the kernel waits and synchronises itself, once per step. Nothing is returned in
-// registers. m0 is set in the same block as it is used.
+// registers. m0 is set in the same block as it is used. The compiler does not see the load either:
+// a scalar that the vector unit wrote (v_readfirstlane) may be read by it after five wait states,
+// which the block's first two instructions are.
 __device__ __forceinline__ void load_lds16(i32x4 buf, uint32_t lds,
                                            uint32_t voff, uint32_t soff) {
     lds = __builtin_amdgcn_readfirstlane(lds);
     soff = __builtin_amdgcn_readfirstlane(soff);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(buf), "s"(soff)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds4(i32x4 buf, uint32_t lds, uint32_t voff,
                                           uint32_t soff) {
     lds = __builtin_amdgcn_readfirstlane(lds);
     soff = __builtin_amdgcn_readfirstlane(soff);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(buf), "s"(soff)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 template <int kOutstanding>
