@@ -1211,8 +1211,12 @@ __device__ __forceinline__ void widen_codes(const u32x4& w, bf16x8 (&v)[2]) {
 // conversions on top (weights of 4096 x 7168: 16 rows of each of 32 experts 160 us against 158,
 // 128 rows of each of 256 experts 2690 against 1800). Every wave converts what it reads, in
 // registers; fewer waves with more channels each, conversions between the products, and
-// conversions through fp32 and a byte permute gained nothing. Tiles of four pairs of subtiles take a
-// step in two parts, each scaled and added, to stay within the registers.
+// conversions through fp32 and a byte permute gained nothing.
+// A step is two sums of 64 products (the words w of a fragment), each scaled and added, whatever the
+// tile's height: a row's result does not depend on how the other experts' rows cut its tile. Tiles
+// of four pairs of subtiles read one word of every fragment at a time, to stay within the registers;
+// lower ones, which have room, both. One sum of 128 in the lower ones took 1544 against 1657 us at 64
+// rows of each of 256 experts, and gave other bits than the high ones.
 template <class S, int kMT>
 __device__ __forceinline__ void widened_step(f32x4 (&acc)[S::kMT][4], const char* stage,
                                              const float* as, const float (&bs)[2], int wm, int wn,
@@ -1220,36 +1224,38 @@ __device__ __forceinline__ void widened_step(f32x4 (&acc)[S::kMT][4], const char
     constexpr int kParts = kMT > 3 ? 2 : 1, kWords = 2 / kParts;
 #pragma unroll
     for (int part = 0; part < kParts; ++part) {
-        bf16x8 a[kMT][2 * kWords];
-        auto read = [&](const char* base, int first, bf16x8* v) {
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                const int place = at.by_row ^ ((part + w) * 64);
-                bf16x8 two[2];
-                widen_codes(*reinterpret_cast<const u32x4*>(base + first * kStepBytes + place), two);
-                v[2 * w] = two[0];
-                v[2 * w + 1] = two[1];
-            }
+        bf16x8 a[kWords][kMT][2];
+        auto read = [&](const char* base, int first, int w, bf16x8 (&v)[2]) {
+            const int place = at.by_row ^ ((part + w) * 64);
+            widen_codes(*reinterpret_cast<const u32x4*>(base + first * kStepBytes + place), v);
         };
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) read(stage, (2 * i + wm) * 16, a[i]);
+        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) read(stage, (2 * i + wm) * 16, w, a[w][i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            bf16x8 b[2 * kWords];
-            read(stage + S::kMBytes, n_first<S>(j, wn), b);
-            f32x4 d[kMT];
+            f32x4 d[kWords][kMT];
 #pragma unroll
-            for (int i = 0; i < kMT; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int w = 0; w < kWords; ++w) {
+                bf16x8 b[2];
+                read(stage + S::kMBytes, n_first<S>(j, wn), w, b);
 #pragma unroll
-            for (int s = 0; s < 2 * kWords; ++s)
+                for (int i = 0; i < kMT; ++i) d[w][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < kMT; ++i)
-                    d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s], a[i][s], d[i], 0, 0, 0);
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < kMT; ++i)
+                        d[w][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s], a[w][i][s],
+                                                                          d[w][i], 0, 0, 0);
+            }
 #pragma unroll
             for (int i = 0; i < kMT; ++i) {
                 const float scale = as[i] * bs[S::kGated ? j >> 1 : 0];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[i][r], scale, acc[i][j][r]);
+                for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[w][i][r], scale, acc[i][j][r]);
             }
         }
     }

@@ -1,0 +1,61 @@
+"""The experts' products at the edges of their contract: sums that do not depend on the other
+experts' rows."""
+import pytest
+import torch
+
+import combine_ep_get_03_amd as ep
+from test_gpu_expert_ffn import BF16, I32, U8, flag, fp8_rows, fp8_weights, gen, offsets, rows_of, weights
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+# The first expert's rows beside others of the same number in all, whose tiles fill the last round
+# more or less, so that the first expert's are whole in one call and cut in two or four in the
+# other; of 128 and of 256 rows.
+BESIDE = [([128, 128, 128, 128], [128, 129, 129, 126], 4096), ([100, 156, 128, 128], [100, 154, 129, 129], 4096),
+          ([70, 186, 128, 128], [70, 130, 130, 182], 4096), ([256, 256, 256, 256], [256, 257, 257, 254], 8192),
+          ([200, 312, 256, 256], [200, 280, 272, 272], 8192)]
+
+
+@pytest.mark.parametrize("counts,others,I", BESIDE, ids=lambda v: str(v))
+def test_a_row_is_the_same_beside_other_rows(counts, others, I):
+    """Sums in an order fixed by the sizes and the expert's own rows."""
+    print(f"\ncase: {counts} {others} {I}", flush=True)
+    H, E, n, mine = 256, 4, sum(counts), counts[0]
+    assert sum(others) == n and others[0] == mine
+    g = gen(50 + mine)
+    x, dout = rows_of(g, counts, 0, 0, H), rows_of(g, counts, 0, 0, H)
+    wide, act = rows_of(g, counts, 0, 0, 2 * I), rows_of(g, counts, 0, 0, I)
+    w, wd, wb = weights(g, E, 2 * I, H), weights(g, E, H, I), weights(g, E, I, H)
+    (x8, xs), (w8, ws) = fp8_rows(g, counts, 0, 0, H), fp8_weights(g, E, 2 * I, H)
+    wd8, wds = fp8_weights(g, E, I, H)  # the second product with as many output channels
+    got = []
+    for c in (counts, others):
+        _, offset = offsets(c, 0)
+        fl = flag()
+        o = dict(act=torch.zeros((n, I), dtype=BF16), gu=torch.zeros((n, 2 * I), dtype=BF16),
+                 codes=torch.zeros((n, 2 * I), dtype=U8), scales=torch.zeros((n, 2 * I // 128)),
+                 act8=torch.zeros((n, I), dtype=U8), act8s=torch.zeros((n, I // 128)),
+                 down=torch.zeros((n, I), dtype=BF16), down8=torch.zeros((n, I), dtype=BF16),
+                 dgu=torch.zeros((n, 2 * I), dtype=BF16), dx=torch.zeros((n, I), dtype=BF16))
+        o = {k: v.cuda() for k, v in o.items()}
+        ep.ep_expert_gate_up(x, w, offset, act=o["act"], gate_up=o["gu"], gate_up_fp8=o["codes"],
+                             gate_up_scales=o["scales"], error_flag=fl)
+        ep.ep_expert_gate_up_fp8(x8, xs, w8, ws, offset, act_fp8=o["act8"], act_scales=o["act8s"],
+                                 error_flag=fl)
+        ep.ep_expert_down(x, wb, offset, expert_out=o["down"], error_flag=fl)
+        ep.ep_expert_down_fp8(x8, xs, wd8, wds, offset, expert_out=o["down8"], error_flag=fl)
+        ep.ep_expert_down_grad(dout, wd, offset, grad_gate_up=o["dgu"], gate_up=wide, error_flag=fl)
+        ep.ep_expert_gate_up_grad(x, w[:, :H].contiguous().view(E, H, H).repeat(1, 1, I // H), offset,
+                                  grad_x=o["dx"], error_flag=fl)
+        assert fl.item() == 0
+        got.append(o)
+    for name in got[0]:
+        a, b = (o[name][:mine] for o in got)
+        assert bool(a.any()), name
+        same = torch.equal(bits(a), bits(b))
+        assert same, name
