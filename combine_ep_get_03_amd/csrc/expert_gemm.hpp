@@ -743,7 +743,9 @@ __device__ __forceinline__ float group_amax(float a) {
 // What a tile's sums become in memory. Lane: row (2 i + wm) 16 + l % 16 of the tile, eight
 // channels of each pair of subtiles. The tile's rows of an array are a buffer, so that rows past
 // its height are dropped (or read as zeros) without a branch, and every tile of mt pairs of
-// subtiles makes the same number of stores.
+// subtiles makes the same number of stores. What moves an access within a row is in its vector
+// offset: a scalar offset is taken off the buffer's size before the comparison, and a piece that
+// got no row has a buffer of none.
 template <class S, int kMT>
 __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32x4 (&acc)[S::kMT][4],
                                            char* lds_amax, int wm, int wn, int lane) {
@@ -811,7 +813,8 @@ __device__ __forceinline__ void gemm_store(const GemmArgs& g, const Tile& t, f32
                 const uint32_t at = in ? m * (I * (S::kFp8 ? 1u : 2u)) + c : kOutOfBuffer;
                 __builtin_amdgcn_raw_buffer_store_b64(e4m3_eight(gate, inv[0]), code_rows, at, 0, 0);
                 if constexpr (!S::kFp8)
-                    __builtin_amdgcn_raw_buffer_store_b64(e4m3_eight(up, inv[1]), code_rows, at, I, 0);
+                    __builtin_amdgcn_raw_buffer_store_b64(e4m3_eight(up, inv[1]), code_rows,
+                                                          in ? at + I : at, 0, 0);
             }
             if constexpr (!S::kFp8) {
                 if (g.gate_up) {

@@ -1,10 +1,13 @@
 """The experts' products at the edges of their contract: sums that do not depend on the other
-experts' rows."""
+experts' rows; pieces of tiles that get no row."""
 import pytest
 import torch
 
 import combine_ep_get_03_amd as ep
-from test_gpu_expert_ffn import BF16, I32, U8, flag, fp8_rows, fp8_weights, gen, offsets, rows_of, weights
+import plain_experts as X
+import plain_ops as P
+from test_gpu_expert_ffn import (BF16, I32, U8, check, check_codes, finite, flag, fp8_rows, fp8_weights, gen,
+                                 offsets, rows_of, sentinel, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +62,27 @@ def test_a_row_is_the_same_beside_other_rows(counts, others, I):
         assert bool(a.any()), name
         same = torch.equal(bits(a), bits(b))
         assert same, name
+
+
+# One row of the last expert, in tiles that are cut in two or four because the last round has room:
+# the pieces behind the first get no row, and would begin in the rows of no expert. Of the lowest,
+# the middle and the highest tiles.
+ONE_ROW = [([30, 0, 0, 1], 49, 4096), ([70, 0, 0, 1], 310, 4736), ([200, 1], 399, 8192), ([200, 1], 1399, 4096)]
+
+
+@pytest.mark.parametrize("counts,tail,I", ONE_ROW, ids=lambda v: str(v))
+def test_a_piece_without_rows_writes_nothing(counts, tail, I):
+    print(f"\ncase: {counts} {tail} {I}", flush=True)
+    g, H = gen(60 + I), 64
+    off, offset = offsets(counts, 0)
+    x, w = rows_of(g, counts, 0, tail, H), weights(g, len(counts), 2 * I, H)
+    n, hi, fl = x.shape[0], off[-1], flag()
+    act, gu = sentinel(n, I), sentinel(n, 2 * I)
+    c = torch.full((n, 2 * I), 0x5A, dtype=U8, device="cuda")
+    s = torch.full((n, 2 * I // 128), -3.0, device="cuda")
+    ep.ep_expert_gate_up(x, w, offset, act=act, gate_up=gu, gate_up_fp8=c, gate_up_scales=s, error_flag=fl)
+    want, err, wact, act_err = X.gate_up(finite(x, 0, hi), P.f64(w), off)
+    check(act, wact, X.rounded(wact, act_err), 0, hi, "act")
+    check(gu, want, X.rounded(want, err), 0, hi, "gate_up")
+    check_codes(c, s, want, err, 0, hi, "gate_up")
+    assert fl.item() == 0
