@@ -316,7 +316,7 @@ class ExpertPath:
             ws = max(16, B.ep_rmsnorm_grad_workspace_bytes(T, H))
             self.norm_workspace = torch.empty(ws, **u8)
         self.gate_up = self.gate_up_fp8 = self.gate_up_scales = None
-        self._kept = False  # experts() has kept gate and up
+        self._kept = False  # experts() has kept gate and up of dispatch()'s batch
         if inter is not None:
             self.expert_out = torch.empty((cap, H), **bf16)
             if fp8:
@@ -365,6 +365,7 @@ class ExpertPath:
     def dispatch(self, topk_idx, stream=None) -> None:
         """The layout of the batch and the norm's rows in expert-major order."""
         lb = self.layout_buf
+        self._kept = False  # gate and up of the batch before do not go with the new offsets
         lb.compute(topk_idx, self.E, self.R, self.N, stream=stream)
         if self.fp8:
             B.ep_dispatch_permute_fp8(self.y_fp8, self.y_scales, None, lb.expert_slot,
@@ -432,7 +433,7 @@ class ExpertPath:
         self._needs_training()
         self._needs_inter()
         if not self._kept:
-            raise ValueError("experts_grad needs experts() first")
+            raise ValueError("experts_grad needs experts() first, of the batch that dispatch() took last")
         off, err = self.expert_offset, self.error_flag
         again = self.checkpoint == "fp8"
         B.ep_expert_down_grad(self.grad_expert_out, w_down, off, grad_gate_up=self.grad_gate_up,
