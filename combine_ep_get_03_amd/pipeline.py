@@ -262,9 +262,10 @@ class ExpertPath:
         norm_grad(weight, grad_residual_out)              grad_x, grad_weight
 
     What experts() keeps of gate and up for experts_grad() is bf16, or with checkpoint="fp8" e4m3
-    in half the bytes, of which experts_grad() makes act again as well: paths of several layers
-    may then share one act (p.act = q.act). The experts' gradients need bf16 rows: inter and
-    training=True do not go with fp8=True.
+    in half the bytes, of which experts_grad() makes act again as well: paths of several layers,
+    all of them with checkpoint="fp8", may then share one act (p.act = q.act). The experts'
+    gradients need bf16 rows: inter and training=True do not go with fp8=True. dispatch() ends what
+    was kept of the batch before.
 
     The gate weights are applied once, by combine(), so their gradient is combine_grad()'s.
     y feeds more than the dispatch: the router that the gate weights come from, and a shared
@@ -323,7 +324,7 @@ class ExpertPath:
                 self.act_fp8 = torch.empty((cap, inter), **u8)
                 self.act_scales = torch.empty((cap, inter // 128), **f32)
             else:
-                self.act = torch.empty((cap, inter), **bf16)
+                self._act = torch.empty((cap, inter), **bf16)
             if training and checkpoint == "fp8":
                 self.gate_up_fp8 = torch.empty((cap, 2 * inter), **u8)
                 self.gate_up_scales = torch.empty((cap, 2 * inter // 128), **f32)
@@ -343,6 +344,17 @@ class ExpertPath:
     @property
     def expert_offset(self) -> torch.Tensor:
         return self.layout_buf.expert_offset
+
+    @property
+    def act(self) -> torch.Tensor:
+        return self._act
+
+    @act.setter
+    def act(self, buffer: torch.Tensor) -> None:
+        if self.training and self.checkpoint == "bf16":
+            raise ValueError("act: with checkpoint='bf16' it is kept for experts_grad(), and cannot "
+                             "be a buffer that other calls write")
+        self._act = buffer
 
     def norm(self, x, weight, residual=None, stream=None) -> None:
         with_sum = residual is not None

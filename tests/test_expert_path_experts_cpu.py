@@ -49,3 +49,20 @@ def test_what_another_batch_has_kept_is_not_used(seen, checkpoint):
         with pytest.raises(ValueError, match="experts\\(\\) first"):
             p.experts_grad(*W)
         assert len(seen) == before
+
+
+def test_act_is_shared_only_where_it_is_made_again(seen):
+    """With checkpoint="fp8" the backward makes act again, and without training nothing reads it
+    later; with checkpoint="bf16" it is what w_down's gradient is taken of."""
+    for kw in (dict(checkpoint="fp8"), dict(training=False), dict(training=False, checkpoint="fp8")):
+        p, q = path(**kw), path(**kw)
+        p.act = q.act
+        assert p.act is q.act
+        step(p) if p.training else p.experts(*W)
+    p, q = path(), path()
+    mine = p.act
+    with pytest.raises(ValueError, match="act"):
+        p.act = q.act
+    assert p.act is mine and p.act.shape == (T * K, I)
+    step(p)
+    p.experts_grad(*W)
