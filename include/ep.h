@@ -659,6 +659,8 @@ int ep_dispatch_permute_grad(const void *grad_perm_x, const float *grad_perm_wei
  *                  the last expert's are neither read nor written. Rows >= num_rows are
  *                  skipped and set EP_DEVERR_SLOT_RANGE; offsets that are negative or descend
  *                  set it too, and nothing is computed.
+ *                  With num_rows 0 only the weights' gradients, which write their zeros, launch
+ *                  anything and read the offsets; the other calls leave the flag as it is.
  *   hidden H, inter I: 1 .. EP_EXPERT_MAX_WIDTH, multiples of 8 (of 128 where e4m3 is read or
  *                  written; else EP_ERR_ALIGN). 1 <= num_experts E <= EP_MAX_EXPERTS,
  *                  0 <= num_rows <= INT32_MAX, and (num_rows / 32 + 1) * (max(H, 2 I) / 128 + 1)

@@ -1,5 +1,5 @@
 """The experts' products at the edges of their contract: sums that do not depend on the other
-experts' rows; pieces of tiles that get no row."""
+experts' rows; pieces of tiles that get no row; arrays of no rows."""
 import pytest
 import torch
 
@@ -86,3 +86,30 @@ def test_a_piece_without_rows_writes_nothing(counts, tail, I):
     check(gu, want, X.rounded(want, err), 0, hi, "gate_up")
     check_codes(c, s, want, err, 0, hi, "gate_up")
     assert fl.item() == 0
+
+
+@pytest.mark.parametrize("off,sets", [([0, 0, 0], False), ([0, 5, 9], True), ([0, 3, 1], True),
+                                      ([-1, 0, 0], True)], ids=str)
+def test_arrays_of_no_rows(off, sets):
+    """Nothing to compute: the row-wise calls launch nothing and leave the flag, whatever the
+    offsets; the weights' gradients write their zeros and look at them."""
+    E, H, I = 2, 128, 128
+    offset = torch.tensor(off, dtype=I32, device="cuda")
+    b = lambda *s: torch.empty(s, dtype=BF16, device="cuda")
+    u = lambda *s: torch.empty(s, dtype=U8, device="cuda")
+    f = lambda *s: torch.ones(s, device="cuda")
+    fl = flag()
+    ep.ep_expert_gate_up(b(0, H), b(E, 2 * I, H), offset, act=b(0, I), gate_up=b(0, 2 * I), error_flag=fl)
+    ep.ep_expert_gate_up_fp8(u(0, H), f(0, 1), u(E, 2 * I, H), f(E, 2, 1), offset, act_fp8=u(0, I),
+                             act_scales=f(0, 1), error_flag=fl)
+    ep.ep_expert_down(b(0, I), b(E, H, I), offset, expert_out=b(0, H), error_flag=fl)
+    ep.ep_expert_down_fp8(u(0, I), f(0, 1), u(E, H, I), f(E, 1, 1), offset, expert_out=b(0, H), error_flag=fl)
+    ep.ep_expert_down_grad(b(0, H), b(E, H, I), offset, grad_gate_up=b(0, 2 * I), gate_up=b(0, 2 * I),
+                           act=b(0, I), error_flag=fl)
+    ep.ep_expert_gate_up_grad(b(0, 2 * I), b(E, 2 * I, H), offset, grad_x=b(0, H), error_flag=fl)
+    assert fl.item() == 0
+    dw = f(E, H, I)
+    ep.ep_expert_weight_grad(b(0, H), b(0, I), offset, grad_weight=dw, error_flag=fl)
+    assert (fl.item() == ep.EP_DEVERR_SLOT_RANGE) == sets
+    ascending = off[0] >= 0 and all(x <= y for x, y in zip(off, off[1:]))
+    assert bool((dw == (0.0 if ascending else 1.0)).all())
