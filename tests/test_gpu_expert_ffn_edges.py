@@ -1,5 +1,6 @@
 """The experts' products at the edges of their contract: sums that do not depend on the other
-experts' rows; pieces of tiles that get no row; arrays of no rows."""
+experts' rows; pieces of tiles that get no row; arrays of no rows;
+sums whose largest products cancel."""
 import pytest
 import torch
 
@@ -113,3 +114,47 @@ def test_arrays_of_no_rows(off, sets):
     assert (fl.item() == ep.EP_DEVERR_SLOT_RANGE) == sets
     ascending = off[0] >= 0 and all(x <= y for x, y in zip(off, off[1:]))
     assert bool((dw == (0.0 if ascending else 1.0)).all())
+
+
+# A block's largest products, of +448^2 and -448^2, cancel beside others of these sizes; or one
+# product of 2^16 stands beside 127 that lie just below 14 bits under it.
+CANCEL = [400.0, 100.0, 10.0, 1.0, 0.1, "beside"]
+
+
+def cancelling(g, size, n, N, K):
+    """Codes of n rows and N channels of the weights."""
+    if size == "beside":
+        a, b = torch.full((n, K), 1.875, device="cuda"), torch.full((1, N, K), 1.875, device="cuda")
+        at = torch.randint(0, 128, (K // 128,), generator=g, device="cuda")
+        for block, place in enumerate(at.tolist()):
+            a[:, 128 * block + place] = 256
+            b[:, :, 128 * block + place] = 256
+    else:
+        a = (torch.randn((n, K), generator=g, device="cuda") * size).clamp(-448, 448)
+        b = (torch.randn((1, N, K), generator=g, device="cuda") * size).clamp(-448, 448)
+        a[:, ::128], a[:, 64::128], b[:, :, ::128], b[:, :, 64::128] = 448, 448, 448, -448
+    return (t.to(torch.float8_e4m3fn).view(U8) for t in (a, b))
+
+
+@pytest.mark.parametrize("n,N,K", [(40, 256, 128), (300, 16384, 512)])
+@pytest.mark.parametrize("size", CANCEL)
+def test_sums_whose_largest_products_cancel(size, n, N, K):
+    """ep_expert_down_fp8 within 2^-11 of its products' magnitudes, ep_expert_gate_up_fp8 within what
+    sums in fp32 keep; scales 1 and 2^-16, so that the activation does not overflow."""
+    print(f"\ncase: {size} {n} {N} {K}", flush=True)
+    g = gen(70 + K)
+    a, b = cancelling(g, size, n, N, K)
+    offset, fl = torch.tensor([0, n], dtype=I32, device="cuda"), flag()
+    s, ws = torch.ones((n, K // 128), device="cuda"), torch.ones((1, N // 128, K // 128), device="cuda")
+    out = sentinel(n, N)
+    ep.ep_expert_down_fp8(a, s, b, ws, offset, expert_out=out, error_flag=fl)
+    want, mag = X.nt(X.fp8_rows(a, s), X.fp8_weights(b, ws), [0, n])
+    # 7 of 8 products lose at most 2^-14 of the largest, less than 2^-11; the blocks' sums in fp32
+    X.assert_within(out, want, X.rounded(want, (2.0**-11 + (K / 128 + 4) * 2.0**-23) * mag), "expert_out")
+    ws = ws * 2.0**-16
+    c = torch.full((n, N // 2), 0x5A, dtype=U8, device="cuda")
+    cs = torch.full((n, N // 256), -3.0, device="cuda")
+    ep.ep_expert_gate_up_fp8(a, s, b, ws, offset, act_fp8=c, act_scales=cs, error_flag=fl)
+    _, _, act, err = X.gate_up(X.fp8_rows(a, s), X.fp8_weights(b, ws), [0, n], fp8=True)
+    check_codes(c, cs, act, err, 0, n, "act")
+    assert fl.item() == 0
