@@ -31,19 +31,29 @@ hipError_t launch_expert_weight_grad(const GemmArgs& g, hipStream_t stream) {
 // A block sums an expert's rows for one tile of the weight, so a weight of few tiles leaves most
 // CUs idle for as long as its rows take. There the rows are cut into pieces of equal length, so
 // many that their tiles fill the chip once; every piece's sums go to the workspace in fp32 (at
-// most 64 MB), and a second launch adds each expert's in order. Measured (us on MI355X, whole /
-// in pieces of the lower tiles / of the higher ones):
-//   1 weight of 112 x 112       512 rows 14 / 13 / 14    16384 rows 256 / 20 / 21
-//   1 of 2048 x 1024 (64 low)   512 rows 23 / 25 / 30     4096 rows 93 / 35 / 43
-//   32 of 192 x 496 (128 low)   512 rows 20 / 24 / 27     1024 rows 29 / 31 / 33    4096 rows 81 / 65 / 60
-//   1 of 2048 x 2048 (128 low)  512 rows 25 / 29 / 35     1024 rows 35 / 36 / 36   16384 rows 335 / 230 / 156
+// most 64 MB), and a second launch adds each expert's in order. It pays from 512 rows per expert on,
+// and from ten times as many as there are tiles: they share the CUs, and their sums are written
+// and read once more. Measured (us on MI355X, whole / in pieces of the lower tiles / of the higher):
+//   1 of 112 x 112 (1 tile)       384 rows 12 / 13 / 14    512 rows 15 / 13 / 15    4096 rows 70 / 15 / 16
+//   1 of 2048 x 1024 (64)         512 rows 24 / 25 / 30    640 rows 27 / 26 / 31    4096 rows 98 / 35 / 43
+//   1 of 1536 x 1792 (84)         1024 rows 36 / 28 / 36   4096 rows 98 / 47 / 51   8192 rows 181 / 74 / 70
+//   3 of 1032 x 1000 (108)        1408 rows 41 / 33 / 36   2048 rows 53 / 44 / 41   8192 rows 176 / 110 / 83
+//   32 of 192 x 496 (128)         1024 rows 29 / 31 / 33   1280 rows 33 / 34 / 36   4096 rows 84 / 65 / 61
+//   1 of 2048 x 2048 (128)        1024 rows 35 / 36 / 37   1280 rows 40 / 40 / 38   16384 rows 335 / 230 / 156
+// The higher tiles, half as many, leave room for more pieces; that is worth their longer steps and
+// larger sums where the lower ones nearly fill the chip, or rows are very many. A weight of no more
+// than 128 channels along m has as few tiles of either height: there the whole rows are as quick in
+// the higher ones, and pieces (of the lower) pay only for what they save, against their bytes:
+//   96 of 128 x 256 (96)          1024 rows 26 / 32 / 33   2048 rows 42 / 44 / 45   4096 rows 82 / 78 / 80
+//   101 of 24 x 40 (101)          1024 rows 18 / 14 / 18   4096 rows 55 / 25 / 43
 namespace {
 
 template <int kTileM>
 using WeightShape = GemmShape<GemmOp::kWeightGrad, false, kTileM>;
 
 constexpr int64_t kLeastPiece = 256;  // four steps; 128 rows are slower from 8192 rows on (18 against 16 us)
-constexpr int64_t kManyTiles = 64;    // of the lower ones
+constexpr int64_t kRowsPerTile = 10;
+constexpr int64_t kBytesPerRow = 12500;  // of pieces per row of an expert, at M <= 128
 constexpr int kManyPieces = 32;
 
 struct Pieces {
@@ -60,13 +70,14 @@ int64_t weight_tiles(int E, int M, int N) {
 Pieces pieces_of(int E, int64_t rows, int M, int N) {
     Pieces p;
     int64_t tiles = weight_tiles<128>(E, M, N);
-    if (tiles > kBlocks / 2 || rows / E < std::max<int64_t>(512, 8 * tiles)) return p;
-    p.high = tiles > kManyTiles;
+    if (tiles > kBlocks / 2 || rows / E < std::max<int64_t>(512, kRowsPerTile * tiles)) return p;
+    p.high = M > 128 && tiles > 64 && rows / E >= (tiles > 96 ? 2048 : 8192);
     if (p.high) tiles = weight_tiles<256>(E, M, N);
     const int64_t left = kBlocks - tiles;  // every expert may have one piece begun
     const int64_t each = std::max(kLeastPiece, (rows * (tiles / E) + left - 1) / left);
     p.rows = static_cast<int>(std::min<int64_t>((each + 63) / 64 * 64, INT32_MAX / 64 * 64));
     p.count = static_cast<int>(rows / p.rows) + E;
+    if (M <= 128 && rows / E < static_cast<int64_t>(p.count) * M * N * 4 / kBytesPerRow) return Pieces{};
     return p;
 }
 
