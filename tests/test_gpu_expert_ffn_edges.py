@@ -21,15 +21,18 @@ def bits(t):
 # more or less, so that the first expert's are whole in one call and cut in two or four in the
 # other; of 128 and of 256 rows.
 BESIDE = [([128, 128, 128, 128], [128, 129, 129, 126], 4096), ([100, 156, 128, 128], [100, 154, 129, 129], 4096),
-          ([70, 186, 128, 128], [70, 130, 130, 182], 4096), ([256, 256, 256, 256], [256, 257, 257, 254], 8192),
-          ([200, 312, 256, 256], [200, 280, 272, 272], 8192)]
+          ([70, 186, 128, 128], [70, 130, 130, 182], 4096), ([256, 256, 256, 256], [256, 257, 257, 254], 4096),
+          ([200, 256, 256, 256, 0], [200, 257, 257, 254, 0], 4096),
+          ([128, 128, 128, 128], [128, 129, 129, 126], 8192),
+          ([256, 256, 256, 256], [256, 257, 257, 254], 8192),
+          ([200, 256, 256, 256, 0], [200, 257, 257, 254, 0], 8192)]
 
 
 @pytest.mark.parametrize("counts,others,I", BESIDE, ids=lambda v: str(v))
 def test_a_row_is_the_same_beside_other_rows(counts, others, I):
     """Sums in an order fixed by the sizes and the expert's own rows."""
     print(f"\ncase: {counts} {others} {I}", flush=True)
-    H, E, n, mine = 256, 4, sum(counts), counts[0]
+    H, E, n, mine = 256, len(counts), sum(counts), counts[0]
     assert sum(others) == n and others[0] == mine
     g = gen(50 + mine)
     x, dout = rows_of(g, counts, 0, 0, H), rows_of(g, counts, 0, 0, H)
@@ -68,7 +71,7 @@ def test_a_row_is_the_same_beside_other_rows(counts, others, I):
 # One row of the last expert, in tiles that are cut in two or four because the last round has room:
 # the pieces behind the first get no row, and would begin in the rows of no expert. Of the lowest,
 # the middle and the highest tiles.
-ONE_ROW = [([30, 0, 0, 1], 49, 4096), ([70, 0, 0, 1], 310, 4736), ([200, 1], 399, 8192), ([200, 1], 1399, 4096)]
+ONE_ROW = [([30, 0, 0, 1], 49, 4096), ([70, 0, 0, 1], 310, 5504), ([200, 1], 399, 8192), ([200, 1], 1399, 4096)]
 
 
 @pytest.mark.parametrize("counts,tail,I", ONE_ROW, ids=lambda v: str(v))
@@ -136,7 +139,7 @@ def cancelling(g, size, n, N, K):
     return (t.to(torch.float8_e4m3fn).view(U8) for t in (a, b))
 
 
-@pytest.mark.parametrize("n,N,K", [(40, 256, 128), (300, 16384, 512)])
+@pytest.mark.parametrize("n,N,K", [(40, 256, 128), (600, 16384, 512)])
 @pytest.mark.parametrize("size", CANCEL)
 def test_sums_whose_largest_products_cancel(size, n, N, K):
     """ep_expert_down_fp8 within 2^-11 of its products' magnitudes, ep_expert_gate_up_fp8 within what
@@ -157,4 +160,43 @@ def test_sums_whose_largest_products_cancel(size, n, N, K):
     ep.ep_expert_gate_up_fp8(a, s, b, ws, offset, act_fp8=c, act_scales=cs, error_flag=fl)
     _, _, act, err = X.gate_up(X.fp8_rows(a, s), X.fp8_weights(b, ws), [0, n], fp8=True)
     check_codes(c, cs, act, err, 0, n, "act")
+    assert fl.item() == 0
+
+
+# Gate and up kept in e4m3, and the gradient written over gate_up, in each of the three tiles (rows
+# per expert and outputs decide): 32, 128 and 256 rows; a last expert of one row, rows of no expert.
+KEPT = [([5, 0, 17, 1], 3, 2, 72, 384), ([70, 0, 60, 1], 1, 130, 40, 11008), ([200, 140, 1], 2, 130, 72, 11008),
+        ([300, 257, 0, 129, 1], 3, 30, 40, 8192)]
+
+
+@pytest.mark.parametrize("counts,lead,tail,H,I", KEPT, ids=lambda v: str(v))
+def test_down_gradient_of_every_kept_form_in_every_tile(counts, lead, tail, H, I):
+    print(f"\ncase: {counts} {H} {I}", flush=True)
+    g = gen(80 + I)
+    off, offset = offsets(counts, lead)
+    lo, hi = off[0], off[-1]
+    wd, dout = weights(g, len(counts), H, I), rows_of(g, counts, lead, tail, H)
+    n, fl = dout.shape[0], flag()
+    kept = rows_of(g, counts, lead, tail, 2 * I, 3.0)
+    c, s = fp8_rows(g, counts, lead, tail, 2 * I)
+    values = torch.zeros((n, 2 * I), dtype=torch.float64)
+    values[lo:hi] = X.fp8_rows(c[lo:hi], s[lo:hi])
+    for form, gu, kw in (("fp8", values, dict(gate_up_fp8=c, gate_up_scales=s)),
+                         ("bf16", finite(kept, lo, hi), dict(gate_up=kept))):
+        grad, bound, again, again_bound = X.down_grad(finite(dout, lo, hi), P.f64(wd), gu, off)
+        outs = []
+        for made in (True, False):  # act again, or not
+            dgu, act = sentinel(n, 2 * I), sentinel(n, I) if made else None
+            ep.ep_expert_down_grad(dout, wd, offset, grad_gate_up=dgu, act=act, error_flag=fl, **kw)
+            check(dgu, grad, bound, lo, hi, f"grad_gate_up, {form}")
+            if made:
+                check(act, again, again_bound, lo, hi, f"act again, {form}")
+            outs.append(dgu)
+        same = torch.equal(bits(outs[0]), bits(outs[1]))
+        assert same, form
+    act = sentinel(n, I)
+    ep.ep_expert_down_grad(dout, wd, offset, grad_gate_up=kept, gate_up=kept, act=act, error_flag=fl)
+    same = torch.equal(bits(kept), bits(outs[0]))  # in place: the same bits as beside it
+    assert same
+    check(act, again, again_bound, lo, hi, "act again, in place")
     assert fl.item() == 0
