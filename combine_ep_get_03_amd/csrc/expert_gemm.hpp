@@ -22,7 +22,10 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kBlocks = 256;        // one per CU; a power of two
 constexpr int kStepBytes = 128;     // bytes of k per row and step: 64 bf16 or 128 e4m3
 constexpr int kScaleSlots = 4;      // steps whose row scales are in LDS
-constexpr int kTableExperts = 1024; // with at most so many experts, their offsets are kept in LDS
+// With at most so many experts, their offsets are kept in LDS; with more, a tile is looked up in memory
+// (128 rows of each of 1024 / 1032 experts of 1024 x 512 weights: gate_up 558 / 579 us, e4m3 down 195 /
+// 219, weight's gradient 1172 / 1286).
+constexpr int kTableExperts = 1024;
 constexpr int kRingBytes = 8 * 32;   // the next eight tiles
 constexpr int kTableBytes = (kTableExperts + 32) * 4 + kRingBytes;
 constexpr uint32_t kOutOfBuffer = 0x80000000u;  // an offset past every buffer made here
@@ -1313,8 +1316,8 @@ __device__ __forceinline__ void stream_tile(const GemmArgs& g, const Tile& t, in
 // k - 1 has been read, and the loaders go on to step k + kStages - 1 in its place. What bounds it
 // is the weights' way from memory: 5.3 to 6.2 of the 6.2 TB/s that a copy reaches from 512 rows of
 // 256 experts down to one token of eight (1213, 435, 81 us); with more rows the e4m3 products
-// (131072 rows of 2048 x 7168 2120 to 2250 us) and the widened ones (32768 rows of 4096 x 7168
-// 2600 to 2690 us) are. A call of a few us waits for 16 to 112 steps of about .3 us.
+// (131072 rows of 2048 x 7168 2120 to 2270 us) and the widened ones (32768 rows of 4096 x 7168
+// 2690 to 2890 us) are. A call of a few us waits for 16 to 112 steps of about .3 us.
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 1) void stream_kernel(const GemmArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[S::kLdsBytes];
