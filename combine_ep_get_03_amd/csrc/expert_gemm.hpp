@@ -1215,17 +1215,18 @@ __device__ __forceinline__ void widen_codes(const u32x4& w, bf16x8 (&v)[2]) {
 }
 
 // A step of e4m3 rows with the products summed in fp32 throughout: the codes are widened to bf16
-// for the bf16 matrix instruction. With normally distributed codes the e4m3 one's sums of 128 are off
-// by 1.5e-5 of their size, these by 1e-8, and the fp32 scales of act show it. It takes twice the matrix time and the
-// conversions on top (weights of 4096 x 7168: 16 rows of each of 32 experts 160 us against 158,
-// 128 rows of each of 256 experts 2750 to 2890 against 1800). Every wave converts what it reads, in
-// registers; fewer waves with more channels each, conversions between the products, and
-// conversions through fp32 and a byte permute gained nothing.
-// A step is two sums of 64 products (the words w of a fragment), each scaled and added, whatever the
-// tile's height: a row's result does not depend on how the other experts' rows cut its tile. Tiles
-// of four pairs of subtiles read one word of every fragment at a time, to stay within the registers;
-// lower ones, which have room, both. One sum of 128 in the lower ones took 1544 against 1657 us at 64
-// rows of each of 256 experts, and gave other bits than the high ones.
+// for the bf16 matrix instruction. With normally distributed codes the e4m3 one's sums of 128 are
+// off by 1.5e-5 of their size, these by 1e-8, and the fp32 scales of act show it. It takes twice
+// the matrix time and the conversions on top, each as long as three other vector operations
+// (weights of 4096 x 7168: 16 rows of each of 32 experts 160 us against 158, 128 rows of each of
+// 256 experts 2690 to 2890 against 1800). Every wave converts what it reads, in registers; fewer
+// waves with more channels each, conversions between the products, and conversions through fp32
+// and a byte permute gained nothing.
+// A step is two sums of 64 products (the words w of a fragment), each scaled and added, whatever
+// the tile's height: a row's result does not depend on how the other experts' rows cut its tile.
+// Tiles of four pairs of subtiles read one word of every fragment at a time, to stay within the
+// registers; lower ones, which have room, both. One sum of 128 in the lower ones took 1544 against
+// 1587 to 1657 us at 64 rows of each of 256 experts, and gave other bits than the high ones.
 template <class S, int kMT>
 __device__ __forceinline__ void widened_step(f32x4 (&acc)[S::kMT][4], const char* stage,
                                              const float* as, const float (&bs)[2], int wm, int wn,
